@@ -91,6 +91,8 @@ typedef enum {
 #define KV4_DEVERR_WORKSPACE 16u /* the batch needs more work items than the workspace holds
                                     (the call then writes zero outputs, lse = -inf) */
 #define KV4_DEVERR_TIMEOUT 32u   /* a bounded wait for an async copy gave up */
+#define KV4_DEVERR_KEEP 64u      /* kv4_evict_compact: a kept position out of range, out of order,
+                                    or a recent window that was not kept whole */
 
 #define KV4_MAX_PROTECTED 144
 
@@ -360,6 +362,131 @@ kv4_status kv4_baseline_decode_attention(kv4_baseline_format fmt, const kv4_conf
                                          const void *q, void *out, float *out_f32, float *lse,
                                          void *workspace, size_t ws_bytes, int32_t *err_flag,
                                          kv4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The 8-bit block-scaled cache: INT8 or e4m3 codes with one scale for each block of 16
+ * positions and kv head (a page's block), next to the per-token scales of KV8. (No passage
+ * of the pages defines it.) No protected set: cfg's num_sinks and num_recent are ignored
+ * (taken as 0), and so are chunk_pages, demotion and prefix_mode; the batch's sink_idx,
+ * ring_idx and plan_reuse are unused.
+ *
+ * Storage, in a kv4_paged_pool, per (page, kv head) block:
+ *   k, v: one byte per element [num_pages][Hkv][8 strips][16 slots][16]; element (slot t,
+ *         dim d) at [d/16][t][d%16]; two's complement INT8, or e4m3 (1 sign, 4 exponent,
+ *         3 mantissa bits; largest 448).
+ *   k_scales, v_scales: fp16 [num_pages][Hkv]. Value = code * scale.
+ * A block's scale is the largest magnitude appended to it over M (127, or 448), each
+ * quotient rounded UP to fp16 (at most 65504), so that no code saturates below that:
+ *   s_call = up16(fp32(max|x| / M)) over the rows one call puts into the block,
+ *   s      = s_call if the call writes the block's slot 0, else max(s_before, s_call),
+ *   code   = rne(fp32(x / s)), ties to even, clamped to [-M, M]   (0 if s = 0).
+ * Where s > s_before, the codes already in the block become rne(fp32(code * s_before / s)).
+ * So a block's codes depend on how its rows were split into calls, by at most the rounding
+ * of those steps.
+ * ------------------------------------------------------------------------------------- */
+typedef enum {
+  KV4_BLOCK8_INT8 = 1,
+  KV4_BLOCK8_E4M3 = 2
+} kv4_block8_format;
+
+/* Append new tokens (the CSR contract of kv4_quantize_append; format: a kv4_block8_format).
+ * Rows are finite (an INT8 code of a NaN is 0, infinities take the largest code). Sequences
+ * must not append into the same page in one call. */
+kv4_status kv4_block8_append(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
+                             const kv4_batch *batch, const void *k_new, const void *v_new,
+                             const int32_t *new_indptr, int32_t total_new, int32_t *err_flag,
+                             kv4_stream_t stream);
+
+/* Workspace bytes for kv4_block8_attention on num_seqs sequences no longer than max_seq_len
+ * with total_q queries, at most max_q_len of one sequence (0 on invalid arguments). It does
+ * not shrink when any of the four grows. */
+size_t kv4_block8_workspace_size(const kv4_config *cfg, int32_t num_seqs, int32_t total_q,
+                                 int32_t max_q_len, int32_t max_seq_len);
+
+/* Attention over the block-scaled cache, causal, for the last positions of each sequence:
+ * with n = q_indptr[b+1] - q_indptr[b] queries, query row q_indptr[b] + i is position
+ * seq_lens[b] - n + i and sees the positions up to and including its own (a decode step, the
+ * verification of drafted tokens, a prefill chunk; its rows were appended before).
+ *   q, out:   bf16 [total_q][Hq][128]; out_f32: optional fp32 of that shape; lse: optional
+ *             fp32 [total_q][Hq] (natural log). Rows of q are finite.
+ *   q_indptr: int32 [num_seqs + 1], device; NULL = one query per sequence (total_q ==
+ *             num_seqs, max_q_len <= 1).
+ *   max_q_len: host-side upper bound on n. A sequence with more queries is refused on the
+ *             device (KV4_DEVERR_SEQ_LEN) and its rows are left as they were, as are rows
+ *             that no sequence covers.
+ *   workspace: device scratch, 256-byte aligned, of kv4_block8_workspace_size(...) bytes; no
+ *             initialisation. Calls that may overlap on the GPU need one each.
+ * A query before position 0 (n > seq_lens[b]), or of an empty sequence, sees nothing: O = 0,
+ * lse = -inf. Positions on a page id outside the pool are left out (KV4_DEVERR_PAGE_ID).
+ * Logits are sums of exact products in fp32; the weights enter PV as fp16 with 11 significant
+ * bits down to 2^-28 of a row's largest. Results do not depend on the order in which warps
+ * run. */
+kv4_status kv4_block8_attention(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
+                                const kv4_batch *batch, const void *q, const int32_t *q_indptr,
+                                int32_t total_q, int32_t max_q_len, void *out, float *out_f32,
+                                float *lse, void *workspace, size_t ws_bytes, int32_t *err_flag,
+                                kv4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Eviction from the KV4 cache by accumulated attention weight: keep the sinks, the recent
+ * window and, per kv head, the positions that past queries weighted most. (No passage of the
+ * pages defines it.) A decode step with eviction:
+ *   kv4_decode_step(..., lse), then kv4_attention_weights with that lse; when a sequence has
+ *   outgrown its budget, kv4_evict_select, kv4_evict_compact, and the batch's lengths become
+ *   new_lens. Keys are stored after their position encoding, so a kept row may move.
+ * ------------------------------------------------------------------------------------- */
+
+/* The attention weight of each cached position in a decode step, summed over the query heads
+ * of its kv head and added to a running total:
+ *   acc_out[b][h][p] = acc_in[b][h][p] + sum over g of exp(q_g k_p / sqrt(128) - lse[b][hG+g])
+ * for p < seq_lens[b]; what lies behind a length is left as it was.
+ *   q:   bf16 [num_seqs][Hq][128], finite;  lse: fp32 [num_seqs][Hq], as the attention of the
+ *        same batch wrote it (a weight is then at most 1).
+ *   acc_in, acc_out: fp32 [num_seqs][Hkv][acc_stride], may be the same; acc_in NULL = zeros.
+ *        A sequence longer than acc_stride is refused (KV4_DEVERR_SEQ_LEN). Positions on a bad
+ *        page or side index are left as they were, with its error bit. */
+kv4_status kv4_attention_weights(const kv4_config *cfg, const kv4_int4_pool *pool,
+                                 const kv4_int8_side *side, const kv4_batch *batch, const void *q,
+                                 const float *lse, const float *acc_in, float *acc_out,
+                                 int32_t acc_stride, int32_t *err_flag, kv4_stream_t stream);
+
+/* The positions to keep of each sequence and kv head. A sequence of at most `budget` positions
+ * keeps all; a longer one keeps `budget`: the S sinks, the R recent positions and the
+ * budget - S - R of the rest with the largest totals (equal ones from the lowest position on;
+ * NaN below everything, -0 equal to +0).
+ *   batch:    seq_lens and num_seqs are read.
+ *   acc:      fp32 [num_seqs][Hkv][acc_stride]; a sequence longer than acc_stride (or of a
+ *             negative length) gets new_lens 0 and KV4_DEVERR_SEQ_LEN.
+ *   budget:   at least 1 and at least S + R.
+ *   keep:     int32 [num_seqs][Hkv][budget], ascending, -1 behind the last.
+ *   new_lens: int32 [num_seqs], min(seq_lens[b], budget); not the batch's seq_lens. */
+kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const float *acc,
+                            int32_t acc_stride, int32_t budget, int32_t *keep, int32_t *new_lens,
+                            int32_t *err_flag, kv4_stream_t stream);
+
+/* Move the kept rows to the front: INT4 codes and parameters of position keep[b][h][j] to
+ * position j (j < new_lens[b]), its total to acc_out[b][h][j], and the INT8 copies of the
+ * recent window to the ring slots of their new positions. The sinks keep their places. What
+ * lies behind new_lens[b] is left as it was.
+ *   batch:     the lengths, pages, sinks and rings before.
+ *   keep:      ascending per (b, h), and holding the recent window whole, as kv4_evict_select
+ *              writes it. A position below j or not below seq_lens[b] is skipped
+ *              (KV4_DEVERR_KEEP); a window not kept whole leaves its ring as it was, with the
+ *              same bit.
+ *   dst_page_table: int32 [num_seqs][dst_max_pages], pages of the same pool that hold no row
+ *              this call reads (for sequences that share their prompt's pages); NULL = each
+ *              sequence's own pages, which no other sequence may then share.
+ *   dst_ring_idx: int32 [num_seqs], another ring for each sequence, which is no ring this call
+ *              reads; NULL = its own.
+ *   acc_in, acc_out: fp32 [num_seqs][Hkv][acc_in_stride / acc_out_stride]; both NULL = no
+ *              totals. One array for both needs equal strides and dst_page_table NULL. */
+kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
+                             const kv4_int8_side *side, const kv4_batch *batch,
+                             const int32_t *keep, int32_t budget, const int32_t *new_lens,
+                             const int32_t *dst_page_table, int32_t dst_max_pages,
+                             const int32_t *dst_ring_idx, const float *acc_in,
+                             int32_t acc_in_stride, float *acc_out, int32_t acc_out_stride,
+                             int32_t *err_flag, kv4_stream_t stream);
 
 /*
  * Testing hook for the error path of the bounded waits. No passage of the pages defines

@@ -168,10 +168,9 @@ void take_test_hook(kv4::Workspace *w) {
   g_withheld = WithheldCopy{};
 }
 
-kv4_status make_baseline_view(kv4_baseline_format fmt, const kv4_config *cfg,
-                              const kv4_paged_pool *pool, const kv4_batch *batch,
-                              kv4::CacheView *v) {
-  if (fmt != KV4_BASELINE_BF16 && fmt != KV4_BASELINE_KV8) return KV4_ERR_INVALID_ARG;
+// The pages of a cache without a protected set: BF16, per-token INT8 or 8-bit blocks.
+kv4_status make_paged_view(const kv4_config *cfg, const kv4_paged_pool *pool,
+                           const kv4_batch *batch, bool scales, kv4::CacheView *v) {
   kv4_status st = check_config(cfg);
   if (st != KV4_OK) return st;
   if (pool == nullptr || batch == nullptr) return KV4_ERR_INVALID_ARG;
@@ -182,8 +181,8 @@ kv4_status make_baseline_view(kv4_baseline_format fmt, const kv4_config *cfg,
     return KV4_ERR_INVALID_ARG;
   if (!pool->k || !pool->v || misaligned16(pool->k) || misaligned16(pool->v))
     return KV4_ERR_INVALID_ARG;
-  if (fmt == KV4_BASELINE_KV8 && (!pool->k_scales || !pool->v_scales ||
-                                  misaligned16(pool->k_scales) || misaligned16(pool->v_scales)))
+  if (scales && (!pool->k_scales || !pool->v_scales || misaligned16(pool->k_scales) ||
+                 misaligned16(pool->v_scales)))
     return KV4_ERR_INVALID_ARG;
   *v = kv4::CacheView{};
   v->k_codes = static_cast<uint8_t *>(pool->k);
@@ -198,6 +197,19 @@ kv4_status make_baseline_view(kv4_baseline_format fmt, const kv4_config *cfg,
   v->num_kv_heads = cfg->num_kv_heads;
   v->gqa = cfg->num_q_heads / cfg->num_kv_heads;
   return KV4_OK;
+}
+
+kv4_status make_baseline_view(kv4_baseline_format fmt, const kv4_config *cfg,
+                              const kv4_paged_pool *pool, const kv4_batch *batch,
+                              kv4::CacheView *v) {
+  if (fmt != KV4_BASELINE_BF16 && fmt != KV4_BASELINE_KV8) return KV4_ERR_INVALID_ARG;
+  return make_paged_view(cfg, pool, batch, fmt == KV4_BASELINE_KV8, v);
+}
+
+kv4_status make_block8_view(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
+                            const kv4_batch *batch, kv4::CacheView *v) {
+  if (format != KV4_BLOCK8_INT8 && format != KV4_BLOCK8_E4M3) return KV4_ERR_INVALID_ARG;
+  return make_paged_view(cfg, pool, batch, true, v);
 }
 
 // Carve the workspace for (cfg, batch): the automatic chunk choice, falling back to the
@@ -398,6 +410,130 @@ kv4_status kv4_baseline_decode_attention(kv4_baseline_format fmt, const kv4_conf
     e = kv4::launch_merge(w.partials, w.unit_offsets, batch->num_seqs * v.num_kv_heads, v.gqa,
                           static_cast<uint16_t *>(out), out_f32, lse, w.counter,
                           w.check_plan ? &sig : nullptr, s);
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_block8_append(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
+                             const kv4_batch *batch, const void *k_new, const void *v_new,
+                             const int32_t *new_indptr, int32_t total_new, int32_t *err_flag,
+                             kv4_stream_t stream) {
+  if (cfg == nullptr) return KV4_ERR_INVALID_ARG;
+  const kv4_config c = without_protection(cfg);
+  kv4::CacheView v;
+  kv4_status st = make_block8_view(format, &c, pool, batch, &v);
+  if (st != KV4_OK) return st;
+  if (total_new < 0) return KV4_ERR_INVALID_ARG;
+  if (new_indptr == nullptr && total_new != batch->num_seqs) return KV4_ERR_INVALID_ARG;
+  if (total_new > 0 && (k_new == nullptr || v_new == nullptr)) return KV4_ERR_INVALID_ARG;
+  if (misaligned16(k_new) || misaligned16(v_new)) return KV4_ERR_INVALID_ARG;
+  if (total_new == 0 || batch->num_seqs == 0) return KV4_OK;
+  cudaError_t e = kv4::launch_block8_append(format, v, static_cast<const uint16_t *>(k_new),
+                                            static_cast<const uint16_t *>(v_new), new_indptr,
+                                            total_new, err_flag,
+                                            reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+size_t kv4_block8_workspace_size(const kv4_config *cfg, int32_t num_seqs, int32_t total_q,
+                                 int32_t max_q_len, int32_t max_seq_len) {
+  if (cfg == nullptr) return 0;
+  const kv4_config c = without_protection(cfg);
+  if (check_config(&c) != KV4_OK || num_seqs < 0 || total_q < 0 || max_q_len < 0 ||
+      max_seq_len < 0)
+    return 0;
+  return kv4::block8_workspace_bytes(num_seqs, total_q, max_q_len, max_seq_len, c.num_kv_heads,
+                                     c.num_q_heads / c.num_kv_heads);
+}
+
+kv4_status kv4_block8_attention(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
+                                const kv4_batch *batch, const void *q, const int32_t *q_indptr,
+                                int32_t total_q, int32_t max_q_len, void *out, float *out_f32,
+                                float *lse, void *workspace, size_t ws_bytes, int32_t *err_flag,
+                                kv4_stream_t stream) {
+  if (cfg == nullptr) return KV4_ERR_INVALID_ARG;
+  const kv4_config c = without_protection(cfg);
+  kv4::CacheView v;
+  kv4_status st = make_block8_view(format, &c, pool, batch, &v);
+  if (st != KV4_OK) return st;
+  if (total_q < 0 || max_q_len < 0) return KV4_ERR_INVALID_ARG;
+  if (q_indptr == nullptr && (total_q != batch->num_seqs || max_q_len > 1))
+    return KV4_ERR_INVALID_ARG;
+  if (total_q == 0 || batch->num_seqs == 0 || max_q_len == 0) return KV4_OK;
+  st = check_attention_args(batch, q, out, out_f32, workspace);
+  if (st != KV4_OK) return st;
+  if (ws_bytes < kv4_block8_workspace_size(cfg, batch->num_seqs, total_q, max_q_len,
+                                           batch->max_seq_len))
+    return KV4_ERR_WORKSPACE_TOO_SMALL;
+  const kv4::Outputs o{static_cast<uint16_t *>(out), out_f32, lse};
+  cudaError_t e = kv4::launch_block8_attention(format, v, static_cast<const uint16_t *>(q), q_indptr,
+                                               total_q, max_q_len, batch->max_seq_len, o, workspace,
+                                               err_flag, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_attention_weights(const kv4_config *cfg, const kv4_int4_pool *pool,
+                                 const kv4_int8_side *side, const kv4_batch *batch, const void *q,
+                                 const float *lse, const float *acc_in, float *acc_out,
+                                 int32_t acc_stride, int32_t *err_flag, kv4_stream_t stream) {
+  kv4::CacheView v;
+  kv4_status st = make_view(cfg, pool, side, batch, &v);
+  if (st != KV4_OK) return st;
+  if (acc_stride < 0) return KV4_ERR_INVALID_ARG;
+  if (batch->num_seqs == 0) return KV4_OK;
+  if (q == nullptr || lse == nullptr || acc_out == nullptr || misaligned16(q))
+    return KV4_ERR_INVALID_ARG;
+  cudaError_t e = kv4::launch_weights(v, batch->max_seq_len, static_cast<const uint16_t *>(q), lse,
+                                      acc_in, acc_out, acc_stride, err_flag,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const float *acc,
+                            int32_t acc_stride, int32_t budget, int32_t *keep, int32_t *new_lens,
+                            int32_t *err_flag, kv4_stream_t stream) {
+  kv4_status st = check_config(cfg);
+  if (st != KV4_OK) return st;
+  if (batch == nullptr || batch->num_seqs < 0 || acc_stride < 0 || budget < 1 ||
+      budget < cfg->num_sinks + cfg->num_recent)
+    return KV4_ERR_INVALID_ARG;
+  if (batch->num_seqs == 0) return KV4_OK;
+  if (batch->seq_lens == nullptr || acc == nullptr || keep == nullptr || new_lens == nullptr)
+    return KV4_ERR_INVALID_ARG;
+  kv4::CacheView v{};
+  v.seq_lens = batch->seq_lens;
+  v.num_seqs = batch->num_seqs;
+  v.num_kv_heads = cfg->num_kv_heads;
+  v.num_sinks = cfg->num_sinks;
+  v.num_recent = cfg->num_recent;
+  cudaError_t e = kv4::launch_select(v, acc, acc_stride, budget, keep, new_lens, err_flag,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
+                             const kv4_int8_side *side, const kv4_batch *batch,
+                             const int32_t *keep, int32_t budget, const int32_t *new_lens,
+                             const int32_t *dst_page_table, int32_t dst_max_pages,
+                             const int32_t *dst_ring_idx, const float *acc_in,
+                             int32_t acc_in_stride, float *acc_out, int32_t acc_out_stride,
+                             int32_t *err_flag, kv4_stream_t stream) {
+  kv4::CacheView v;
+  kv4_status st = make_view(cfg, pool, side, batch, &v);
+  if (st != KV4_OK) return st;
+  if (budget < 1 || acc_in_stride < 0 || acc_out_stride < 0) return KV4_ERR_INVALID_ARG;
+  if (dst_page_table != nullptr && dst_max_pages < 1) return KV4_ERR_INVALID_ARG;
+  if ((acc_in == nullptr) != (acc_out == nullptr)) return KV4_ERR_INVALID_ARG;
+  // rows moved to other pages are moved in any order, so their totals need other room too;
+  // in one array the rows of the totals must not slide over one another either
+  if (acc_in != nullptr && acc_in == acc_out &&
+      (dst_page_table != nullptr || acc_in_stride != acc_out_stride))
+    return KV4_ERR_INVALID_ARG;
+  if (batch->num_seqs == 0) return KV4_OK;
+  if (keep == nullptr || new_lens == nullptr || new_lens == batch->seq_lens)
+    return KV4_ERR_INVALID_ARG;
+  cudaError_t e = kv4::launch_compact(v, keep, budget, new_lens, dst_page_table, dst_max_pages,
+                                      dst_ring_idx, acc_in, acc_in_stride, acc_out, acc_out_stride,
+                                      err_flag, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
 }
 

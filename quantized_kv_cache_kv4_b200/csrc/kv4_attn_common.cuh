@@ -271,4 +271,11 @@ __device__ __forceinline__ float query_step(float amax) {
   return ldexpf(1.0f, ex);
 }
 
+// Step of a query that enters as fp16: its largest element over the step is in
+// [2^14, 2^15), where bf16 elements down to 2^-31 of the largest are exact (the step stays
+// above 2^-120, so that its reciprocal is finite).
+__device__ __forceinline__ float half_range_step(float amax) {
+  return fmaxf(query_step(amax) * 0.5f, 0x1p-120f);
+}
+
 }  // namespace kv4

@@ -1,0 +1,709 @@
+// The 8-bit block-scaled cache: pages of 16 positions held as INT8 or e4m3 codes with one
+// fp16 scale per (page, kv head), for K and for V. Value = code * scale.
+//
+//   block8_append_token_kernel  one new row per sequence: one warp per (sequence, kv head).
+//   block8_append_rows_kernel   CSR rows: one warp per (page touched, kv head).
+//   block8_attn_kernel<F>       attention with up to 8 query rows (a kv head's query heads
+//                               of one or more positions) per warp, split over the pages.
+//   block8_merge_kernel         the exact merge of the units that several warps share.
+//
+// Block scale. A block's scale is the largest row magnitude it has seen over the largest
+// code (127, or 448 for e4m3), rounded UP to fp16, so that no code saturates (rounding to
+// nearest would lose up to half the range where fp16 is subnormal). A row that raises it
+// has the codes already in the block rounded again: code' = rne(code * s_old / s).
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "kv4_attn_common.cuh"
+#include "kv4_split.cuh"
+
+namespace kv4 {
+
+constexpr int kFmtInt8 = KV4_BLOCK8_INT8;
+constexpr int kFmtE4m3 = KV4_BLOCK8_E4M3;
+
+template <int F>
+struct Fmt8 {
+  static constexpr float kMax = F == KV4_BLOCK8_INT8 ? 127.0f : 448.0f;
+  static constexpr float kRcp = 1.0f / (F == KV4_BLOCK8_INT8 ? 127.0f : 448.0f);
+};
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+// fp16 scale of a block whose largest magnitude is amax, rounded up, at most 65504.
+template <int F>
+__device__ __forceinline__ __half block_scale(float amax) {
+  const float s = quotient_rn(fminf(amax, 3.0e38f), Fmt8<F>::kMax, Fmt8<F>::kRcp);
+  return __float2half_ru(fminf(s, 65504.0f));
+}
+
+// Four values over the scale (y = 1/s; 0 when s = 0) to four codes. The quotient is the
+// IEEE one (quotient_rn: the scale has 11 significant bits), so a code is the nearest one
+// to the exact quotient: bf16 rows and stored code * scale products have at most 18.
+template <int F>
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float s, float y) {
+  if constexpr (F == kFmtInt8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = max(-127, min(127, __float2int_rn(quotient_rn(x[i], s, y))));
+      w |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * i);
+    }
+    return w;
+  } else {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(quotient_rn(x[0], s, y), quotient_rn(x[1], s, y)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(quotient_rn(x[2], s, y), quotient_rn(x[3], s, y)), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
+}
+
+template <int F>
+__device__ __forceinline__ void values4(uint32_t w, float s, float (&x)[4]) {
+  if constexpr (F == kFmtInt8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = static_cast<float>(static_cast<int8_t>((w >> (8 * i)) & 0xFFu)) * s;
+  } else {
+    const float2 a = __half22float2(
+        __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3)));
+    const float2 b = __half22float2(
+        __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)));
+    x[0] = a.x * s; x[1] = a.y * s; x[2] = b.x * s; x[3] = b.y * s;
+  }
+}
+
+__device__ __forceinline__ void unpack_bf16x4(uint2 raw, float (&x)[4]) {
+  x[0] = __uint_as_float(raw.x << 16);
+  x[1] = __uint_as_float(raw.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(raw.y << 16);
+  x[3] = __uint_as_float(raw.y & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+// The codes of rows [0, rows) of a block rounded again from scale s_old to s.
+template <int F>
+__device__ __forceinline__ void rescale_block(uint8_t *block, int rows, float s_old, float s, float y,
+                                              int lane) {
+  for (int i = lane; i < rows * 8; i += 32) {  // 16-byte pieces: strip i / rows, row i % rows
+    uint4 *p = reinterpret_cast<uint4 *>(block + (i / rows) * (kPage * 16) + (i % rows) * 16);
+    uint4 v = *p;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float x[4];
+      values4<F>(w[k], s_old, x);
+      w[k] = codes4<F>(x, s, y);
+    }
+    *p = v;
+  }
+}
+
+// New rows `first` .. first+n-1 (n <= 16 - slot) of one kv head into slots slot .. of block
+// (page, head) of one array. One warp; lane l holds dims 4l .. 4l+3.
+template <int F, int N>
+__device__ __forceinline__ void append_block(uint8_t *block, uint16_t *scale,
+                                             const uint16_t *__restrict__ rows, size_t row_stride,
+                                             int n, int slot, int lane) {
+  uint2 raw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    raw[i] = i < n ? *reinterpret_cast<const uint2 *>(rows + i * row_stride + 4 * lane)
+                   : make_uint2(0u, 0u);
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x[4];
+    unpack_bf16x4(raw[i], x);
+    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+  }
+  __half sh = block_scale<F>(warp_max(amax));
+  float s = __half2float(sh);
+  const float s_old = slot > 0 ? __half2float(__ushort_as_half(*scale)) : 0.f;
+  if (slot > 0 && s <= s_old) {  // (a block's first slot starts its scale anew)
+    s = s_old;
+  } else {
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale = __half_as_ushort(sh);
+  }
+  const float y = s == 0.f ? 0.f : __frcp_rn(s);
+  if (slot > 0 && s > s_old) rescale_block<F>(block, slot, s_old, s, y, lane);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i >= n) break;
+    float x[4];
+    unpack_bf16x4(raw[i], x);
+    // [8 strips of 16 dims][16 slots][16 bytes]: lane l -> strip l / 4, bytes 4 (l % 4)
+    *reinterpret_cast<uint32_t *>(block + (lane >> 2) * (kPage * 16) + (slot + i) * 16 +
+                                  4 * (lane & 3)) = codes4<F>(x, s, y);
+  }
+}
+
+template <int F>
+__global__ void __launch_bounds__(256) block8_append_token_kernel(
+    CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
+    int32_t *err) {
+  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const int H = c.num_kv_heads;
+  if (warp >= c.num_seqs * H) return;
+  const int b = warp / H, h = warp - b * H;
+  const int L = c.seq_lens[b], pos = L - 1;
+  if (pos < 0 || L > c.max_pages * kPage) {
+    if (lane == 0) set_err(err, KV4_DEVERR_SEQ_LEN);
+    return;
+  }
+  const int page = c.page_table[static_cast<size_t>(b) * c.max_pages + pos / kPage];
+  if (page < 0 || page >= c.num_pages) {
+    if (lane == 0) set_err(err, KV4_DEVERR_PAGE_ID);
+    return;
+  }
+  const size_t blk = static_cast<size_t>(page) * H + h;
+  const size_t row = static_cast<size_t>(warp) * kHeadDim;
+  append_block<F, 1>(c.k_codes + blk * kInt8CodeBytes, c.k_params + blk, k_new + row, 0, 1,
+                     pos % kPage, lane);
+  append_block<F, 1>(c.v_codes + blk * kInt8CodeBytes, c.v_params + blk, v_new + row, 0, 1,
+                     pos % kPage, lane);
+}
+
+// A CTA looks over 16 rows; the first row of the call in each page leads that page's rows
+// (they may reach past the CTA's 16). One warp per (led page, kv head, K or V).
+constexpr int kRowsPerCta = 16;
+template <int F>
+__global__ void __launch_bounds__(256) block8_append_rows_kernel(
+    CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
+    const int32_t *__restrict__ indptr, int32_t total_new, int32_t *err) {
+  __shared__ int4 lead[kRowsPerCta];  // (first row, rows, slot, page)
+  __shared__ int n_lead;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H = c.num_kv_heads;
+  if (warp == 0) {
+    const int row = blockIdx.x * kRowsPerCta + lane;
+    int4 e = make_int4(0, 0, 0, 0);
+    bool leads = false;
+    if (lane < kRowsPerCta && row < total_new) {
+      int b, pos, L;
+      locate_new_token(c.seq_lens, c.num_seqs, indptr, row, b, pos, L);
+      const int i = row - indptr[b], n = indptr[b + 1] - indptr[b];
+      if (i >= 0 && i < n) {  // (rows behind the last sequence belong to none)
+        if (pos < 0 || pos >= L || L > c.max_pages * kPage || indptr[b + 1] > total_new) {
+          set_err(err, KV4_DEVERR_SEQ_LEN);
+        } else if (i == 0 || pos % kPage == 0) {
+          const int page = c.page_table[static_cast<size_t>(b) * c.max_pages + pos / kPage];
+          if (page < 0 || page >= c.num_pages) {
+            set_err(err, KV4_DEVERR_PAGE_ID);
+          } else {
+            leads = true;
+            e = make_int4(row, min(n - i, kPage - pos % kPage), pos % kPage, page);
+          }
+        }
+      }
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, leads);
+    if (leads) lead[__popc(m & ((1u << lane) - 1u))] = e;
+    if (lane == 0) n_lead = __popc(m);
+  }
+  __syncthreads();
+  const int tasks = n_lead * H * 2;
+  for (int t = warp; t < tasks; t += blockDim.x >> 5) {
+    const int4 e = lead[t / (2 * H)];
+    const int r = t % (2 * H), h = r >> 1;
+    const bool v = (r & 1) != 0;
+    const size_t blk = static_cast<size_t>(e.w) * H + h;
+    const size_t stride = static_cast<size_t>(H) * kHeadDim;
+    append_block<F, 16>((v ? c.v_codes : c.k_codes) + blk * kInt8CodeBytes,
+                        (v ? c.v_params : c.k_params) + blk,
+                        (v ? v_new : k_new) + e.x * stride + h * kHeadDim, stride, e.y, e.z, lane);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// attention: the split of a batch over warps
+// ---------------------------------------------------------------------------
+// A unit is 8 query rows of one (sequence, kv head): row r = position i * G + query head g
+// of the sequence's last n positions. Every unit reads the sequence's pages, so the batch
+// is T = sum over sequences of units * pages; warp w takes the w-th of W contiguous, equal
+// shares (to one page). A unit inside one warp's share is finished there; of a unit that
+// several warps share, each writes a partial record and the merge kernel joins them in
+// order. A warp has at most two such units: its first (record 2w) and its last (2w + 1).
+constexpr int kAttnCtas = 148 * 3;            // resident CTAs of the largest grid
+constexpr int kAttnWarps = kAttnCtas * kWarps;
+constexpr int kCols = 8;                      // query rows of a unit (MMA N)
+
+struct Seq8 {
+  int L, n, row0;  // length, queries, first query row
+  int pages;       // pages a unit of it takes (1 for an empty sequence: it writes zeros)
+  int units;       // per kv head
+};
+
+// The queries of a call: CSR rows (indptr nullptr: one per sequence), at most max_n of one
+// sequence.
+struct Queries {
+  const uint16_t *q;
+  const int32_t *indptr;
+  int32_t total, max_n;
+};
+
+__device__ __forceinline__ Seq8 seq_of(const CacheView &c, const Queries &qs, int b, int32_t *err) {
+  Seq8 s;
+  s.L = c.seq_lens[b];
+  if (s.L < 0 || s.L > c.max_pages * kPage) {
+    set_err(err, KV4_DEVERR_SEQ_LEN);
+    s.L = 0;
+  }
+  s.row0 = b;
+  s.n = 1;
+  if (qs.indptr != nullptr) {
+    s.row0 = qs.indptr[b];
+    const int end = qs.indptr[b + 1];
+    s.n = end - s.row0;
+    if (s.row0 < 0 || end < s.row0 || end > qs.total || s.n > qs.max_n) {
+      set_err(err, KV4_DEVERR_SEQ_LEN);
+      s.n = 0;
+    }
+  }
+  s.pages = max(1, (s.L + kPage - 1) / kPage);
+  s.units = (s.n * c.gqa + kCols - 1) / kCols;
+  return s;
+}
+
+// Sum over a block of up to 128 threads' values; every thread gets it.
+__device__ __forceinline__ long long block_sum(long long v, long long *scratch) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  long long t = 0;
+  for (int i = 0; i < (blockDim.x >> 5); ++i) t += scratch[i];
+  __syncthreads();
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// attention: codes to tensor-core operands
+// ---------------------------------------------------------------------------
+// A 32-bit word of four codes (bytes 0..3) as two fp16 pairs: (0, 1), (2, 3) for K and
+// (0, 2), (1, 3) for V, whose transposed ldmatrix words hold two dims of two tokens.
+// Both formats are exact in fp16.
+template <int F, bool V>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &a, uint32_t &b) {
+  if constexpr (F == kFmtInt8) {
+    const uint32_t u = w ^ 0x80808080u;
+    a = V ? s8_pair<0x4240>(u) : s8_pair<0x4140>(u);
+    b = V ? s8_pair<0x4341>(u) : s8_pair<0x4342>(u);
+  } else {
+    const uint32_t u = V ? prmt(w, 0u, 0x3120) : w;
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u & 0xFFFFu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16), __NV_E4M3);
+    a = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
+    b = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
+  }
+}
+
+// 8 x 8 fp16 matrix held as MMA fragments, transposed in registers.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+constexpr int kStages8 = 4;                               // pages in flight per warp
+constexpr int kStage8Bytes = 2 * kInt8CodeBytes;          // K then V of one (page, kv head)
+constexpr int kWarp8Smem = kStages8 * kStage8Bytes;
+constexpr int kCta8Smem = kWarps * kWarp8Smem;
+// The weights p = 2^(s - m) enter PV in fp16 as p * 2^14: 11 significant bits down to
+// p = 2^-28, and at most 16384. The running maximum is kept as m - 14, which makes
+// (m - 14, l 2^14, acc 2^14) the same softmax state.
+constexpr float kLift8 = 14.0f;
+
+template <int F>
+__global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
+    CacheView c, Queries qs, Outputs out, float *__restrict__ partials, int32_t *err) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ SplitSmem split;
+  __shared__ uint64_t bars_all[kWarps][kStages8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int G = c.gqa, H = c.num_kv_heads, B = c.num_seqs;
+  uint8_t *stage0 = smem + warp * kWarp8Smem;
+  uint64_t *bars = bars_all[warp];
+  if (lane == 0) {
+    for (int s = 0; s < kStages8; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
+  }
+  auto items = [&](const Seq8 &s) { return static_cast<long long>(s.units) * s.pages * H; };
+  const int me = blockIdx.x * kWarps + warp;
+  const Share share = take_share(B, me, gridDim.x * kWarps, split, [&](int i, bool check) {
+    return items(seq_of(c, qs, i, check && blockIdx.x == 0 ? err : nullptr));
+  });
+  const long long t_begin = share.begin, t_end = share.end;
+  if (t_begin >= t_end) return;
+  int b = share.b;
+  long long seq_first = share.seq_first;  // first item of sequence b
+  Seq8 sq = seq_of(c, qs, b, nullptr);
+
+  uint32_t parity = 0;
+  const int mi = lane >> 3, r8 = lane & 7;
+  // ldmatrix lane addresses of two strips: (strip 2pr | slots 0-7), (| slots 8-15), strip 2pr+1
+  const int ld8 = ((mi >> 1) * 256) + (mi & 1) * 128 + r8 * 16;
+  for (long long t = t_begin; t < t_end;) {
+    while (t >= seq_first + items(sq)) {
+      seq_first += items(sq);
+      sq = seq_of(c, qs, ++b, nullptr);
+    }
+    // unit (h, u) of the sequence: its pages pg0 .. pg1-1 are this warp's
+    const long long in_seq = t - seq_first;
+    const int unit = static_cast<int>(in_seq / sq.pages);
+    const int pg0 = static_cast<int>(in_seq - static_cast<long long>(unit) * sq.pages);
+    const int pg1 = static_cast<int>(min(static_cast<long long>(sq.pages), pg0 + (t_end - t)));
+    const int h = unit / sq.units, u = unit - h * sq.units;
+    const bool whole = pg0 == 0 && pg1 == sq.pages;
+    const int np = sq.L > 0 ? pg1 - pg0 : 0;
+    const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages + pg0;
+
+    // page ids and scales of 32 pages at a time, page k in lane k % 32
+    int pid = -1;
+    float ks_l = 0.f, vs_l = 0.f;
+    auto load_pages = [&](int k0) {
+      pid = -1;
+      ks_l = vs_l = 0.f;
+      if (k0 + lane < np) {
+        pid = pt[k0 + lane];
+        if (pid < 0 || pid >= c.num_pages) {
+          set_err(err, KV4_DEVERR_PAGE_ID);
+          pid = -1;  // the page's positions are left out
+        } else {
+          ks_l = __half2float(__ushort_as_half(c.k_params[static_cast<size_t>(pid) * H + h]));
+          vs_l = __half2float(__ushort_as_half(c.v_params[static_cast<size_t>(pid) * H + h]));
+        }
+      }
+    };
+    int pid_next = -1;  // ids of the 32 pages after those (their copies start early)
+    auto load_next = [&](int k0) {
+      pid_next = -1;
+      if (k0 + lane < np) {
+        pid_next = pt[k0 + lane];
+        if (pid_next < 0 || pid_next >= c.num_pages) pid_next = -1;
+      }
+    };
+    int block0 = 0;  // first page of pid's 32
+    auto issue = [&](int k) {
+      const int p_now = __shfl_sync(0xffffffffu, pid, k & 31);
+      const int p_nxt = __shfl_sync(0xffffffffu, pid_next, k & 31);
+      const int pk = k - block0 < 32 ? p_now : p_nxt;
+      const int st = k % kStages8;
+      if (lane == 0) {
+        uint8_t *dst = stage0 + st * kStage8Bytes;
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&bars[st], pk < 0 ? 0 : kStage8Bytes);
+        if (pk >= 0) {
+          const size_t off = (static_cast<size_t>(pk) * H + h) * kInt8CodeBytes;
+          bulk_g2s(dst, c.k_codes + off, kInt8CodeBytes, &bars[st]);
+          bulk_g2s(dst + kInt8CodeBytes, c.v_codes + off, kInt8CodeBytes, &bars[st]);
+        }
+      }
+    };
+    load_pages(0);
+    load_next(32);
+    int issued = min(np, kStages8);
+    for (int k = 0; k < issued; ++k) issue(k);
+
+    // ---- query fragments: column gid = query row u * 8 + gid, scaled by a power of two to
+    // [2^14, 2^15) at its largest element, so that its bf16 elements are exact in fp16 (what
+    // is under 2^-31 of the largest loses bits that no logit shows) ----
+    const int rows = sq.n * G;
+    const int r = u * kCols + gid;
+    uint32_t qb[8][2];
+    float kq[2];
+    int lim[2];  // last position the columns 2tig, 2tig + 1 see
+    {
+      const bool live = r < rows;
+      const uint16_t *qrow = qs.q + (static_cast<size_t>(sq.row0 + r / G) * H * G + h * G + r % G) * kHeadDim;
+      float qv[8][4];
+      float amax = 0.f;
+#pragma unroll
+      for (int cc = 0; cc < 8; ++cc) {
+        const uint2 v = live ? *reinterpret_cast<const uint2 *>(qrow + 16 * cc + 4 * tig) : make_uint2(0u, 0u);
+        unpack_bf16x4(v, qv[cc]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(qv[cc][i]));
+      }
+      const float step = half_range_step(amax);
+      const float inv = 1.0f / step;               // a power of two: exact
+#pragma unroll
+      for (int cc = 0; cc < 8; ++cc) {
+        qb[cc][0] = pack_h2(qv[cc][0] * inv, qv[cc][1] * inv);
+        qb[cc][1] = pack_h2(qv[cc][2] * inv, qv[cc][3] * inv);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kq[e] = __shfl_sync(0xffffffffu, step, 4 * (2 * tig + e)) * kScaleLog2;
+        const int rc = u * kCols + 2 * tig + e;
+        lim[e] = rc < rows ? sq.L - sq.n + rc / G : -1;
+      }
+    }
+    float m[2] = {kNegBig, kNegBig}, l[2] = {0.f, 0.f};
+    float o[8][4];
+#pragma unroll
+    for (int cc = 0; cc < 8; ++cc) o[cc][0] = o[cc][1] = o[cc][2] = o[cc][3] = 0.f;
+
+    bool dead = false;
+    for (int j = 0; j < np; ++j) {
+      if (j - block0 == 32) {
+        block0 += 32;
+        load_pages(block0);
+        load_next(block0 + 32);
+      }
+      const int st = j % kStages8;
+      if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u)) {
+        if (lane == 0) set_err(err, KV4_DEVERR_TIMEOUT);
+        for (int k = j; k < issued; ++k)  // let its copies in flight land before it ends
+          mbar_wait_bounded(&bars[k % kStages8], (parity >> (k % kStages8)) & 1u, kWaitLimit * 16u);
+        dead = true;
+        break;
+      }
+      parity ^= 1u << st;
+      const bool bad = __shfl_sync(0xffffffffu, pid, j & 31) < 0;
+      const float ks = __shfl_sync(0xffffffffu, ks_l, j & 31);
+      const float vs = __shfl_sync(0xffffffffu, vs_l, j & 31);
+      if (!bad) {
+        const uint32_t sa = smem_u32(stage0 + st * kStage8Bytes);
+        const int tok0 = (pg0 + j) * kPage;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr) {
+          uint32_t kw[4];
+          ldsm_x4(kw, sa + pr * 512 + ld8);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t a01, a23, a45, a67;
+            code_pairs<F, false>(kw[2 * hf], a01, a45);
+            code_pairs<F, false>(kw[2 * hf + 1], a23, a67);
+            mma_f16(d, a01, a23, a45, a67, qb[2 * pr + hf][0], qb[2 * pr + hf][1]);
+          }
+        }
+        float s[2][2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            s[hf][e] = tok0 + gid + 8 * hf <= lim[e] ? d[2 * hf + e] * (ks * kq[e]) : -CUDART_INF_F;
+        float a[2];
+        softmax_step(s, m, l, a, kLift8);
+        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+          for (int cc = 0; cc < 8; ++cc) {
+            o[cc][0] *= a[0]; o[cc][1] *= a[1]; o[cc][2] *= a[0]; o[cc][3] *= a[1];
+          }
+        }
+        // P (tokens x columns) to the B operand (columns' tokens in pairs)
+        const uint32_t b01 = transpose8x8(pack_h2(s[0][0], s[0][1]));
+        const uint32_t b23 = transpose8x8(pack_h2(s[1][0], s[1][1]));
+        // the slots behind the length may hold anything (e4m3 NaN codes): zero them
+        uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;  // tokens 2tig, +1 and 8 + those
+        if (tok0 + kPage > sq.L) {
+          const int left = sq.L - tok0;
+          keep_lo = (2 * tig < left ? 0xFFFFu : 0u) | (2 * tig + 1 < left ? 0xFFFF0000u : 0u);
+          keep_hi = (2 * tig + 8 < left ? 0xFFFFu : 0u) | (2 * tig + 9 < left ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr) {
+          uint32_t vw[4];
+          ldsm_x4_t(vw, sa + kInt8CodeBytes + pr * 512 + ld8);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t a01, a23, a45, a67;
+            code_pairs<F, true>(vw[2 * hf] & keep_lo, a01, a23);
+            code_pairs<F, true>(vw[2 * hf + 1] & keep_hi, a45, a67);
+            float t4[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(t4, a01, a23, a45, a67, b01, b23);
+            float (&oo)[4] = o[2 * pr + hf];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oo[i] = fmaf(vs, t4[i], oo[i]);
+          }
+        }
+      }
+      __syncwarp();
+      if (issued < np) issue(issued++);  // the stage is free again
+    }
+    if (dead) return;
+
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = 2 * tig + e, rc = u * kCols + col;
+      if (whole) {
+        if (rc >= rows) continue;
+        const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
+        const float inv = l[e] > 0.f ? 1.0f / l[e] : 0.f;
+#pragma unroll
+        for (int cc = 0; cc < 8; ++cc) {  // C rows gid, gid + 8: dims 16cc + 2gid, + 1
+          const float x = o[cc][e] * inv, y = o[cc][2 + e] * inv;
+          *reinterpret_cast<__nv_bfloat162 *>(out.out + qr * kHeadDim + 16 * cc + 2 * gid) =
+              __floats2bfloat162_rn(x, y);
+          if (out.out_f32)
+            *reinterpret_cast<float2 *>(out.out_f32 + qr * kHeadDim + 16 * cc + 2 * gid) = make_float2(x, y);
+        }
+        if (out.lse && gid == 0) out.lse[qr] = l[e] > 0.f ? m[e] * kLn2 + logf(l[e]) : -CUDART_INF_F;
+      } else {
+        float *rec = partials + (static_cast<size_t>(2 * me + (t == t_begin ? 0 : 1)) * kCols + col) *
+                                    kRecordFloats;
+#pragma unroll
+        for (int cc = 0; cc < 8; ++cc)
+          st_rec(reinterpret_cast<float2 *>(rec + 16 * cc + 2 * gid), make_float2(o[cc][e], o[cc][2 + e]));
+        if (gid == 0) st_rec(reinterpret_cast<float2 *>(rec + kHeadDim), make_float2(m[e], l[e]));
+      }
+    }
+    t += pg1 - pg0;
+  }
+}
+
+// One CTA row per sequence (blockIdx.x), its units spread over blockIdx.y and the warps:
+// the units that several warps shared are joined in warp order; each column by a warp.
+__global__ void __launch_bounds__(kWarps * 32) block8_merge_kernel(
+    CacheView c, Queries qs, Outputs out, const float *__restrict__ partials, int attn_warps) {
+  __shared__ long long scratch[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = c.gqa, H = c.num_kv_heads, B = c.num_seqs, b = blockIdx.x;
+  long long before = 0, all = 0;
+  for (int i = threadIdx.x; i < B; i += blockDim.x) {
+    const Seq8 s = seq_of(c, qs, i, nullptr);
+    const long long n = static_cast<long long>(s.units) * s.pages * H;
+    all += n;
+    if (i < b) before += n;
+  }
+  const long long T = block_sum(all, scratch);
+  const long long first = block_sum(before, scratch);
+  if (T == 0) return;
+  const Shares sh(T, attn_warps);
+  const Seq8 sq = seq_of(c, qs, b, nullptr);
+  const int rows = sq.n * G;
+  const int n_tasks = sq.units * H * kCols;  // (unit, column)
+  for (int task = blockIdx.y * kWarps + warp; task < n_tasks; task += gridDim.y * kWarps) {
+    const int unit = task / kCols, col = task % kCols;
+    const int h = unit / sq.units, u = unit - h * sq.units;
+    const int rc = u * kCols + col;
+    if (rc >= rows) continue;
+    const long long t0 = first + static_cast<long long>(unit) * sq.pages;
+    const int w0 = sh.owner(t0), w1 = sh.owner(t0 + sq.pages - 1);
+    if (w0 == w1) continue;  // finished by its warp
+    float mm = kNegBig, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0; w <= w1; ++w) {
+      const int slot = sh.begin(w) >= t0 ? 0 : 1;
+      const float *rec = partials + (static_cast<size_t>(2 * w + slot) * kCols + col) * kRecordFloats;
+      const float2 ml = *reinterpret_cast<const float2 *>(rec + kHeadDim);
+      if (ml.y <= 0.f) continue;
+      const float4 v = *reinterpret_cast<const float4 *>(rec + 4 * lane);
+      const float mn = fmaxf(mm, ml.x);
+      const float a = fast_exp2(mm - mn), e = fast_exp2(ml.x - mn);
+      ll = ll * a + ml.y * e;
+      acc.x = acc.x * a + v.x * e; acc.y = acc.y * a + v.y * e;
+      acc.z = acc.z * a + v.z * e; acc.w = acc.w * a + v.w * e;
+      mm = mn;
+    }
+    const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
+    const float inv = ll > 0.f ? 1.0f / ll : 0.f;
+    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    uint2 packed = make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+    *reinterpret_cast<uint2 *>(out.out + qr * kHeadDim + 4 * lane) = packed;
+    if (out.out_f32) *reinterpret_cast<float4 *>(out.out_f32 + qr * kHeadDim + 4 * lane) = acc;
+    if (out.lse && lane == 0) out.lse[qr] = ll > 0.f ? mm * kLn2 + logf(ll) : -CUDART_INF_F;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+template <int F>
+static cudaError_t launch_block8_append_t(const CacheView &c, const uint16_t *k_new,
+                                          const uint16_t *v_new, const int32_t *indptr,
+                                          int32_t total_new, int32_t *err, cudaStream_t s) {
+  if (indptr == nullptr) {
+    const long long warps = static_cast<long long>(c.num_seqs) * c.num_kv_heads;
+    const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
+    block8_append_token_kernel<F><<<blocks, 256, 0, s>>>(c, k_new, v_new, err);
+  } else {
+    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(total_new) + kRowsPerCta - 1) / kRowsPerCta);
+    block8_append_rows_kernel<F><<<blocks, 256, 0, s>>>(c, k_new, v_new, indptr, total_new, err);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_block8_append(int fmt, const CacheView &c, const uint16_t *k_new,
+                                 const uint16_t *v_new, const int32_t *indptr, int32_t total_new,
+                                 int32_t *err, cudaStream_t s) {
+  return fmt == kFmtInt8 ? launch_block8_append_t<kFmtInt8>(c, k_new, v_new, indptr, total_new, err, s)
+                         : launch_block8_append_t<kFmtE4m3>(c, k_new, v_new, indptr, total_new, err, s);
+}
+
+// Warps of the attention grid for a batch of at most T_max items.
+static int attn_warps(long long t_max) {
+  const long long w = std::max(1LL, std::min<long long>(kAttnWarps, t_max / kMinShare));
+  return static_cast<int>((w + kWarps - 1) / kWarps * kWarps);
+}
+
+static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, int G) {
+  const long long units = (static_cast<long long>(total_q) * G + kCols - 1) / kCols + num_seqs;
+  return units * H * std::max(1, (max_seq_len + kPage - 1) / kPage);
+}
+
+size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_seq_len, int H, int G) {
+  const size_t n = 2u * attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G));
+  return (n * kCols * kRecordFloats * sizeof(float) + 255) / 256 * 256;
+}
+
+template <int F>
+static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, int ctas,
+                                        const Outputs &out, float *partials, int32_t *err,
+                                        cudaStream_t s) {
+  static PerDevice grids;
+  int most = 0;
+  cudaError_t e = once_per_device(grids, [](int dev, int *g) {
+    cudaError_t r = cudaFuncSetAttribute(block8_attn_kernel<F>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCta8Smem);
+    int sms = 0, per_sm = 0;
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (r == cudaSuccess)
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block8_attn_kernel<F>, kWarps * 32,
+                                                        kCta8Smem);
+    *g = sms * (per_sm > 0 ? per_sm : 1);
+    return r;
+  }, &most);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(ctas, most);
+  block8_attn_kernel<F><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, err);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // units of the largest sequence spread over blockIdx.y (a decode step: one CTA per 8 heads)
+  const int rows_y = qs.indptr == nullptr ? (c.num_kv_heads * kCols + 15) / 16
+                                         : std::min(64, (c.num_kv_heads * kCols * 4 + 15) / 16);
+  block8_merge_kernel<<<dim3(c.num_seqs, rows_y), kWarps * 32, 0, s>>>(c, qs, out, partials,
+                                                                       grid * kWarps);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t *q,
+                                    const int32_t *q_indptr, int total_q, int max_q_len,
+                                    int max_seq_len, const Outputs &out, void *workspace,
+                                    int32_t *err, cudaStream_t s) {
+  const int ctas = attn_warps(items_bound(c.num_seqs, total_q, max_seq_len, c.num_kv_heads, c.gqa)) / kWarps;
+  float *partials = static_cast<float *>(workspace);
+  const Queries qs{q, q_indptr, total_q, max_q_len};
+  return fmt == kFmtInt8 ? launch_block8_attn_t<kFmtInt8>(c, qs, ctas, out, partials, err, s)
+                         : launch_block8_attn_t<kFmtE4m3>(c, qs, ctas, out, partials, err, s);
+}
+
+}  // namespace kv4

@@ -147,4 +147,26 @@ cudaError_t launch_baseline_append(int fmt, const CacheView &c, const uint16_t *
 cudaError_t launch_baseline_attention(int fmt, const CacheView &c, const Workspace &w,
                                       const uint16_t *q, int32_t *err_flag, cudaStream_t s);
 
+// 8-bit block-scaled cache (kv4_block8.cu): fmt is a kv4_block8_format. The view's k_codes /
+// v_codes hold the pages, k_params / v_params the block scales [num_pages][Hkv].
+cudaError_t launch_block8_append(int fmt, const CacheView &c, const uint16_t *k_new,
+                                 const uint16_t *v_new, const int32_t *indptr, int32_t total_new,
+                                 int32_t *err, cudaStream_t s);
+size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_seq_len, int H, int G);
+cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t *q,
+                                    const int32_t *q_indptr, int total_q, int max_q_len,
+                                    int max_seq_len, const Outputs &out, void *workspace,
+                                    int32_t *err, cudaStream_t s);
+
+// Eviction (kv4_evict.cu).
+cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
+                           const float *acc_in, float *acc_out, int acc_stride, int32_t *err,
+                           cudaStream_t s);
+cudaError_t launch_select(const CacheView &c, const float *acc, int acc_stride, int budget,
+                          int32_t *keep, int32_t *new_lens, int32_t *err, cudaStream_t s);
+cudaError_t launch_compact(const CacheView &c, const int32_t *keep, int budget,
+                           const int32_t *new_lens, const int32_t *dst_table, int dst_max_pages,
+                           const int32_t *dst_ring, const float *acc_in, int in_stride,
+                           float *acc_out, int out_stride, int32_t *err, cudaStream_t s);
+
 }  // namespace kv4

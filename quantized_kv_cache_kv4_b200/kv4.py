@@ -22,7 +22,7 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape",
           -3: "protected set larger than 144 positions", -4: "workspace too small",
           -5: "CUDA error"}
 DEVERR = {1: "page id", 2: "seq len", 4: "side index", 8: "q range", 16: "workspace",
-          32: "timeout"}
+          32: "timeout", 64: "keep index"}
 MAX_PROTECTED = 144
 HEAD_DIM = 128
 PAGE = 16
@@ -33,10 +33,14 @@ EXPORTS = ("kv4_workspace_size", "kv4_chunk_pages_for", "kv4_quantize_append",
            "kv4_status_string", "kv4_version",
            "kv4_decode_attention_noalloc", "kv4_noalloc_scratch_bytes",
            "kv4_baseline_append", "kv4_baseline_workspace_size",
-           "kv4_baseline_decode_attention", "kv4_test_withhold_copy")
+           "kv4_baseline_decode_attention", "kv4_test_withhold_copy",
+           "kv4_block8_append", "kv4_block8_workspace_size", "kv4_block8_attention",
+           "kv4_attention_weights", "kv4_evict_select", "kv4_evict_compact")
 
 BASELINE_BF16 = 1  # kv4_baseline_format
 BASELINE_KV8 = 2
+BLOCK8_INT8 = 1  # kv4_block8_format
+BLOCK8_E4M3 = 2
 
 
 class Config(ctypes.Structure):
@@ -118,6 +122,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                   ctypes.POINTER(PagedPool),
                                                   ctypes.POINTER(Batch), P, P, P, P, P,
                                                   ctypes.c_size_t, P, P]
+    I = ctypes.c_int32
+    lib.kv4_block8_append.restype = ctypes.c_int
+    lib.kv4_block8_append.argtypes = [I, ctypes.POINTER(Config), ctypes.POINTER(PagedPool),
+                                      ctypes.POINTER(Batch), P, P, P, I, P, P]
+    lib.kv4_block8_workspace_size.restype = ctypes.c_size_t
+    lib.kv4_block8_workspace_size.argtypes = [ctypes.POINTER(Config), I, I, I, I]
+    lib.kv4_block8_attention.restype = ctypes.c_int
+    lib.kv4_block8_attention.argtypes = [I, ctypes.POINTER(Config), ctypes.POINTER(PagedPool),
+                                         ctypes.POINTER(Batch), P, P, I, I, P, P, P, P,
+                                         ctypes.c_size_t, P, P]
+    cache4 = [ctypes.POINTER(Config), ctypes.POINTER(Int4Pool), ctypes.POINTER(Int8Side),
+              ctypes.POINTER(Batch)]
+    lib.kv4_attention_weights.restype = ctypes.c_int
+    lib.kv4_attention_weights.argtypes = cache4 + [P, P, P, P, I, P, P]
+    lib.kv4_evict_select.restype = ctypes.c_int
+    lib.kv4_evict_select.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(Batch), P, I, I, P, P,
+                                     P, P]
+    lib.kv4_evict_compact.restype = ctypes.c_int
+    lib.kv4_evict_compact.argtypes = cache4 + [P, I, P, P, I, P, P, I, P, I, P, P]
     lib.kv4_test_withhold_copy.restype = None
     lib.kv4_test_withhold_copy.argtypes = [ctypes.c_int32, ctypes.c_uint32]
     lib.kv4_status_string.restype = ctypes.c_char_p
@@ -226,14 +249,15 @@ def allocate_cache(cfg: Config, num_pages: int, num_sink_sets: int, num_rings: i
 class BatchTensors:
     page_table: torch.Tensor  # int32 [B, max_pages]
     seq_lens: torch.Tensor    # int32 [B]
-    sink_idx: torch.Tensor    # int32 [B]
+    sink_idx: torch.Tensor | None  # int32 [B]; None where there are no sinks
     ring_idx: torch.Tensor | None
     max_seq_len: int
     plan_reuse: bool = False  # use the work list the last call on the workspace left
 
     def struct(self) -> Batch:
         return Batch(self.page_table.data_ptr(), self.page_table.shape[1],
-                     self.seq_lens.data_ptr(), self.sink_idx.data_ptr(),
+                     self.seq_lens.data_ptr(),
+                     0 if self.sink_idx is None else self.sink_idx.data_ptr(),
                      0 if self.ring_idx is None else self.ring_idx.data_ptr(),
                      self.seq_lens.shape[0], int(self.max_seq_len), int(self.plan_reuse))
 
@@ -394,3 +418,192 @@ def baseline_decode_attention(cache: BaselineCache, batch: BatchTensors, q: torc
                                             _ptr(out), _ptr(out_f32), _ptr(lse), _ptr(workspace),
                                             workspace.numel(), _ptr(err), _stream(stream))
     _check(st, "kv4_baseline_decode_attention")
+
+
+# ----------------------------------------------------------------------------
+# 8-bit block-scaled cache
+# ----------------------------------------------------------------------------
+
+def _tensor(t, what, dtype, shape=None, optional=False):
+    """Device pointer of an argument whose type (one, or a tuple) and shape are checked (None
+    in a shape: any size)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: a tensor is wanted, not {type(t).__name__}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{what}: {dtype} is wanted, not {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{what}: shape {tuple(shape)} is wanted, not {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _on_device(fn, stream, *tensors):
+    """Calls fn(stream handle) with the tensors' device current: a launch goes to the current
+    device, whichever the caller left current."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"kv4 arguments on different devices: {dev} and {t.device}")
+    if dev is None or dev.index == torch.cuda.current_device():
+        return fn(_stream(stream))
+    with torch.cuda.device(dev):
+        return fn(_stream(stream))
+
+
+@dataclasses.dataclass
+class Block8Cache:
+    """Device storage of one layer's 8-bit block-scaled cache (layout in kv4.h): codes
+    [pages, Hkv, 8 strips, 16 slots, 16] as int8 (BLOCK8_INT8) or float8_e4m3fn
+    (BLOCK8_E4M3), scales float16 [pages, Hkv]."""
+
+    fmt: int
+    cfg: Config
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+
+    @property
+    def num_pages(self):
+        return self.k.shape[0]
+
+    def pool_struct(self) -> PagedPool:
+        if self.fmt not in _BLOCK8_DTYPES:
+            raise ValueError(f"unknown block8 format {self.fmt}")
+        pages, H = self.k.shape[0], self.cfg.num_kv_heads
+        code, shape = _BLOCK8_DTYPES[self.fmt], (pages, H, 8, PAGE, 16)
+        return PagedPool(_tensor(self.k, "k", code, shape), _tensor(self.v, "v", code, shape),
+                         _tensor(self.k_scales, "k_scales", torch.float16, (pages, H)),
+                         _tensor(self.v_scales, "v_scales", torch.float16, (pages, H)), pages)
+
+
+_BLOCK8_DTYPES = {BLOCK8_INT8: torch.int8, BLOCK8_E4M3: torch.float8_e4m3fn}
+
+
+def allocate_block8_cache(fmt: int, cfg: Config, num_pages: int, device="cuda") -> Block8Cache:
+    """Zero-initialised block-scaled page pool."""
+    if fmt not in _BLOCK8_DTYPES:
+        raise ValueError(f"unknown block8 format {fmt}")
+    H = cfg.num_kv_heads
+    codes = lambda: torch.zeros((num_pages, H, 8, PAGE, 16), dtype=torch.int8,
+                                device=device).view(_BLOCK8_DTYPES[fmt])
+    scales = lambda: torch.zeros((num_pages, H), dtype=torch.float16, device=device)
+    return Block8Cache(fmt, cfg, codes(), codes(), scales(), scales())
+
+
+def block8_append(cache: Block8Cache, batch: BatchTensors, k_new: torch.Tensor,
+                  v_new: torch.Tensor, new_indptr: torch.Tensor | None = None,
+                  err: torch.Tensor | None = None, stream=None):
+    """k_new, v_new: bf16 [rows, Hkv, 128]; new_indptr int32 [B+1] or None (one row per seq)."""
+    rows = (None, cache.cfg.num_kv_heads, HEAD_DIM)
+    k = _tensor(k_new, "k_new", torch.bfloat16, rows)
+    v = _tensor(v_new, "v_new", torch.bfloat16, k_new.shape)
+    B = batch.seq_lens.shape[0]
+    ip = _tensor(new_indptr, "new_indptr", torch.int32, (B + 1,), optional=True)
+    pool, bs = cache.pool_struct(), batch.struct()
+    st = _on_device(lambda s: _lib.kv4_block8_append(
+        cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(pool), ctypes.byref(bs), k, v, ip,
+        k_new.shape[0], _ptr(err), s), stream, cache.k, batch.seq_lens, k_new, v_new, new_indptr)
+    _check(st, "kv4_block8_append")
+
+
+def block8_workspace_size(cfg: Config, num_seqs: int, total_q: int, max_q_len: int,
+                          max_seq_len: int) -> int:
+    n = _lib.kv4_block8_workspace_size(ctypes.byref(cfg), num_seqs, total_q, max_q_len, max_seq_len)
+    if n == 0:
+        raise KV4Error("kv4_block8_workspace_size: invalid arguments")
+    return n
+
+
+def block8_attention(cache: Block8Cache, batch: BatchTensors, q: torch.Tensor, out: torch.Tensor,
+                     workspace: torch.Tensor, q_indptr: torch.Tensor | None = None,
+                     max_q_len: int = 1, out_f32: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                     stream=None):
+    """q, out: bf16 [rows, Hq, 128]; q_indptr int32 [B+1]: sequence b's rows are its last
+    positions, at most max_q_len of them, causal (None: one per sequence); out_f32 fp32 like
+    out; lse fp32 [rows, Hq]; workspace: uint8, block8_workspace_size(...) bytes."""
+    n, Hq = q.shape[0], cache.cfg.num_q_heads
+    B = batch.seq_lens.shape[0]
+    args = (_tensor(q, "q", torch.bfloat16, (None, Hq, HEAD_DIM)),
+            _tensor(q_indptr, "q_indptr", torch.int32, (B + 1,), optional=True), n, max_q_len,
+            _tensor(out, "out", torch.bfloat16, q.shape),
+            _tensor(out_f32, "out_f32", torch.float32, q.shape, optional=True),
+            _tensor(lse, "lse", torch.float32, (n, Hq), optional=True),
+            _tensor(workspace, "workspace", torch.uint8, (None,)), workspace.numel(), _ptr(err))
+    pool, bs = cache.pool_struct(), batch.struct()
+    st = _on_device(lambda s: _lib.kv4_block8_attention(
+        cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(pool), ctypes.byref(bs), *args, s), stream,
+        cache.k, batch.seq_lens, q, out, q_indptr, workspace)
+    _check(st, "kv4_block8_attention")
+
+
+# ----------------------------------------------------------------------------
+# eviction by accumulated attention weight
+# ----------------------------------------------------------------------------
+
+def attention_weights(cache: Cache, batch: BatchTensors, q: torch.Tensor, lse: torch.Tensor,
+                      acc_out: torch.Tensor, acc_in: torch.Tensor | None = None,
+                      err: torch.Tensor | None = None, stream=None):
+    """acc_out = acc_in + each position's attention weight in this decode step. q bf16
+    [B, Hq, 128]; lse fp32 [B, Hq] as decode_attention wrote it; acc_in, acc_out fp32
+    [B, Hkv, positions] (may be the same; None: zeros)."""
+    B, cfg = batch.seq_lens.shape[0], cache.cfg
+    total = (B, cfg.num_kv_heads, None)
+    args = (_tensor(q, "q", torch.bfloat16, (B, cfg.num_q_heads, HEAD_DIM)),
+            _tensor(lse, "lse", torch.float32, (B, cfg.num_q_heads)),
+            _tensor(acc_in, "acc_in", torch.float32, acc_out.shape, optional=True),
+            _tensor(acc_out, "acc_out", torch.float32, total), acc_out.shape[2], _ptr(err))
+    pool, side, bs = cache.pool_struct(), cache.side_struct(), batch.struct()
+    st = _on_device(lambda s: _lib.kv4_attention_weights(
+        ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(side), ctypes.byref(bs), *args, s),
+        stream, cache.k_codes, batch.seq_lens, q, lse, acc_in, acc_out)
+    _check(st, "kv4_attention_weights")
+
+
+def evict_select(cfg: Config, batch: BatchTensors, acc: torch.Tensor, keep: torch.Tensor,
+                 new_lens: torch.Tensor, err: torch.Tensor | None = None, stream=None):
+    """The positions to keep: acc fp32 [B, Hkv, positions]; keep int32 [B, Hkv, budget]
+    (ascending, -1 behind the last) and new_lens int32 [B] are written."""
+    B, H = batch.seq_lens.shape[0], cfg.num_kv_heads
+    args = (_tensor(acc, "acc", torch.float32, (B, H, None)), acc.shape[2], keep.shape[-1],
+            _tensor(keep, "keep", torch.int32, (B, H, None)),
+            _tensor(new_lens, "new_lens", torch.int32, (B,)), _ptr(err))
+    if keep.shape[-1] > 0 and new_lens.data_ptr() == batch.seq_lens.data_ptr() and B:
+        raise ValueError("new_lens must not be the batch's seq_lens")
+    bs = batch.struct()
+    st = _on_device(lambda s: _lib.kv4_evict_select(ctypes.byref(cfg), ctypes.byref(bs), *args, s),
+                    stream, acc, batch.seq_lens, keep, new_lens)
+    _check(st, "kv4_evict_select")
+
+
+def evict_compact(cache: Cache, batch: BatchTensors, keep: torch.Tensor, new_lens: torch.Tensor,
+                  dst_page_table: torch.Tensor | None = None,
+                  dst_ring_idx: torch.Tensor | None = None, acc_in: torch.Tensor | None = None,
+                  acc_out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                  stream=None):
+    """Moves the kept rows (keep, new_lens as evict_select wrote them) to the front of the pages
+    of dst_page_table int32 [B, pages] (None: the sequence's own), the recent window's INT8
+    copies to ring dst_ring_idx int32 [B] (None: its own), and the totals to acc_out."""
+    B, cfg = batch.seq_lens.shape[0], cache.cfg
+    H = cfg.num_kv_heads
+    args = (_tensor(keep, "keep", torch.int32, (B, H, None)), keep.shape[2],
+            _tensor(new_lens, "new_lens", torch.int32, (B,)),
+            _tensor(dst_page_table, "dst_page_table", torch.int32, (B, None), optional=True),
+            0 if dst_page_table is None else dst_page_table.shape[1],
+            _tensor(dst_ring_idx, "dst_ring_idx", torch.int32, (B,), optional=True),
+            _tensor(acc_in, "acc_in", torch.float32, (B, H, None), optional=True),
+            0 if acc_in is None else acc_in.shape[2],
+            _tensor(acc_out, "acc_out", torch.float32, (B, H, None), optional=True),
+            0 if acc_out is None else acc_out.shape[2], _ptr(err))
+    pool, side, bs = cache.pool_struct(), cache.side_struct(), batch.struct()
+    st = _on_device(lambda s: _lib.kv4_evict_compact(
+        ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(side), ctypes.byref(bs), *args, s),
+        stream, cache.k_codes, batch.seq_lens, keep, new_lens, dst_page_table, dst_ring_idx,
+        acc_in, acc_out)
+    _check(st, "kv4_evict_compact")

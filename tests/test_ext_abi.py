@@ -1,0 +1,144 @@
+"""Host-side checks of the block-scaled cache's and the eviction's entry points: refused calls
+return before anything is launched, so these run without a GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+
+
+@pytest.fixture(scope="module")
+def kv4():
+    from quantized_kv_cache_kv4_b200 import build
+    build.build()
+    from quantized_kv_cache_kv4_b200 import kv4 as m
+    return m
+
+
+FAKE = 0x10000  # an aligned address nothing reads: every call here is refused
+
+
+def structs(kv4, **kw):
+    cfg = kv4.make_config(kw.pop("hq", 8), kw.pop("hkv", 2), kw.pop("S", 4), kw.pop("R", 32))
+    pool = kv4.PagedPool(FAKE, FAKE, FAKE, FAKE, 10)
+    int4 = kv4.Int4Pool(FAKE, FAKE, FAKE, FAKE, 10)
+    side = kv4.Int8Side(FAKE, FAKE, FAKE, FAKE, 2, FAKE, FAKE, FAKE, FAKE, 2)
+    batch = kv4.Batch(FAKE, 4, FAKE, FAKE, FAKE, kw.pop("B", 2), kw.pop("max_len", 64), 0)
+    assert not kw
+    return cfg, pool, int4, side, batch
+
+
+def test_block8_append_refusals(kv4):
+    cfg, pool, _, _, batch = structs(kv4)
+    r = ctypes.byref
+
+    def call(fmt=1, c=cfg, p=pool, b=batch, k=FAKE, v=FAKE, ip=None, n=2):
+        return kv4._lib.kv4_block8_append(fmt, r(c) if c else None, r(p) if p else None, r(b) if b else None,
+                                          k, v, ip, n, None, None)
+
+    for bad in (dict(fmt=0), dict(fmt=3), dict(c=None), dict(p=None), dict(b=None), dict(k=None), dict(v=None),
+                dict(k=FAKE + 2), dict(n=-1), dict(n=3)):
+        assert call(**bad) == -1, bad
+    for field in ("k", "v", "k_scales", "v_scales"):
+        for value in (0, FAKE + 8):
+            broken = kv4.PagedPool(FAKE, FAKE, FAKE, FAKE, 10)
+            setattr(broken, field, value)
+            assert call(p=broken) == -1, (field, value)
+    shape = kv4.make_config(8, 3, 0, 0)
+    assert call(c=shape) == -2
+    wide = kv4.make_config(18, 2, 0, 0)
+    assert call(c=wide) == -2
+    assert call(ip=FAKE, n=0) == 0  # nothing to do
+    empty = kv4.Batch(FAKE, 4, FAKE, FAKE, FAKE, 0, 64, 0)
+    assert call(b=empty, n=0) == 0
+
+
+def test_block8_attention_refusals(kv4):
+    cfg, pool, _, _, batch = structs(kv4)
+    r = ctypes.byref
+    size = kv4.block8_workspace_size(cfg, 2, 2, 1, 64)
+
+    def call(fmt=1, c=cfg, p=pool, b=batch, q=FAKE, ip=None, n=2, m=1, out=FAKE, f=None, ws=FAKE, bytes_=size):
+        return kv4._lib.kv4_block8_attention(fmt, r(c), r(p), r(b), q, ip, n, m, out, f, None, ws, bytes_, None,
+                                             None)
+
+    for bad in (dict(fmt=7), dict(q=None), dict(out=None), dict(ws=None), dict(ws=FAKE + 16), dict(q=FAKE + 4),
+                dict(out=FAKE + 4), dict(f=FAKE + 4), dict(n=-1), dict(m=-1), dict(n=3), dict(m=2)):
+        assert call(**bad) == -1, bad
+    assert call(bytes_=size - 1) == -4
+    assert call(ip=FAKE, n=0) == 0 and call(ip=FAKE, n=2, m=0) == 0
+
+
+def test_block8_workspace_grows_with_the_batch(kv4):
+    rng = np.random.default_rng(1)
+    for hq, hkv in ((32, 8), (8, 2), (4, 4), (16, 2), (9, 3)):
+        cfg = kv4.make_config(hq, hkv, 0, 0)
+        for _ in range(300):
+            big = [int(2 ** x) for x in rng.uniform(0, [11, 13, 13, 15])]
+            small = [int(rng.integers(0, x + 1)) for x in big]
+            assert kv4.block8_workspace_size(cfg, *small) <= kv4.block8_workspace_size(cfg, *big), (small, big)
+    for bad in ((-1, 1, 1, 1), (1, -1, 1, 1), (1, 1, -1, 1), (1, 1, 1, -1)):
+        with pytest.raises(kv4.KV4Error):
+            kv4.block8_workspace_size(cfg, *bad)
+    assert kv4.block8_workspace_size(cfg, 1024, 1024, 1, 1 << 20) < 64 << 20
+
+
+def test_weights_refusals(kv4):
+    cfg, _, pool, side, batch = structs(kv4)
+    r = ctypes.byref
+
+    def call(c=cfg, p=pool, q=FAKE, lse=FAKE, out=FAKE, stride=64):
+        return kv4._lib.kv4_attention_weights(r(c), r(p) if p else None, r(side), r(batch), q, lse, None, out,
+                                              stride, None, None)
+
+    for bad in (dict(p=None), dict(q=None), dict(lse=None), dict(out=None), dict(q=FAKE + 8), dict(stride=-1)):
+        assert call(**bad) == -1, bad
+    assert call(c=kv4.make_config(8, 2, 100, 45)) == -3
+
+
+def test_select_refusals(kv4):
+    cfg, _, _, _, batch = structs(kv4)
+    r = ctypes.byref
+
+    def call(c=cfg, b=batch, acc=FAKE, stride=64, budget=40, keep=FAKE, new=FAKE):
+        return kv4._lib.kv4_evict_select(r(c), r(b) if b else None, acc, stride, budget, keep, new, None, None)
+
+    for bad in (dict(b=None), dict(acc=None), dict(stride=-1), dict(budget=35), dict(budget=0), dict(keep=None),
+                dict(new=None)):
+        assert call(**bad) == -1, bad
+    none = kv4.make_config(8, 2, 0, 0)
+    assert call(c=none, budget=0) == -1
+
+
+def test_compact_refusals(kv4):
+    cfg, _, pool, side, batch = structs(kv4)
+    r = ctypes.byref
+    other = FAKE + 0x1000
+
+    def call(keep=FAKE, budget=40, new=other, to=None, pages=0, a=None, sa=0, z=None, sz=0):
+        return kv4._lib.kv4_evict_compact(r(cfg), r(pool), r(side), r(batch), keep, budget, new, to, pages, None,
+                                          a, sa, z, sz, None, None)
+
+    for bad in (dict(keep=None), dict(budget=0), dict(new=None), dict(new=FAKE), dict(to=FAKE, pages=0),
+                dict(a=FAKE), dict(z=FAKE), dict(a=FAKE, z=FAKE, sa=5, sz=6), dict(a=FAKE, z=other, sa=-1, sz=6),
+                dict(a=FAKE, z=FAKE, sa=5, sz=5, to=other, pages=3)):
+        assert call(**bad) == -1, bad
+
+
+def test_binding_refuses_wrong_types_and_shapes(kv4):
+    """Types and shapes are refused by the binding before it takes a pointer; so are tensors
+    that are not on a GPU."""
+    import torch
+    t = torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        kv4._tensor(t, "x", torch.float32)
+    with pytest.raises(ValueError):
+        kv4._tensor(t, "x", torch.bfloat16, (2, 3, 128))
+    with pytest.raises(ValueError):
+        kv4._tensor(t, "x", torch.bfloat16, (2, 2))
+    with pytest.raises(ValueError):
+        kv4._tensor(t, "x", torch.bfloat16, (2, 2, None))  # host memory
+    with pytest.raises(ValueError):
+        kv4._tensor(None, "x", torch.bfloat16)
+    assert kv4._tensor(None, "x", torch.bfloat16, optional=True) is None
+    with pytest.raises(ValueError):
+        kv4.allocate_block8_cache(5, kv4.make_config(8, 2, 0, 0), 4, device="cpu")
