@@ -12,9 +12,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkv4.so")
 SOURCES = ["kv4_api.cu", "kv4_append.cu", "kv4_attention.cu", "kv4_baseline.cu", "kv4_noalloc.cu",
-           "kv4_block8.cu", "kv4_evict.cu"]
+           "kv4_block8.cu", "kv4_block8_tile.cu", "kv4_evict.cu"]
 HEADERS = ["kv4_device.cuh", "kv4_internal.h", "kv4_attn_common.cuh", "kv4_plan.cuh",
-           "kv4_split.cuh"]
+           "kv4_split.cuh", "kv4_block8.cuh"]
 
 
 def nvcc() -> str:

@@ -11,23 +11,11 @@
 // code (127, or 448 for e4m3), rounded UP to fp16, so that no code saturates (rounding to
 // nearest would lose up to half the range where fp16 is subnormal). A row that raises it
 // has the codes already in the block rounded again: code' = rne(code * s_old / s).
-#include <cuda_fp8.h>
-
 #include <algorithm>
 
-#include "kv4_attn_common.cuh"
-#include "kv4_split.cuh"
+#include "kv4_block8.cuh"
 
 namespace kv4 {
-
-constexpr int kFmtInt8 = KV4_BLOCK8_INT8;
-constexpr int kFmtE4m3 = KV4_BLOCK8_E4M3;
-
-template <int F>
-struct Fmt8 {
-  static constexpr float kMax = F == KV4_BLOCK8_INT8 ? 127.0f : 448.0f;
-  static constexpr float kRcp = 1.0f / (F == KV4_BLOCK8_INT8 ? 127.0f : 448.0f);
-};
 
 // ---------------------------------------------------------------------------
 // append
@@ -74,13 +62,6 @@ __device__ __forceinline__ void values4(uint32_t w, float s, float (&x)[4]) {
         __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)));
     x[0] = a.x * s; x[1] = a.y * s; x[2] = b.x * s; x[3] = b.y * s;
   }
-}
-
-__device__ __forceinline__ void unpack_bf16x4(uint2 raw, float (&x)[4]) {
-  x[0] = __uint_as_float(raw.x << 16);
-  x[1] = __uint_as_float(raw.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(raw.y << 16);
-  x[3] = __uint_as_float(raw.y & 0xFFFF0000u);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -236,78 +217,25 @@ __global__ void __launch_bounds__(256) block8_append_rows_kernel(
 // order. A warp has at most two such units: its first (record 2w) and its last (2w + 1).
 constexpr int kAttnCtas = 148 * 3;            // resident CTAs of the largest grid
 constexpr int kAttnWarps = kAttnCtas * kWarps;
+constexpr int kMinShare = 4;                  // pages per warp, at least
 constexpr int kCols = 8;                      // query rows of a unit (MMA N)
 
-struct Seq8 {
-  int L, n, row0;  // length, queries, first query row
-  int pages;       // pages a unit of it takes (1 for an empty sequence: it writes zeros)
-  int units;       // per kv head
-};
-
-// The queries of a call: CSR rows (indptr nullptr: one per sequence), at most max_n of one
-// sequence.
-struct Queries {
-  const uint16_t *q;
-  const int32_t *indptr;
-  int32_t total, max_n;
+struct Seq8 : SeqRows {
+  int pages;  // pages a unit of it takes (1 for an empty sequence: it writes zeros)
+  int units;  // per kv head
 };
 
 __device__ __forceinline__ Seq8 seq_of(const CacheView &c, const Queries &qs, int b, int32_t *err) {
   Seq8 s;
-  s.L = c.seq_lens[b];
-  if (s.L < 0 || s.L > c.max_pages * kPage) {
-    set_err(err, KV4_DEVERR_SEQ_LEN);
-    s.L = 0;
-  }
-  s.row0 = b;
-  s.n = 1;
-  if (qs.indptr != nullptr) {
-    s.row0 = qs.indptr[b];
-    const int end = qs.indptr[b + 1];
-    s.n = end - s.row0;
-    if (s.row0 < 0 || end < s.row0 || end > qs.total || s.n > qs.max_n) {
-      set_err(err, KV4_DEVERR_SEQ_LEN);
-      s.n = 0;
-    }
-  }
+  static_cast<SeqRows &>(s) = rows_of(c, qs, b, err);
   s.pages = max(1, (s.L + kPage - 1) / kPage);
   s.units = (s.n * c.gqa + kCols - 1) / kCols;
   return s;
 }
 
-// Sum over a block of up to 128 threads' values; every thread gets it.
-__device__ __forceinline__ long long block_sum(long long v, long long *scratch) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long t = 0;
-  for (int i = 0; i < (blockDim.x >> 5); ++i) t += scratch[i];
-  __syncthreads();
-  return t;
-}
-
 // ---------------------------------------------------------------------------
 // attention: codes to tensor-core operands
 // ---------------------------------------------------------------------------
-// A 32-bit word of four codes (bytes 0..3) as two fp16 pairs: (0, 1), (2, 3) for K and
-// (0, 2), (1, 3) for V, whose transposed ldmatrix words hold two dims of two tokens.
-// Both formats are exact in fp16.
-template <int F, bool V>
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &a, uint32_t &b) {
-  if constexpr (F == kFmtInt8) {
-    const uint32_t u = w ^ 0x80808080u;
-    a = V ? s8_pair<0x4240>(u) : s8_pair<0x4140>(u);
-    b = V ? s8_pair<0x4341>(u) : s8_pair<0x4342>(u);
-  } else {
-    const uint32_t u = V ? prmt(w, 0u, 0x3120) : w;
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u & 0xFFFFu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16), __NV_E4M3);
-    a = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
-    b = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
-  }
-}
-
 // 8 x 8 fp16 matrix held as MMA fragments, transposed in registers.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -341,7 +269,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
   }
   auto items = [&](const Seq8 &s) { return static_cast<long long>(s.units) * s.pages * H; };
   const int me = blockIdx.x * kWarps + warp;
-  const Share share = take_share(B, me, gridDim.x * kWarps, split, [&](int i, bool check) {
+  const Share share = take_share(B, me, gridDim.x * kWarps, kMinShare, split, [&](int i, bool check) {
     return items(seq_of(c, qs, i, check && blockIdx.x == 0 ? err : nullptr));
   });
   const long long t_begin = share.begin, t_end = share.end;
@@ -569,58 +497,35 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
   }
 }
 
-// One CTA row per sequence (blockIdx.x), its units spread over blockIdx.y and the warps:
-// the units that several warps shared are joined in warp order; each column by a warp.
-__global__ void __launch_bounds__(kWarps * 32) block8_merge_kernel(
-    CacheView c, Queries qs, Outputs out, const float *__restrict__ partials, int attn_warps) {
-  __shared__ long long scratch[kWarps];
+// Where warp blockIdx.x + 1's share starts inside a unit that starts in the share before it,
+// the block joins that unit's records (a unit over more warps is the first such warp's to join).
+__global__ void __launch_bounds__(kSplitThreads) block8_merge_kernel(CacheView c, Queries qs, Outputs out,
+                                                                     const float *__restrict__ partials,
+                                                                     int attn_warps) {
+  __shared__ SplitSmem split;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = c.gqa, H = c.num_kv_heads, B = c.num_seqs, b = blockIdx.x;
-  long long before = 0, all = 0;
-  for (int i = threadIdx.x; i < B; i += blockDim.x) {
+  const int G = c.gqa, H = c.num_kv_heads, me = blockIdx.x + 1;
+  long long T;
+  const Share share = take_share(c.num_seqs, me, attn_warps, kMinShare, split, [&](int i, bool) {
     const Seq8 s = seq_of(c, qs, i, nullptr);
-    const long long n = static_cast<long long>(s.units) * s.pages * H;
-    all += n;
-    if (i < b) before += n;
-  }
-  const long long T = block_sum(all, scratch);
-  const long long first = block_sum(before, scratch);
-  if (T == 0) return;
-  const Shares sh(T, attn_warps);
-  const Seq8 sq = seq_of(c, qs, b, nullptr);
-  const int rows = sq.n * G;
-  const int n_tasks = sq.units * H * kCols;  // (unit, column)
-  for (int task = blockIdx.y * kWarps + warp; task < n_tasks; task += gridDim.y * kWarps) {
-    const int unit = task / kCols, col = task % kCols;
-    const int h = unit / sq.units, u = unit - h * sq.units;
-    const int rc = u * kCols + col;
-    if (rc >= rows) continue;
-    const long long t0 = first + static_cast<long long>(unit) * sq.pages;
-    const int w0 = sh.owner(t0), w1 = sh.owner(t0 + sq.pages - 1);
-    if (w0 == w1) continue;  // finished by its warp
-    float mm = kNegBig, ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = w0; w <= w1; ++w) {
-      const int slot = sh.begin(w) >= t0 ? 0 : 1;
-      const float *rec = partials + (static_cast<size_t>(2 * w + slot) * kCols + col) * kRecordFloats;
-      const float2 ml = *reinterpret_cast<const float2 *>(rec + kHeadDim);
-      if (ml.y <= 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4 *>(rec + 4 * lane);
-      const float mn = fmaxf(mm, ml.x);
-      const float a = fast_exp2(mm - mn), e = fast_exp2(ml.x - mn);
-      ll = ll * a + ml.y * e;
-      acc.x = acc.x * a + v.x * e; acc.y = acc.y * a + v.y * e;
-      acc.z = acc.z * a + v.z * e; acc.w = acc.w * a + v.w * e;
-      mm = mn;
-    }
-    const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
-    const float inv = ll > 0.f ? 1.0f / ll : 0.f;
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    uint2 packed = make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-    *reinterpret_cast<uint2 *>(out.out + qr * kHeadDim + 4 * lane) = packed;
-    if (out.out_f32) *reinterpret_cast<float4 *>(out.out_f32 + qr * kHeadDim + 4 * lane) = acc;
-    if (out.lse && lane == 0) out.lse[qr] = ll > 0.f ? mm * kLn2 + logf(ll) : -CUDART_INF_F;
+    return static_cast<long long>(s.units) * s.pages * H;
+  }, &T);
+  if (share.begin >= share.end) return;
+  const Seq8 sq = seq_of(c, qs, share.b, nullptr);
+  const long long in_seq = share.begin - share.seq_first;
+  const int unit = static_cast<int>(in_seq / sq.pages);
+  const int pg0 = static_cast<int>(in_seq - static_cast<long long>(unit) * sq.pages);
+  if (pg0 == 0) return;
+  const Shares sh(T, attn_warps, kMinShare);
+  const long long t0 = share.begin - pg0;
+  if (sh.owner(t0) != me - 1) return;
+  const int w1 = sh.owner(t0 + sq.pages - 1);
+  const int h = unit / sq.units, u = unit - h * sq.units;
+  for (int col = warp; col < kCols && u * kCols + col < sq.n * G; col += kSplitThreads / 32) {
+    const int r = u * kCols + col;
+    const size_t qr = static_cast<size_t>(sq.row0 + r / G) * H * G + h * G + r % G;
+    join_records(partials, kCols, col, me - 1, w1, [&](int w) { return sh.begin(w) >= t0 ? 0 : 1; }, out, qr,
+                 lane);
   }
 }
 
@@ -662,7 +567,9 @@ static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, 
 
 size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_seq_len, int H, int G) {
   const size_t n = 2u * attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G));
-  return (n * kCols * kRecordFloats * sizeof(float) + 255) / 256 * 256;
+  const size_t bytes = (n * kCols * kRecordFloats * sizeof(float) + 255) / 256 * 256;
+  if (static_cast<long long>(max_q_len) * G <= kWarpRows) return bytes;
+  return std::max(bytes, tile_workspace_bytes(num_seqs, total_q, max_seq_len, H, G));
 }
 
 template <int F>
@@ -687,11 +594,7 @@ static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, i
   block8_attn_kernel<F><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, err);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // units of the largest sequence spread over blockIdx.y (a decode step: one CTA per 8 heads)
-  const int rows_y = qs.indptr == nullptr ? (c.num_kv_heads * kCols + 15) / 16
-                                         : std::min(64, (c.num_kv_heads * kCols * 4 + 15) / 16);
-  block8_merge_kernel<<<dim3(c.num_seqs, rows_y), kWarps * 32, 0, s>>>(c, qs, out, partials,
-                                                                       grid * kWarps);
+  block8_merge_kernel<<<grid * kWarps - 1, kSplitThreads, 0, s>>>(c, qs, out, partials, grid * kWarps);
   return cudaGetLastError();
 }
 
@@ -702,6 +605,8 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
   const int ctas = attn_warps(items_bound(c.num_seqs, total_q, max_seq_len, c.num_kv_heads, c.gqa)) / kWarps;
   float *partials = static_cast<float *>(workspace);
   const Queries qs{q, q_indptr, total_q, max_q_len};
+  if (static_cast<long long>(max_q_len) * c.gqa > kWarpRows)
+    return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, err, s);
   return fmt == kFmtInt8 ? launch_block8_attn_t<kFmtInt8>(c, qs, ctas, out, partials, err, s)
                          : launch_block8_attn_t<kFmtE4m3>(c, qs, ctas, out, partials, err, s);
 }

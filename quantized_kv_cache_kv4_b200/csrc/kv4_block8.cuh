@@ -1,0 +1,119 @@
+// Pieces shared by the kernels of the 8-bit block-scaled cache (kv4_block8.cu: append and
+// the attention of few query rows; kv4_block8_tile.cu: the attention of many).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "kv4_attn_common.cuh"
+#include "kv4_split.cuh"
+
+namespace kv4 {
+
+constexpr int kFmtInt8 = KV4_BLOCK8_INT8;
+constexpr int kFmtE4m3 = KV4_BLOCK8_E4M3;
+
+template <int F>
+struct Fmt8 {
+  static constexpr float kMax = F == KV4_BLOCK8_INT8 ? 127.0f : 448.0f;
+  static constexpr float kRcp = 1.0f / (F == KV4_BLOCK8_INT8 ? 127.0f : 448.0f);
+};
+
+__device__ __forceinline__ void unpack_bf16x4(uint2 raw, float (&x)[4]) {
+  x[0] = __uint_as_float(raw.x << 16);
+  x[1] = __uint_as_float(raw.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(raw.y << 16);
+  x[3] = __uint_as_float(raw.y & 0xFFFF0000u);
+}
+
+// The queries of a call: CSR rows (indptr nullptr: one per sequence), at most max_n of one
+// sequence.
+struct Queries {
+  const uint16_t *q;
+  const int32_t *indptr;
+  int32_t total, max_n;
+};
+
+// Length, queries and first query row of sequence b (wrong ones are flagged: a wrong length
+// counts as 0, wrong rows as none).
+struct SeqRows {
+  int L, n, row0;
+};
+__device__ __forceinline__ SeqRows rows_of(const CacheView &c, const Queries &qs, int b, int32_t *err) {
+  SeqRows s;
+  s.L = c.seq_lens[b];
+  if (s.L < 0 || s.L > c.max_pages * kPage) {
+    set_err(err, KV4_DEVERR_SEQ_LEN);
+    s.L = 0;
+  }
+  s.row0 = b;
+  s.n = 1;
+  if (qs.indptr != nullptr) {
+    s.row0 = qs.indptr[b];
+    const int end = qs.indptr[b + 1];
+    if (s.row0 < 0 || end < s.row0 || end > qs.total || end - s.row0 > qs.max_n) {
+      set_err(err, KV4_DEVERR_SEQ_LEN);
+      s.n = 0;
+    } else {
+      s.n = end - s.row0;
+    }
+  }
+  return s;
+}
+
+// A 32-bit word of four codes (bytes 0..3) as two fp16 pairs: (0, 1), (2, 3) for K and
+// (0, 2), (1, 3) for V, whose transposed ldmatrix words hold two dims of two tokens.
+// Both formats are exact in fp16.
+template <int F, bool V>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &a, uint32_t &b) {
+  if constexpr (F == kFmtInt8) {
+    const uint32_t u = w ^ 0x80808080u;
+    a = V ? s8_pair<0x4240>(u) : s8_pair<0x4140>(u);
+    b = V ? s8_pair<0x4341>(u) : s8_pair<0x4342>(u);
+  } else {
+    const uint32_t u = V ? prmt(w, 0u, 0x3120) : w;
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u & 0xFFFFu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16), __NV_E4M3);
+    a = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
+    b = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
+  }
+}
+
+// Joins the partial records (max in log2 units, sum, weighted values) of one row of a unit that
+// workers w0 .. w1 share, in that order, and writes the row. Records: [2 per worker][rows][132];
+// slot(w): which of worker w's two.
+template <class Slot>
+__device__ __forceinline__ void join_records(const float *__restrict__ partials, int rows, int x, int w0,
+                                             int w1, Slot slot, const Outputs &out, size_t qr, int lane) {
+  float mm = kNegBig, ll = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = w0; w <= w1; ++w) {
+    const float *rec = partials + ((2 * static_cast<size_t>(w) + slot(w)) * rows + x) * kRecordFloats;
+    const float2 ml = *reinterpret_cast<const float2 *>(rec + kHeadDim);
+    const float4 v = *reinterpret_cast<const float4 *>(rec + 4 * lane);
+    if (ml.y <= 0.f) continue;  // nothing visible there
+    const float mn = fmaxf(mm, ml.x);
+    const float a = fast_exp2(mm - mn), e = fast_exp2(ml.x - mn);
+    ll = ll * a + ml.y * e;
+    acc.x = acc.x * a + v.x * e; acc.y = acc.y * a + v.y * e;
+    acc.z = acc.z * a + v.z * e; acc.w = acc.w * a + v.w * e;
+    mm = mn;
+  }
+  const float inv = ll > 0.f ? 1.0f / ll : 0.f;
+  acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+  *reinterpret_cast<uint2 *>(out.out + qr * kHeadDim + 4 * lane) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+  if (out.out_f32) *reinterpret_cast<float4 *>(out.out_f32 + qr * kHeadDim + 4 * lane) = acc;
+  if (out.lse && lane == 0) out.lse[qr] = ll > 0.f ? mm * kLn2 + logf(ll) : -CUDART_INF_F;
+}
+
+// Launches of the many-rows attention (kv4_block8_tile.cu).
+size_t tile_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G);
+cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs, int max_seq_len,
+                                  const Outputs &out, void *workspace, int32_t *err, cudaStream_t s);
+
+// Up to this many query rows (positions x query heads of a kv head) of a sequence the warp
+// kernel takes the call, beyond it the tile kernel.
+constexpr int kWarpRows = 8;
+
+}  // namespace kv4

@@ -1,0 +1,684 @@
+// Attention over the 8-bit block-scaled cache for many query rows of a sequence: prefill
+// chunks and the verification of drafted tokens, on the tcgen05 tensor cores.
+//
+// Rows. Row r of a (sequence, kv head) is position i = r / G of its last n positions and query
+// head g = r % G, so a tile of 128 rows shares every K and V block it reads. Key tiles are 128
+// positions (8 pages).
+//
+// A CTA runs two pipelines of 128 rows each:
+//   softmax warps (4 + 4)  one thread per row: the row's logits from TMEM, the running maximum
+//                          and sum, the weights back to TMEM over the logits;
+//   MMA warps (1 + 1)      one thread issues S = Q K^T (both operands in shared memory) and
+//                          O += P V (P in TMEM); accumulators S and O in TMEM, 4 x 128 columns;
+//   convert warps (4)      load pages' codes and write them as fp16 (exact for both formats)
+//                          into the 128-byte-swizzled tiles the MMAs read.
+// SHARED: the pipelines hold rows 0-127 and 128-255 of one unit and read the same key tiles,
+// which are converted once (two stages). Otherwise each pipeline is a worker of its own, with
+// its own units, key tiles (one stage) and two of the convert warps: for sequences of at most
+// 128 rows, whose time is the reading of the cache.
+//
+// Scales. A key block's scale multiplies its 16 logits, a value block's scale its 16 weights:
+// P = p 2^7 vs / 2^vref with vref the exponent of the largest value scale so far, so P is at
+// most 2^15 (p up to 2^8: the maximum a row subtracts is moved only when it is outgrown by
+// that factor, which spares most rescales of O). fp16 keeps 11 significant bits of P down to
+// 2^-14, and 2^-25 below: about 2^-31 of the largest weight times the largest value scale.
+//
+// Split. The key tiles of all units, in order, are dealt to the workers in equal contiguous
+// shares; units that two or more workers share leave partial records (first and last unit of
+// a worker) for the merge.
+#include <algorithm>
+
+#include "kv4_block8.cuh"
+
+namespace kv4 {
+
+constexpr int kTile = 128;               // rows of a pipeline, positions of a key tile
+constexpr int kTilePages = kTile / kPage;
+constexpr int kOperandBytes = kTile * kHeadDim * 2;  // one fp16 operand tile: 32 KB
+constexpr int kTileThreads = 448;        // 8 softmax, 4 convert and 2 MMA warps
+constexpr int kTileSmem = 6 * kOperandBytes + 1024;  // Q x 2, K x 2, V x 2 (+ alignment)
+constexpr int kTileCtas = 148;
+constexpr int kTileMinShare = 1;
+constexpr float kLazy = 8.0f;            // log2 of how far a row may outgrow its maximum
+constexpr float kPShift = 7.0f;          // P is at most 2^(kLazy + kPShift)
+constexpr uint32_t kTileWait = 1u << 18;  // attempts of one bounded wait
+
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+// Instruction descriptor of kind::f16, fp16 x fp16 -> fp32, M = N = 128: D format f32 at bit 4,
+// B transposed (MN-major) at bit 16, N / 8 at bit 17, M / 16 at bit 24.
+constexpr uint32_t kIdescQK = (1u << 4) | ((kTile / 8) << 17) | ((kTile / 16) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+// Shared-memory operand descriptor, 128-byte swizzle: address / 16, leading offset / 16 at bit
+// 16, stride offset / 16 at bit 32, version 1 at bit 46, swizzle mode 2 at bit 61. Operand
+// tiles are [2 halves of 64 dims][128 rows][128 bytes]: groups of 8 rows are 1024 bytes apart
+// (stride offset), the halves 16384 bytes (leading offset, read for the MN-major V).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+// The barrier gets one arrival when every MMA this thread has issued so far is done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 32 columns of this warp's 32 TMEM lanes, one lane per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+        "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(addr));
+}
+
+// ---------------------------------------------------------------------------
+// units and segments
+// ---------------------------------------------------------------------------
+template <int ROWS>
+struct SeqTiles : SeqRows {
+  int units, per_head;  // units of a kv head, and their key tiles together
+  int gqa;
+  __device__ __forceinline__ int unit_tiles(int u) const {  // at least 1: an empty unit writes zeros
+    const int last = min(n - 1, ((u + 1) * ROWS - 1) / gqa);  // its last position
+    return max(0, L - n + last) / kTile + 1;
+  }
+};
+
+template <int ROWS>
+__device__ __forceinline__ SeqTiles<ROWS> tiles_of_seq(const CacheView &c, const Queries &qs, int b,
+                                                       int32_t *err) {
+  SeqTiles<ROWS> s;
+  static_cast<SeqRows &>(s) = rows_of(c, qs, b, err);
+  s.gqa = c.gqa;
+  s.units = static_cast<int>((static_cast<long long>(s.n) * c.gqa + ROWS - 1) / ROWS);
+  s.per_head = 0;
+  for (int u = 0; u < s.units; ++u) s.per_head += s.unit_tiles(u);
+  return s;
+}
+
+// A worker's next run of key tiles of one unit.
+template <int ROWS>
+struct Segments {
+  const CacheView &c;
+  const Queries &qs;
+  Share share;
+  long long at;
+  int b;
+  long long seq_first;
+  SeqTiles<ROWS> sq;
+  // the segment: unit u of kv head h, its key tiles [k0, k1) of nt
+  int h, u, k0, k1, nt;
+  bool first;  // the worker's first
+
+  __device__ __forceinline__ Segments(const CacheView &cc, const Queries &q, const Share &s)
+      : c(cc), qs(q), share(s), at(s.begin), b(s.b), seq_first(s.seq_first) {
+    if (share.begin < share.end) sq = tiles_of_seq<ROWS>(c, qs, b, nullptr);
+  }
+  __device__ __forceinline__ bool next() {
+    if (at >= share.end) return false;
+    while (at >= seq_first + static_cast<long long>(c.num_kv_heads) * sq.per_head) {
+      seq_first += static_cast<long long>(c.num_kv_heads) * sq.per_head;
+      sq = tiles_of_seq<ROWS>(c, qs, ++b, nullptr);
+    }
+    const long long in_seq = at - seq_first;
+    h = static_cast<int>(in_seq / sq.per_head);
+    int rest = static_cast<int>(in_seq - static_cast<long long>(h) * sq.per_head);
+    u = 0;
+    while (rest >= (nt = sq.unit_tiles(u))) {
+      rest -= nt;
+      ++u;
+    }
+    k0 = rest;
+    k1 = static_cast<int>(min(static_cast<long long>(nt), k0 + (share.end - at)));
+    first = at == share.begin;
+    at += k1 - k0;
+    return true;
+  }
+};
+
+// What a key tile's blocks are scaled by; a ring of four per pipeline (SHARED: of one ring), so
+// that a slot is written again only after the softmax threads have left it.
+struct TileScales {
+  float ks[kTilePages];  // negative: the page is left out
+  float vs[kTilePages];
+  float vlog;            // exponent e with every vs <= 2^e
+  int any_bad;
+};
+
+struct TileBars {
+  uint64_t q_full[2], s_full[2], p_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+};
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <int F, bool SHARED>
+__global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView c, Queries qs, Outputs out,
+                                                                     float *__restrict__ partials,
+                                                                     int32_t *err) {
+  constexpr int ROWS = SHARED ? 2 * kTile : kTile;  // rows of a unit
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ SplitSmem split;
+  __shared__ TileBars bars;
+  __shared__ TileScales scales[2][4];
+  __shared__ uint32_t tmem_base_s;
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = c.num_kv_heads, G = c.gqa;
+  // pipeline of this warp: softmax warps 0-3 and 4-7, convert warps 8-11 (two each, or all
+  // four for both), MMA warps 12 and 13
+  const int pipe = warp < 8 ? warp >> 2 : warp < 12 ? (SHARED ? 0 : (warp - 8) >> 1) : warp - 12;
+
+  if (threadIdx.x == 0) {
+    const int converters = SHARED ? 4 : 2;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], kTile);
+      mbar_init(&bars.s_full[i], 2);  // the MMAs' completion, and the issuing thread itself
+      mbar_init(&bars.p_full[i], kTile);
+      mbar_init(&bars.k_full[i], converters);
+      mbar_init(&bars.v_full[i], converters);
+      mbar_init(&bars.k_empty[i], SHARED ? 2 : 1);
+      mbar_init(&bars.v_empty[i], SHARED ? 2 : 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 12) {  // all 512 columns: S and O of both pipelines
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base_s))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  const int me = SHARED ? blockIdx.x : 2 * blockIdx.x + pipe;
+  const int workers = SHARED ? gridDim.x : 2 * gridDim.x;
+  const Share share = take_share(c.num_seqs, me, workers, kTileMinShare, split, [&](int i, bool check) {
+    return static_cast<long long>(H) *
+           tiles_of_seq<ROWS>(c, qs, i, check && blockIdx.x == 0 ? err : nullptr).per_head;
+  });
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  const uint32_t tm_s = tmem + 256 * pipe, tm_o = tm_s + 128;
+  uint8_t *q_tile = smem + pipe * kOperandBytes;
+  uint8_t *k_tiles = smem + 2 * kOperandBytes, *v_tiles = smem + 4 * kOperandBytes;
+  auto stage_of = [&](int k) { return SHARED ? k & 1 : pipe; };   // of the worker's k-th tile
+  auto phase_of = [&](int k) { return SHARED ? (k >> 1) & 1 : k & 1; };
+  auto slot_of = [&](int k) -> TileScales & { return scales[SHARED ? 0 : pipe][k & 3]; };
+  auto wait = [&](uint64_t *bar, int parity) {
+    if (mbar_wait_bounded(bar, parity, kTileWait)) return true;
+    set_err(err, KV4_DEVERR_TIMEOUT);
+    return false;
+  };
+  Segments<ROWS> sg(c, qs, share);
+  int kt = 0;      // tiles of the worker so far
+  bool ok = true;  // no wait has given up
+
+  if (warp >= 12) {
+    // ------------------------------- MMA -------------------------------
+    int seg = 0, pp = 0;  // live segments and phases of p_full so far
+    while (ok && sg.next()) {
+      const int n = sg.k1 - sg.k0;
+      const bool live = sg.u * ROWS + (SHARED ? pipe * kTile : 0) < sg.sq.n * G;
+      if (lane == 0) {
+        if (!live) {  // no rows here: only let go of the shared tiles
+          for (int j = 0; ok && j < n; ++j) {
+            const int st = stage_of(kt + j), ph = phase_of(kt + j);
+            ok = wait(&bars.k_full[st], ph);
+            mbar_arrive(&bars.k_empty[st]);
+            ok = ok && wait(&bars.v_full[st], ph);
+            mbar_arrive(&bars.v_empty[st]);
+          }
+        } else {
+          const uint64_t qd = smem_desc(smem_u32(q_tile));
+          // S (or the last O) is there; the thread's own arrival hands on what it has seen of
+          // the convert warps' writes (the tile's scales)
+          auto done = [&]() {
+            mma_commit(&bars.s_full[pipe]);
+            mbar_arrive(&bars.s_full[pipe]);
+          };
+          auto qk = [&](int k) {
+            const int st = stage_of(k);
+            ok = ok && wait(&bars.k_full[st], phase_of(k));
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t kd = smem_desc(smem_u32(k_tiles + st * kOperandBytes));
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {  // 16 dims: 32 bytes of a row; the halves 16 KB apart
+              const uint64_t off = static_cast<uint64_t>(((x >> 2) * 16384 + (x & 3) * 32) >> 4);
+              mma_ss(tm_s, qd + off, kd + off, kIdescQK, x > 0);
+            }
+            mma_commit(&bars.k_empty[st]);
+            done();
+          };
+          ok = wait(&bars.q_full[pipe], seg & 1);
+          tc_fence_after();
+          qk(kt);
+          for (int j = 0; ok && j < n; ++j) {
+            const int st = stage_of(kt + j);
+            ok = wait(&bars.p_full[pipe], pp & 1);
+            ++pp;
+            ok = ok && wait(&bars.v_full[st], phase_of(kt + j));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = smem_desc(smem_u32(v_tiles + st * kOperandBytes));
+#pragma unroll
+            for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
+              mma_ts(tm_o, tm_s + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4), kIdescPV, j > 0 || x > 0);
+            mma_commit(&bars.v_empty[st]);
+            if (j + 1 < n) qk(kt + j + 1);
+            else done();
+          }
+          ++seg;
+        }
+      }
+      kt += n;
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+    }
+  } else if (warp >= 8) {
+    // ------------------------------- convert -------------------------------
+    constexpr int kThreads = SHARED ? 128 : 64;
+    constexpr int kPieces = 128 / kThreads;  // 16-byte pieces of a page per thread
+    const int tid = SHARED ? threadIdx.x - 256 : (threadIdx.x - 256) & 63;
+    while (ok && sg.next()) {
+      const int32_t *pt = c.page_table + static_cast<size_t>(sg.b) * c.max_pages;
+      const int pages = (sg.sq.L + kPage - 1) / kPage;
+      for (int k = sg.k0; ok && k < sg.k1; ++k, ++kt) {
+        const int st = stage_of(kt), free_phase = phase_of(kt) ^ 1;
+        int pid = -1;
+        float ks = 0.f, vs = 0.f;
+        if (lane < kTilePages && k * kTilePages + lane < pages) {
+          pid = pt[k * kTilePages + lane];
+          if (pid < 0 || pid >= c.num_pages) {
+            set_err(err, KV4_DEVERR_PAGE_ID);
+            pid = -1;
+            ks = -1.f;
+          } else {
+            ks = __half2float(__ushort_as_half(c.k_params[static_cast<size_t>(pid) * H + sg.h]));
+            vs = __half2float(__ushort_as_half(c.v_params[static_cast<size_t>(pid) * H + sg.h]));
+          }
+        }
+        auto convert = [&](const uint8_t *codes) {
+          uint4 v[kTilePages][kPieces];
+#pragma unroll
+          for (int p = 0; p < kTilePages; ++p) {
+            const int page = __shfl_sync(0xffffffffu, pid, p);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              const int piece = tid + i * kThreads;  // strip piece / 16, slot piece % 16
+              const int pos = (k * kTilePages + p) * kPage + (piece & 15);
+              v[p][i] = make_uint4(0u, 0u, 0u, 0u);  // what lies behind the length may hold anything
+              if (page >= 0 && pos < sg.sq.L)
+                v[p][i] = *reinterpret_cast<const uint4 *>(
+                    codes + (static_cast<size_t>(page) * H + sg.h) * kInt8CodeBytes + piece * 16);
+            }
+          }
+          return [=](uint8_t *to) {
+#pragma unroll
+            for (int p = 0; p < kTilePages; ++p)
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) {
+                const int piece = tid + i * kThreads;
+                const int row = p * kPage + (piece & 15), strip = piece >> 4;
+                const uint32_t w[4] = {v[p][i].x, v[p][i].y, v[p][i].z, v[p][i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) code_pairs<F, false>(w[q], o[2 * q], o[2 * q + 1]);
+                uint8_t *at = to + (strip >> 2) * 16384 + row * 128;
+                const int chunk = (strip & 3) * 2;  // 16-byte chunks, xor-swizzled by the row
+                *reinterpret_cast<uint4 *>(at + ((chunk ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(at + (((chunk + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+          };
+        };
+        auto put_k = convert(c.k_codes);
+        ok = wait(&bars.k_empty[st], free_phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        put_k(k_tiles + st * kOperandBytes);
+        if (tid < 32) {  // the pipeline's first convert warp writes the scales
+          TileScales &sl = slot_of(kt);
+          float top = vs;
+#pragma unroll
+          for (int off = 1; off < kTilePages; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const unsigned bad = __ballot_sync(0xffffffffu, ks < 0.f);
+          if (lane < kTilePages) {
+            sl.ks[lane] = ks;
+            sl.vs[lane] = vs;
+          }
+          if (lane == 0) {
+            int e = -24;
+            if (top > 0.f) frexpf(top, &e);  // top < 2^e
+            sl.vlog = static_cast<float>(e);
+            sl.any_bad = bad != 0u;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.k_full[st]);
+        auto put_v = convert(c.v_codes);
+        ok = wait(&bars.v_empty[st], free_phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        put_v(v_tiles + st * kOperandBytes);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_full[st]);
+      }
+    }
+  } else {
+    // ------------------------------- softmax -------------------------------
+    const int row = threadIdx.x & 127;  // of the pipeline; its TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4), bits 16+
+    const uint32_t ts = tm_s + lane_off, to = tm_o + lane_off;
+    int sp = 0;  // phases of s_full
+    while (ok && sg.next()) {
+      const int n_tiles = sg.k1 - sg.k0;
+      const int r0 = sg.u * ROWS + (SHARED ? pipe * kTile : 0);
+      const int rows = sg.sq.n * G;
+      if (r0 >= rows) {  // (the MMA warp skips it too)
+        kt += n_tiles;
+        continue;
+      }
+      const int r = r0 + row;
+      const bool live = r < rows;
+      const int i = r / G;
+      const size_t qr = static_cast<size_t>(sg.sq.row0 + i) * H * G + sg.h * G + r % G;
+      const int lim = live ? sg.sq.L - sg.sq.n + i : -1;  // last position the row sees
+      float a;  // logit units: step of the fixed query times log2(e) / sqrt(128)
+      {
+        uint4 v[16];
+        float amax = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          v[x] = live ? reinterpret_cast<const uint4 *>(qs.q + qr * kHeadDim)[x] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xFFFF0000u))));
+        }
+        int ex = 0;
+        if (amax > 0.f) {
+          frexpf(amax, &ex);
+          ex -= 15;
+        }
+        const float step = fmaxf(ldexpf(1.0f, ex), 0x1p-120f);  // largest element in [2^14, 2^15)
+        const float inv = 1.0f / step;
+        a = step * kScaleLog2;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            o[y] = pack_h2(__uint_as_float(w[y] << 16) * inv, __uint_as_float(w[y] & 0xFFFF0000u) * inv);
+          *reinterpret_cast<uint4 *>(q_tile + (x >> 3) * 16384 + row * 128 + (((x & 7) ^ (row & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&bars.q_full[pipe]);
+
+      float m = kNegBig, l = 0.f, vref = 0.f;
+      for (int j = 0; ok && j < n_tiles; ++j, ++kt) {
+        ok = wait(&bars.s_full[pipe], sp & 1);
+        ++sp;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const TileScales &sl = slot_of(kt);
+        const int tok0 = (sg.k0 + j) * kTile;
+        const bool masked = __any_sync(0xffffffffu, tok0 + kTile - 1 > lim) || sl.any_bad;
+        // visible positions of block (16) x: the first `left` of it
+        auto left = [&](int x) { return sl.ks[x] < 0.f ? 0 : lim + 1 - tok0 - 16 * x; };
+        // ---- maximum ----
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          tmem_ld32(ts + 32 * q, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {
+            float mb = -CUDART_INF_F;
+            if (masked) {
+              const int n = left(2 * q + hb);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) mb = x < n ? fmaxf(mb, __uint_as_float(s[16 * hb + x])) : mb;
+            } else {
+#pragma unroll
+              for (int x = 0; x < 16; x += 2)
+                mb = fmaxf(mb, fmaxf(__uint_as_float(s[16 * hb + x]), __uint_as_float(s[16 * hb + x + 1])));
+            }
+            if (!masked || left(2 * q + hb) > 0) mx = fmaxf(mx, mb * (a * sl.ks[2 * q + hb]));
+          }
+        }
+        const float mn = mx > m + kLazy ? mx : m;
+        const float vn = j == 0 ? sl.vlog : fmaxf(vref, sl.vlog);
+        if (j > 0) {
+          const float f = fast_exp2(m - mn + vref - vn);
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st32(to + 32 * q, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        l *= fast_exp2(m - mn);
+        m = mn;
+        vref = vn;
+        // ---- weights ----
+        const float unit = fast_exp2(kPShift - vref);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32], p[16];
+          tmem_ld32(ts + 32 * q, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {
+            const float ak = a * sl.ks[2 * q + hb], cv = sl.vs[2 * q + hb] * unit;
+            const int n = masked ? left(2 * q + hb) : 16;
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+              float p0 = fast_exp2(fmaf(__uint_as_float(s[16 * hb + x]), ak, -m));
+              float p1 = fast_exp2(fmaf(__uint_as_float(s[16 * hb + x + 1]), ak, -m));
+              if (masked) {
+                p0 = x < n ? p0 : 0.f;
+                p1 = x + 1 < n ? p1 : 0.f;
+              }
+              l += p0 + p1;
+              p[8 * hb + x / 2] = pack_h2(p0 * cv, p1 * cv);
+            }
+          }
+          tmem_st16(ts + 16 * q, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[pipe]);
+      }
+      ok = ok && wait(&bars.s_full[pipe], sp & 1);  // O is complete
+      ++sp;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // ---- out ----
+      const bool whole = sg.k0 == 0 && sg.k1 == sg.nt;
+      const float undo = fast_exp2(vref - kPShift);
+      const float scale = whole ? (l > 0.f ? undo / l : 0.f) : undo;
+      float *rec = partials + (static_cast<size_t>(2 * me + (sg.first ? 0 : 1)) * ROWS +
+                               (SHARED ? pipe * kTile : 0) + row) * kRecordFloats;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * q, o);
+        tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] = l > 0.f ? __uint_as_float(o[x]) * scale : 0.f;
+        if (!live) continue;
+        if (whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * x + 2 * y], v[8 * x + 2 * y + 1]);
+              w[y] = *reinterpret_cast<const uint32_t *>(&t);
+            }
+            reinterpret_cast<uint4 *>(out.out + qr * kHeadDim + 32 * q)[x] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        float *f32 = whole ? (out.out_f32 ? out.out_f32 + qr * kHeadDim : nullptr) : rec;
+        if (f32 != nullptr)
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            reinterpret_cast<float4 *>(f32 + 32 * q)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+      }
+      if (live && whole && out.lse) out.lse[qr] = l > 0.f ? m * kLn2 + logf(l) : -CUDART_INF_F;
+      if (live && !whole) *reinterpret_cast<float2 *>(rec + kHeadDim) = make_float2(m, l);
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// Where worker blockIdx.x's share starts inside a unit that starts in the share before it, the
+// block joins that unit's records, in worker order (a unit over more workers is the first such
+// worker's to join). Rows over blockIdx.y and the warps.
+template <int ROWS>
+__global__ void __launch_bounds__(256) block8_tile_merge_kernel(CacheView c, Queries qs, Outputs out,
+                                                                const float *__restrict__ partials,
+                                                                int workers) {
+  __shared__ SplitSmem split;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = c.gqa, H = c.num_kv_heads, me = blockIdx.x + 1;
+  long long T;
+  const Share share = take_share(c.num_seqs, me, workers, kTileMinShare, split, [&](int i, bool) {
+    return static_cast<long long>(H) * tiles_of_seq<ROWS>(c, qs, i, nullptr).per_head;
+  }, &T);
+  Segments<ROWS> sg(c, qs, share);
+  if (!sg.next() || sg.k0 == 0) return;
+  const Shares sh(T, workers, kTileMinShare);
+  const long long t0 = share.begin - sg.k0;
+  if (sh.owner(t0) != me - 1) return;
+  const int w1 = sh.owner(t0 + sg.nt - 1);
+  const int last = min(ROWS, sg.sq.n * G - sg.u * ROWS);
+  for (int x = blockIdx.y * 8 + warp; x < last; x += gridDim.y * 8) {
+    const int r = sg.u * ROWS + x;
+    const size_t qr = static_cast<size_t>(sg.sq.row0 + r / G) * H * G + sg.h * G + r % G;
+    join_records(partials, ROWS, x, me - 1, w1, [&](int w) { return sh.begin(w) >= t0 ? 0 : 1; }, out, qr, lane);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+// CTAs for at most this many key tiles, of units of `rows` rows.
+static int tile_ctas(int num_seqs, int total_q, int max_seq_len, int H, int G, int rows) {
+  const long long units = (static_cast<long long>(total_q) * G + rows - 1) / rows + num_seqs;
+  const long long tiles = units * H * (max_seq_len / kTile + 1);
+  const int per_cta = rows == kTile ? 2 : 1;  // workers
+  return static_cast<int>(std::max(1LL, std::min<long long>(kTileCtas, (tiles + per_cta - 1) / per_cta)));
+}
+
+size_t tile_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G) {
+  // two records of 256 rows per CTA in either form
+  const size_t ctas = std::max(tile_ctas(num_seqs, total_q, max_seq_len, H, G, kTile),
+                               tile_ctas(num_seqs, total_q, max_seq_len, H, G, 2 * kTile));
+  return ctas * 2 * 2 * kTile * kRecordFloats * sizeof(float);
+}
+
+template <int F, bool SHARED>
+static cudaError_t launch_tile_t(const CacheView &c, const Queries &qs, int max_seq_len, const Outputs &out,
+                                 float *partials, int32_t *err, cudaStream_t s) {
+  constexpr int ROWS = SHARED ? 2 * kTile : kTile;
+  static PerDevice sms;
+  int n_sm = 0;
+  cudaError_t e = once_per_device(sms, [](int dev, int *g) {
+    cudaError_t r = cudaFuncSetAttribute(block8_tile_kernel<F, SHARED>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    return r == cudaSuccess ? cudaDeviceGetAttribute(g, cudaDevAttrMultiProcessorCount, dev) : r;
+  }, &n_sm);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::min(n_sm, tile_ctas(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa, ROWS));
+  block8_tile_kernel<F, SHARED><<<ctas, kTileThreads, kTileSmem, s>>>(c, qs, out, partials, err);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int workers = SHARED ? ctas : 2 * ctas;
+  if (workers > 1)
+    block8_tile_merge_kernel<ROWS><<<dim3(workers - 1, 4), 256, 0, s>>>(c, qs, out, partials, workers);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs, int max_seq_len,
+                                  const Outputs &out, void *workspace, int32_t *err, cudaStream_t s) {
+  float *p = static_cast<float *>(workspace);
+  const bool shared = static_cast<long long>(qs.max_n) * c.gqa > kTile;
+  if (fmt == kFmtInt8)
+    return shared ? launch_tile_t<kFmtInt8, true>(c, qs, max_seq_len, out, p, err, s)
+                  : launch_tile_t<kFmtInt8, false>(c, qs, max_seq_len, out, p, err, s);
+  return shared ? launch_tile_t<kFmtE4m3, true>(c, qs, max_seq_len, out, p, err, s)
+                : launch_tile_t<kFmtE4m3, false>(c, qs, max_seq_len, out, p, err, s);
+}
+
+}  // namespace kv4

@@ -37,6 +37,7 @@ __device__ __forceinline__ Tiles tiles_of(const CacheView &c, int acc_stride, in
   return t;
 }
 
+constexpr int kWMinShare = 4;  // tiles per warp, at least
 constexpr int kWStages = 8;
 constexpr int kWStageBytes = 2304;  // K codes (at most 2048), then K scales or parameters
 constexpr int kWWarpSmem = kWStages * kWStageBytes;
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     fence_barrier_init();
   }
   const int me = blockIdx.x * kWarps + warp;
-  const Share share = take_share(c.num_seqs, me, gridDim.x * kWarps, split, [&](int i, bool check) {
+  const Share share = take_share(c.num_seqs, me, gridDim.x * kWarps, kWMinShare, split, [&](int i, bool check) {
     return static_cast<long long>(H) *
            tiles_of(c, acc_stride, i, check && blockIdx.x == 0 ? err : nullptr).n();
   });
@@ -645,7 +646,7 @@ cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>(c.num_seqs) * c.num_kv_heads *
                           (max_seq_len / kPage + 2 + c.sink_tiles + c.ring_tiles);
-  const long long want = (tiles / kMinShare + kWarps) / kWarps;
+  const long long want = (tiles / kWMinShare + kWarps) / kWarps;
   const int grid = static_cast<int>(want < most ? want : most);
   weights_kernel<<<grid, kWarps * 32, kWCtaSmem, s>>>(c, q, lse, acc_in, acc_out, acc_stride, err);
   return cudaGetLastError();

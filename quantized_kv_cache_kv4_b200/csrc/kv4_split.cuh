@@ -1,5 +1,5 @@
 // A batch of T work items (runs of pages, in sequence order) split into equal contiguous
-// shares, one per warp: no work list, no counter and no launch of its own. Every CTA scans
+// shares, one per worker (a warp, or a CTA's pipeline): no work list, no counter and no launch of its own. Every CTA scans
 // the sequences' item counts itself (a few KB of lengths from L2), so that a share starts
 // with a search over the block's scan and a walk over one thread's run of sequences.
 #pragma once
@@ -8,15 +8,14 @@
 
 namespace kv4 {
 
-constexpr int kSplitThreads = 128;  // threads of a CTA that splits (4 warps)
-constexpr int kMinShare = 4;        // items per warp, at least
+constexpr int kSplitThreads = 128;  // threads of a CTA that scan (its first 4 warps)
 
-// The share of warp w and the owner of item t, for T items over up to W warps: the first
-// `more` warps take per + 1 items, the others per.
+// The share of worker w and the owner of item t, for T items over up to W workers with at
+// least `least` items each: the first `more` workers take per + 1 items, the others per.
 struct Shares {
   long long per, more;
-  __device__ __forceinline__ Shares(long long T, int W) {
-    const long long w = max(1LL, min(static_cast<long long>(W), T / kMinShare));
+  __device__ __forceinline__ Shares(long long T, int W, int least) {
+    const long long w = max(1LL, min(static_cast<long long>(W), T / least));
     per = T / w;
     more = T - per * w;
   }
@@ -32,19 +31,22 @@ struct SplitSmem {
   long long wsum[kSplitThreads / 32];
 };
 
-// The share [begin, end) of this warp, number `me` of W, and the sequence its first item is
+// The share [begin, end) of worker `me` of W (a warp; all its lanes pass the same), and the sequence its first item is
 // in (whose first item is seq_first). items(b): items of sequence b (>= 0). An empty share
 // has begin >= end. All threads of the block call it.
+// total: where the number of items goes.
 struct Share {
   long long begin, end, seq_first;
   int b;
 };
 template <class Items>
-__device__ __forceinline__ Share take_share(int B, int me, int W, SplitSmem &sm, Items items) {
+__device__ __forceinline__ Share take_share(int B, int me, int W, int least, SplitSmem &sm, Items items,
+                                            long long *total = nullptr) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int run = (B + kSplitThreads - 1) / kSplitThreads;
   long long mine = 0;
-  for (int i = 0; i < run; ++i) {
+  const bool scans = threadIdx.x < kSplitThreads;
+  for (int i = 0; scans && i < run; ++i) {
     const int b = threadIdx.x * run + i;
     if (b < B) mine += items(b, true);
   }
@@ -54,15 +56,18 @@ __device__ __forceinline__ Share take_share(int B, int me, int W, SplitSmem &sm,
     const long long y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
-  if (lane == 31) sm.wsum[warp] = incl;
+  if (scans && lane == 31) sm.wsum[warp] = incl;
   __syncthreads();
-  long long base = 0;
-  for (int i = 0; i < warp; ++i) base += sm.wsum[i];
-  sm.scan[threadIdx.x + 1] = base + incl;
+  if (scans) {
+    long long base = 0;
+    for (int i = 0; i < warp; ++i) base += sm.wsum[i];
+    sm.scan[threadIdx.x + 1] = base + incl;
+  }
   if (threadIdx.x == 0) sm.scan[0] = 0;
   __syncthreads();
   const long long T = sm.scan[kSplitThreads];
-  const Shares sh(T, W);
+  if (total != nullptr) *total = T;
+  const Shares sh(T, W, least);
   Share s{sh.begin(me), min(sh.begin(me + 1), T), 0, 0};
   if (s.begin >= s.end) return s;
   int lo = 0, hi = kSplitThreads - 1;  // the last run that starts at or before the share

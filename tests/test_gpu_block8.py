@@ -108,6 +108,15 @@ class Model:
             out.append(y)
         return out
 
+    def code_sums(self, b):
+        """Largest value scale times the sum of |value codes| of each kv head: [H, 128]."""
+        out = np.zeros((self.H, 128))
+        for h in range(self.H):
+            blocks = [self.blocks[("v", b, p, h)] for p in range(-(-int(self.lens[b]) // 16))]
+            if blocks:
+                out[h] = max(x.scale for x in blocks) * sum(np.abs(x.codes).sum(0) for x in blocks)
+        return out
+
     def attend(self, n, seed=1, qscale=1.0, behind=0, stream=None, workspace=None):
         """Attention of the last n[b] positions of every sequence, against the oracle."""
         kv4 = _kv4()
@@ -151,6 +160,11 @@ class Model:
             # most 2^-25 there: 2^-39 of the largest weight for each row (the largest one's value
             # may be 0 where A is then made of such weights alone)
             to += 2.0 ** -39 * np.repeat(np.abs(V).sum(0), self.G, 0)
+            # more than 8 query rows of a kv head: the weights carry the value scales, p 2^7 vs /
+            # 2^e with 2^e at most twice the largest scale, and an fp16 subnormal of that is off by
+            # at most 2^-25: 2^-31 of the largest scale for each code
+            if max(n) * self.G > 8:
+                to += 2.0 ** -31 * np.repeat(self.code_sums(b), self.G, 0)
             assert np.all(np.abs(o32[sl] - Or) <= to), (b, (np.abs(o32[sl] - Or) / to).max())
             assert np.all(np.abs(out[sl] - Or) <= to + 2.0 ** -8 * np.abs(Or)), b
             seen = np.isfinite(lr)
