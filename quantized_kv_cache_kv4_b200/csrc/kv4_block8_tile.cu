@@ -35,7 +35,10 @@ namespace kv4 {
 constexpr int kTile = 128;               // rows of a pipeline, positions of a key tile
 constexpr int kTilePages = kTile / kPage;
 constexpr int kOperandBytes = kTile * kHeadDim * 2;  // one fp16 operand tile: 32 KB
-constexpr int kTileThreads = 448;        // 8 softmax, 4 convert and 2 MMA warps
+constexpr int kTileThreads = 512;        // 8 softmax, 4 convert and 2 MMA warps (and 2 idle)
+// registers per thread of the three kinds: 256 x 176 + 128 x 112 + 128 x 48 = 512 x 128, what
+// the block is launched with
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 112, kMmaRegs = 48;
 constexpr int kTileSmem = 6 * kOperandBytes + 1024;  // Q x 2, K x 2, V x 2 (+ alignment)
 constexpr int kTileCtas = 148;
 constexpr int kTileMinShare = 1;
@@ -103,15 +106,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
-          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
-        "r"(addr));
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -120,6 +120,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
         "r"(addr));
 }
+
+template <int N>
+struct Setmax {
+  static __device__ __forceinline__ void inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+  static __device__ __forceinline__ void dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+};
 
 // ---------------------------------------------------------------------------
 // units and segments
@@ -188,17 +194,40 @@ struct Segments {
 
 // What a key tile's blocks are scaled by; a ring of four per pipeline (SHARED: of one ring), so
 // that a slot is written again only after the softmax threads have left it.
-struct TileScales {
+struct alignas(16) TileScales {
   float ks[kTilePages];  // negative: the page is left out
-  float vs[kTilePages];
-  float vlog;            // exponent e with every vs <= 2^e
+  float cv[kTilePages];  // vs 2^(kPShift - vref)
+  float vref;            // exponent with every value scale of the segment so far at most 2^vref
+  float moved;           // vref before this tile, less vref (0: it has not moved)
   int any_bad;
 };
 
+// A segment as the scheduling warp hands it to the others (b < 0: no more).
+struct Seg {
+  int b, h, u, k0, k1, nt, first;
+  int L, n, row0;  // the sequence's length, queries and first query row
+};
+constexpr int kSegRing = 4;
+
 struct TileBars {
+  uint64_t seg_full[2][kSegRing], seg_empty[2][kSegRing];
   uint64_t q_full[2], s_full[2], p_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
 };
+
+// The logits of positions that a row does not see, -inf: all but the tile's first `left`, and
+// those of pages that are left out.
+__device__ __forceinline__ void mask_logits(uint32_t (&s)[4][32], const TileScales &sl, int left) {
+#pragma unroll
+  for (int x = 0; x < kTilePages; ++x) {
+    const int n = sl.ks[x] < 0.f ? 0 : left - 16 * x;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) {
+      uint32_t &v = s[x >> 1][16 * (x & 1) + y];
+      v = y < n ? v : 0xff800000u;
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------
 // the kernel
@@ -212,22 +241,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   __shared__ SplitSmem split;
   __shared__ TileBars bars;
   __shared__ TileScales scales[2][4];
+  __shared__ Seg segs[2][kSegRing];
   __shared__ uint32_t tmem_base_s;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = c.num_kv_heads, G = c.gqa;
-  // pipeline of this warp: softmax warps 0-3 and 4-7, convert warps 8-11 (two each, or all
-  // four for both), MMA warps 12 and 13
-  const int pipe = warp < 8 ? warp >> 2 : warp < 12 ? (SHARED ? 0 : (warp - 8) >> 1) : warp - 12;
+  // pipeline of this warp: softmax warps 0-3 and 4-7, MMA warps 12 and 13, scheduling warps 14
+  // and 15; convert warps 8-11 serve both
+  const int pipe = warp < 8 ? warp >> 2 : warp < 12 ? 0 : (warp - 12) & 1;
+  const int ring = SHARED ? 0 : pipe;  // of segments
 
   if (threadIdx.x == 0) {
-    const int converters = SHARED ? 4 : 2;
     for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < kSegRing; ++k) {
+        mbar_init(&bars.seg_full[i][k], 1);
+        mbar_init(&bars.seg_empty[i][k], SHARED ? 14 : 9);  // warps that read it
+      }
       mbar_init(&bars.q_full[i], kTile);
       mbar_init(&bars.s_full[i], 2);  // the MMAs' completion, and the issuing thread itself
       mbar_init(&bars.p_full[i], kTile);
-      mbar_init(&bars.k_full[i], converters);
-      mbar_init(&bars.v_full[i], converters);
+      mbar_init(&bars.k_full[i], 4);
+      mbar_init(&bars.v_full[i], 4);
       mbar_init(&bars.k_empty[i], SHARED ? 2 : 1);
       mbar_init(&bars.v_empty[i], SHARED ? 2 : 1);
     }
@@ -241,10 +275,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   }
   const int me = SHARED ? blockIdx.x : 2 * blockIdx.x + pipe;
   const int workers = SHARED ? gridDim.x : 2 * gridDim.x;
-  const Share share = take_share(c.num_seqs, me, workers, kTileMinShare, split, [&](int i, bool check) {
+  auto items = [&](int i, bool check) {
     return static_cast<long long>(H) *
            tiles_of_seq<ROWS>(c, qs, i, check && blockIdx.x == 0 ? err : nullptr).per_head;
-  });
+  };
+  const Share share = take_share(c.num_seqs, me, workers, kTileMinShare, split, items);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
@@ -259,16 +294,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     set_err(err, KV4_DEVERR_TIMEOUT);
     return false;
   };
-  Segments<ROWS> sg(c, qs, share);
   int kt = 0;      // tiles of the worker so far
+  int seg_no = 0;  // segments read from the ring so far
   bool ok = true;  // no wait has given up
+  auto read_seg = [&](int r, int no, Seg &s) {  // all lanes of a warp; false: no more
+    const int at = no & (kSegRing - 1);
+    ok = __all_sync(0xffffffffu, wait(&bars.seg_full[r][at], (no / kSegRing) & 1));
+    if (!ok) return false;
+    s = segs[r][at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.seg_empty[r][at]);
+    return s.b >= 0;
+  };
 
-  if (warp >= 12) {
+  if (warp >= 14) {
+    // ------------------------------- schedule -------------------------------
+    Setmax<kMmaRegs>::dec();
+    if (lane == 0 && (!SHARED || pipe == 0)) {
+      Segments<ROWS> sg(c, qs, share);
+      for (int no = 0;; ++no) {
+        const bool more = sg.next();
+        const int at = no & (kSegRing - 1);
+        if (!wait(&bars.seg_empty[ring][at], ((no / kSegRing) & 1) ^ 1)) break;
+        segs[ring][at] = more ? Seg{sg.b, sg.h, sg.u, sg.k0, sg.k1, sg.nt, sg.first, sg.sq.L, sg.sq.n, sg.sq.row0}
+                              : Seg{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        mbar_arrive(&bars.seg_full[ring][at]);
+        if (!more) break;
+      }
+    }
+  } else if (warp >= 12) {
+    Setmax<kMmaRegs>::dec();
     // ------------------------------- MMA -------------------------------
     int seg = 0, pp = 0;  // live segments and phases of p_full so far
-    while (ok && sg.next()) {
+    Seg sg;
+    while (ok && read_seg(ring, seg_no++, sg)) {
       const int n = sg.k1 - sg.k0;
-      const bool live = sg.u * ROWS + (SHARED ? pipe * kTile : 0) < sg.sq.n * G;
+      const bool live = sg.u * ROWS + (SHARED ? pipe * kTile : 0) < sg.n * G;
       if (lane == 0) {
         if (!live) {  // no rows here: only let go of the shared tiles
           for (int j = 0; ok && j < n; ++j) {
@@ -326,105 +387,161 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     }
   } else if (warp >= 8) {
     // ------------------------------- convert -------------------------------
-    constexpr int kThreads = SHARED ? 128 : 64;
-    constexpr int kPieces = 128 / kThreads;  // 16-byte pieces of a page per thread
-    const int tid = SHARED ? threadIdx.x - 256 : (threadIdx.x - 256) & 63;
-    while (ok && sg.next()) {
-      const int32_t *pt = c.page_table + static_cast<size_t>(sg.b) * c.max_pages;
-      const int pages = (sg.sq.L + kPage - 1) / kPage;
-      for (int k = sg.k0; ok && k < sg.k1; ++k, ++kt) {
-        const int st = stage_of(kt), free_phase = phase_of(kt) ^ 1;
-        int pid = -1;
-        float ks = 0.f, vs = 0.f;
-        if (lane < kTilePages && k * kTilePages + lane < pages) {
-          pid = pt[k * kTilePages + lane];
-          if (pid < 0 || pid >= c.num_pages) {
-            set_err(err, KV4_DEVERR_PAGE_ID);
-            pid = -1;
-            ks = -1.f;
-          } else {
-            ks = __half2float(__ushort_as_half(c.k_params[static_cast<size_t>(pid) * H + sg.h]));
-            vs = __half2float(__ushort_as_half(c.v_params[static_cast<size_t>(pid) * H + sg.h]));
-          }
-        }
-        auto convert = [&](const uint8_t *codes) {
-          uint4 v[kTilePages][kPieces];
-#pragma unroll
-          for (int p = 0; p < kTilePages; ++p) {
-            const int page = __shfl_sync(0xffffffffu, pid, p);
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-              const int piece = tid + i * kThreads;  // strip piece / 16, slot piece % 16
-              const int pos = (k * kTilePages + p) * kPage + (piece & 15);
-              v[p][i] = make_uint4(0u, 0u, 0u, 0u);  // what lies behind the length may hold anything
-              if (page >= 0 && pos < sg.sq.L)
-                v[p][i] = *reinterpret_cast<const uint4 *>(
-                    codes + (static_cast<size_t>(page) * H + sg.h) * kInt8CodeBytes + piece * 16);
-            }
-          }
-          return [=](uint8_t *to) {
-#pragma unroll
-            for (int p = 0; p < kTilePages; ++p)
-#pragma unroll
-              for (int i = 0; i < kPieces; ++i) {
-                const int piece = tid + i * kThreads;
-                const int row = p * kPage + (piece & 15), strip = piece >> 4;
-                const uint32_t w[4] = {v[p][i].x, v[p][i].y, v[p][i].z, v[p][i].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) code_pairs<F, false>(w[q], o[2 * q], o[2 * q + 1]);
-                uint8_t *at = to + (strip >> 2) * 16384 + row * 128;
-                const int chunk = (strip & 3) * 2;  // 16-byte chunks, xor-swizzled by the row
-                *reinterpret_cast<uint4 *>(at + ((chunk ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(at + (((chunk + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-              }
-          };
-        };
-        auto put_k = convert(c.k_codes);
-        ok = wait(&bars.k_empty[st], free_phase);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        put_k(k_tiles + st * kOperandBytes);
-        if (tid < 32) {  // the pipeline's first convert warp writes the scales
-          TileScales &sl = slot_of(kt);
-          float top = vs;
-#pragma unroll
-          for (int off = 1; off < kTilePages; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          const unsigned bad = __ballot_sync(0xffffffffu, ks < 0.f);
-          if (lane < kTilePages) {
-            sl.ks[lane] = ks;
-            sl.vs[lane] = vs;
-          }
-          if (lane == 0) {
-            int e = -24;
-            if (top > 0.f) frexpf(top, &e);  // top < 2^e
-            sl.vlog = static_cast<float>(e);
-            sl.any_bad = bad != 0u;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.k_full[st]);
-        auto put_v = convert(c.v_codes);
-        ok = wait(&bars.v_empty[st], free_phase);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        put_v(v_tiles + st * kOperandBytes);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.v_full[st]);
+    // One tile ahead in registers (its codes), two ahead its blocks' scales, three ahead its page
+    // ids: nothing waits for what it has just asked for. The workers' tiles in turn (SHARED: the
+    // one worker's); 128 threads, a 16-byte piece of each page each.
+    Setmax<kConvertRegs>::dec();
+    const int tid = threadIdx.x - 256;
+    const int strip = tid >> 4, slot = tid & 15;
+    struct Meta {
+      int w;          // worker (0 or 1), -1: no tile
+      int kt, k, L;   // the worker's tile number, its key tile, the length
+      int h, pid;     // kv head; page (lane % 8) of the tile (-2: behind the length)
+      uint16_t ks, vs;  // and its scales
+      bool first;     // the segment's first tile
+    };
+    Seg seg0, seg1;  // the workers' segments
+    int at0 = 0, end0 = 0, at1 = 0, end1 = 0, n0 = 0, n1 = 0, s0 = 0, s1 = 0;
+    bool more0 = true, more1 = !SHARED;
+    int turn = 0;
+    // the next tile of worker w: its segment, or nullptr
+    auto step = [&](int w, Seg &s, int &at, int &end, int &n_tiles, int &n_segs, bool &more, Meta &m) {
+      if (at == end) {
+        more = more && read_seg(w, n_segs++, s);
+        if (!more) return false;
+        at = s.k0;
+        end = s.k1;
       }
+      m.w = w;
+      m.kt = n_tiles++;
+      m.first = at == s.k0;
+      m.k = at++;
+      m.L = s.L;
+      m.h = s.h;
+      return true;
+    };
+    auto ask_page = [&]() {  // the next tile and its page ids
+      Meta m{-1, 0, 0, 0, 0, -2, 0, 0, false};
+      int b = 0;
+      if constexpr (SHARED) {
+        if (step(0, seg0, at0, end0, n0, s0, more0, m)) b = seg0.b;
+      } else {
+        for (int t = 0; t < 2 && m.w < 0; ++t, turn ^= 1) {
+          if (turn == 0 && step(0, seg0, at0, end0, n0, s0, more0, m)) b = seg0.b;
+          else if (turn == 1 && step(1, seg1, at1, end1, n1, s1, more1, m)) b = seg1.b;
+        }
+      }
+      const int page = m.k * kTilePages + (lane & 7);
+      if (m.w >= 0 && page < (m.L + kPage - 1) / kPage)
+        m.pid = __ldg(c.page_table + static_cast<size_t>(b) * c.max_pages + page);
+      return m;
+    };
+    auto ask_scales = [&](Meta &m) {  // of its pages, and whether the ids are any
+      if (m.pid == -2 && (m.w < 0 || m.k * kTilePages + (lane & 7) >= (m.L + kPage - 1) / kPage)) return;
+      if (m.pid < 0 || m.pid >= c.num_pages) {
+        set_err(err, KV4_DEVERR_PAGE_ID);
+        m.pid = -1;
+      } else {
+        m.ks = __ldg(c.k_params + static_cast<size_t>(m.pid) * H + m.h);
+        m.vs = __ldg(c.v_params + static_cast<size_t>(m.pid) * H + m.h);
+      }
+    };
+    // A thread's piece of each page; of page 0 where there is none (put() then writes zeros)
+    auto load = [&](const uint8_t *codes, const Meta &m, uint4 (&v)[kTilePages]) {
+      if (c.num_pages == 0) return;  // (nor is there a page 0 then)
+#pragma unroll
+      for (int p = 0; p < kTilePages; ++p) {
+        const int page = max(0, __shfl_sync(0xffffffffu, m.pid, p));
+        v[p] = __ldg(reinterpret_cast<const uint4 *>(
+            codes + (static_cast<size_t>(page) * H + m.h) * kInt8CodeBytes + tid * 16));
+      }
+    };
+    auto put = [&](uint8_t *tile, const Meta &m, uint4 (&v)[kTilePages]) {
+      // what lies behind the length, or on a page that is none, may hold anything
+      if (__any_sync(0xffffffffu, m.pid < 0) || (m.k + 1) * kTile > m.L) {
+#pragma unroll
+        for (int p = 0; p < kTilePages; ++p)
+          if (__shfl_sync(0xffffffffu, m.pid, p) < 0 || (m.k * kTilePages + p) * kPage + slot >= m.L)
+            v[p] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int p = 0; p < kTilePages; ++p) {
+        const int row = p * kPage + slot;
+        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) code_pairs<F, false>(w[q], o[2 * q], o[2 * q + 1]);
+        uint8_t *at = tile + (strip >> 2) * 16384 + row * 128;
+        const int chunk = (strip & 3) * 2;  // 16-byte chunks, xor-swizzled by the row
+        *reinterpret_cast<uint4 *>(at + ((chunk ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(at + (((chunk + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    float vref0 = 0.f, vref1 = 0.f;
+    uint4 kv[kTilePages] = {}, vv[kTilePages] = {};
+    Meta cur = ask_page(), nxt = ask_page();
+    ask_scales(cur);
+    ask_scales(nxt);
+    Meta nx2 = ask_page();
+    if (cur.w >= 0) {
+      load(c.k_codes, cur, kv);
+      load(c.v_codes, cur, vv);
+    }
+    while (cur.w >= 0) {
+      const int st = SHARED ? cur.kt & 1 : cur.w;
+      const int free_phase = (SHARED ? (cur.kt >> 1) & 1 : cur.kt & 1) ^ 1;
+      ok = __all_sync(0xffffffffu, wait(&bars.k_empty[st], free_phase));
+      if (!ok) break;
+      if (tid < 32) {  // the first convert warp writes the scales
+        TileScales &sl = scales[cur.w][cur.kt & 3];
+        const float ks = cur.pid == -1 ? -1.f : __half2float(__ushort_as_half(cur.ks));
+        const float vs = __half2float(__ushort_as_half(cur.vs));
+        float top = vs;
+#pragma unroll
+        for (int off = 1; off < kTilePages; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const unsigned bad = __ballot_sync(0xffffffffu, cur.pid == -1);
+        int e = -24;
+        if (top > 0.f) frexpf(top, &e);  // top < 2^e
+        float &vref = cur.w == 0 ? vref0 : vref1;
+        const float before = cur.first ? static_cast<float>(e) : vref;
+        vref = fmaxf(before, static_cast<float>(e));
+        if (lane < kTilePages) {
+          sl.ks[lane] = ks;
+          sl.cv[lane] = vs * fast_exp2(kPShift - vref);
+        }
+        if (lane == 0) {
+          sl.vref = vref;
+          sl.moved = before - vref;
+          sl.any_bad = bad != 0u;
+        }
+      }
+      put(k_tiles + st * kOperandBytes, cur, kv);
+      if (lane == 0) mbar_arrive(&bars.k_full[st]);
+      if (nxt.w >= 0) load(c.k_codes, nxt, kv);
+      ok = __all_sync(0xffffffffu, wait(&bars.v_empty[st], free_phase));
+      if (!ok) break;
+      put(v_tiles + st * kOperandBytes, cur, vv);
+      if (lane == 0) mbar_arrive(&bars.v_full[st]);
+      if (nxt.w >= 0) load(c.v_codes, nxt, vv);
+      cur = nxt;
+      nxt = nx2;
+      ask_scales(nxt);
+      nx2 = ask_page();
     }
   } else {
     // ------------------------------- softmax -------------------------------
+    Setmax<kSoftmaxRegs>::inc();
     const int row = threadIdx.x & 127;  // of the pipeline; its TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4), bits 16+
     const uint32_t ts = tm_s + lane_off, to = tm_o + lane_off;
     int sp = 0;  // phases of s_full
-    while (ok && sg.next()) {
+    Seg sg;
+    while (ok && read_seg(ring, seg_no++, sg)) {
       const int n_tiles = sg.k1 - sg.k0;
       const int r0 = sg.u * ROWS + (SHARED ? pipe * kTile : 0);
-      const int rows = sg.sq.n * G;
+      const int rows = sg.n * G;
       if (r0 >= rows) {  // (the MMA warp skips it too)
         kt += n_tiles;
         continue;
@@ -432,8 +549,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       const int r = r0 + row;
       const bool live = r < rows;
       const int i = r / G;
-      const size_t qr = static_cast<size_t>(sg.sq.row0 + i) * H * G + sg.h * G + r % G;
-      const int lim = live ? sg.sq.L - sg.sq.n + i : -1;  // last position the row sees
+      const size_t qr = static_cast<size_t>(sg.row0 + i) * H * G + sg.h * G + r % G;
+      const int lim = live ? sg.L - sg.n + i : -1;  // last position the row sees
       float a;  // logit units: step of the fixed query times log2(e) / sqrt(128)
       {
         uint4 v[16];
@@ -479,75 +596,70 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         const TileScales &sl = slot_of(kt);
         const int tok0 = (sg.k0 + j) * kTile;
         const bool masked = __any_sync(0xffffffffu, tok0 + kTile - 1 > lim) || sl.any_bad;
-        // visible positions of block (16) x: the first `left` of it
-        auto left = [&](int x) { return sl.ks[x] < 0.f ? 0 : lim + 1 - tok0 - 16 * x; };
-        // ---- maximum ----
+        // ---- the row's logits, and their maximum ----
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+        tmem_wait_ld();
+        if (masked) mask_logits(s, sl, lim + 1 - tok0);
+        // (-inf * 0 would be no logit: a block of zero keys has scale 0)
+        auto scale_of = [&](int x) { return fmaxf(a * sl.ks[x], 0x1p-126f); };
         float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          tmem_ld32(ts + 32 * q, s);
-          tmem_wait_ld();
+        for (int x = 0; x < kTilePages; ++x) {
+          const uint32_t *z = s[x >> 1] + 16 * (x & 1);
+          float mb = __uint_as_float(z[0]);
 #pragma unroll
-          for (int hb = 0; hb < 2; ++hb) {
-            float mb = -CUDART_INF_F;
-            if (masked) {
-              const int n = left(2 * q + hb);
-#pragma unroll
-              for (int x = 0; x < 16; ++x) mb = x < n ? fmaxf(mb, __uint_as_float(s[16 * hb + x])) : mb;
-            } else {
-#pragma unroll
-              for (int x = 0; x < 16; x += 2)
-                mb = fmaxf(mb, fmaxf(__uint_as_float(s[16 * hb + x]), __uint_as_float(s[16 * hb + x + 1])));
-            }
-            if (!masked || left(2 * q + hb) > 0) mx = fmaxf(mx, mb * (a * sl.ks[2 * q + hb]));
-          }
+          for (int y = 1; y < 15; y += 2) mb = fmaxf(fmaxf(mb, __uint_as_float(z[y])), __uint_as_float(z[y + 1]));
+          mx = fmaxf(mx, fmaxf(mb, __uint_as_float(z[15])) * scale_of(x));
         }
-        const float mn = mx > m + kLazy ? mx : m;
-        const float vn = j == 0 ? sl.vlog : fmaxf(vref, sl.vlog);
-        if (j > 0) {
-          const float f = fast_exp2(m - mn + vref - vn);
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * q, o);
+        vref = sl.vref;
+        const float moved = sl.moved;
+        if (__any_sync(0xffffffffu, mx > m + kLazy) || moved != 0.f) {
+          const float mn = mx > m + kLazy ? mx : m;
+          const float drop = fast_exp2(m - mn);
+          if (j > 0) {
+            const float f = drop * fast_exp2(moved);
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {  // (16 columns at a time: the logits are in registers)
+              uint32_t o[16];
+              tmem_ld16(to + 16 * q, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st32(to + 32 * q, o);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st16(to + 16 * q, o);
             }
             tmem_wait_st();
           }
+          l *= drop;
+          m = mn;
         }
-        l *= fast_exp2(m - mn);
-        m = mn;
-        vref = vn;
         // ---- weights ----
-        const float unit = fast_exp2(kPShift - vref);
+        float2 l2 = make_float2(0.f, 0.f);
+        const float2 m2 = make_float2(-m, -m);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t s[32], p[16];
-          tmem_ld32(ts + 32 * q, s);
-          tmem_wait_ld();
+          uint32_t p[16];
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {
-            const float ak = a * sl.ks[2 * q + hb], cv = sl.vs[2 * q + hb] * unit;
-            const int n = masked ? left(2 * q + hb) : 16;
+            const float cv = sl.cv[2 * q + hb];
+            const float ak = scale_of(2 * q + hb);
+            const float2 ak2 = make_float2(ak, ak);
+            const float2 cv2 = make_float2(cv, cv);
 #pragma unroll
             for (int x = 0; x < 16; x += 2) {
-              float p0 = fast_exp2(fmaf(__uint_as_float(s[16 * hb + x]), ak, -m));
-              float p1 = fast_exp2(fmaf(__uint_as_float(s[16 * hb + x + 1]), ak, -m));
-              if (masked) {
-                p0 = x < n ? p0 : 0.f;
-                p1 = x + 1 < n ? p1 : 0.f;
-              }
-              l += p0 + p1;
-              p[8 * hb + x / 2] = pack_h2(p0 * cv, p1 * cv);
+              float2 z = ffma2(make_float2(__uint_as_float(s[q][16 * hb + x]), __uint_as_float(s[q][16 * hb + x + 1])),
+                               ak2, m2);
+              z.x = fast_exp2(z.x);
+              z.y = fast_exp2(z.y);
+              l2 = fadd2(l2, z);
+              z = fmul2(z, cv2);
+              p[8 * hb + x / 2] = pack_h2(z.x, z.y);
             }
           }
           tmem_st16(ts + 16 * q, p);
         }
+        l += l2.x + l2.y;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars.p_full[pipe]);

@@ -39,6 +39,31 @@ struct Share {
   long long begin, end, seq_first;
   int b;
 };
+// The share of worker `me` from the block's scan (after take_share; no barrier).
+template <class Items>
+__device__ __forceinline__ Share find_share(int B, int me, int W, int least, const SplitSmem &sm,
+                                            Items items) {
+  const int run = (B + kSplitThreads - 1) / kSplitThreads;
+  const long long T = sm.scan[kSplitThreads];
+  const Shares sh(T, W, least);
+  Share s{sh.begin(me), min(sh.begin(me + 1), T), 0, 0};
+  if (s.begin >= s.end) return s;
+  int lo = 0, hi = kSplitThreads - 1;  // the last run that starts at or before the share
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sm.scan[mid] <= s.begin) lo = mid; else hi = mid - 1;
+  }
+  s.b = lo * run;
+  s.seq_first = sm.scan[lo];
+  for (;;) {
+    const long long n = items(s.b, false);
+    if (s.begin < s.seq_first + n) break;
+    s.seq_first += n;
+    ++s.b;
+  }
+  return s;
+}
+
 template <class Items>
 __device__ __forceinline__ Share take_share(int B, int me, int W, int least, SplitSmem &sm, Items items,
                                             long long *total = nullptr) {
@@ -65,25 +90,8 @@ __device__ __forceinline__ Share take_share(int B, int me, int W, int least, Spl
   }
   if (threadIdx.x == 0) sm.scan[0] = 0;
   __syncthreads();
-  const long long T = sm.scan[kSplitThreads];
-  if (total != nullptr) *total = T;
-  const Shares sh(T, W, least);
-  Share s{sh.begin(me), min(sh.begin(me + 1), T), 0, 0};
-  if (s.begin >= s.end) return s;
-  int lo = 0, hi = kSplitThreads - 1;  // the last run that starts at or before the share
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sm.scan[mid] <= s.begin) lo = mid; else hi = mid - 1;
-  }
-  s.b = lo * run;
-  s.seq_first = sm.scan[lo];
-  for (;;) {
-    const long long n = items(s.b, false);
-    if (s.begin < s.seq_first + n) break;
-    s.seq_first += n;
-    ++s.b;
-  }
-  return s;
+  if (total != nullptr) *total = sm.scan[kSplitThreads];
+  return find_share(B, me, W, least, sm, items);
 }
 
 }  // namespace kv4
