@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(256) block8_append_rows_kernel(
 // ---------------------------------------------------------------------------
 // attention: the split of a batch over warps
 // ---------------------------------------------------------------------------
-// A unit is 8 query rows of one (sequence, kv head): row r = position i * G + query head g
+// A unit is 8 (or 16) query rows of one (sequence, kv head): row r = position i * G + query head g
 // of the sequence's last n positions. Every unit reads the sequence's pages, so the batch
 // is T = sum over sequences of units * pages; warp w takes the w-th of W contiguous, equal
 // shares (to one page). A unit inside one warp's share is finished there; of a unit that
@@ -225,11 +225,12 @@ struct Seq8 : SeqRows {
   int units;  // per kv head
 };
 
-__device__ __forceinline__ Seq8 seq_of(const CacheView &c, const Queries &qs, int b, int32_t *err) {
+__device__ __forceinline__ Seq8 seq_of(const CacheView &c, const Queries &qs, int unit_rows, int b,
+                                       int32_t *err) {
   Seq8 s;
   static_cast<SeqRows &>(s) = rows_of(c, qs, b, err);
   s.pages = max(1, (s.L + kPage - 1) / kPage);
-  s.units = (s.n * c.gqa + kCols - 1) / kCols;
+  s.units = static_cast<int>((static_cast<long long>(s.n) * c.gqa + unit_rows - 1) / unit_rows);
   return s;
 }
 
@@ -243,18 +244,29 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-constexpr int kStages8 = 4;                               // pages in flight per warp
-constexpr int kStage8Bytes = 2 * kInt8CodeBytes;          // K then V of one (page, kv head)
+constexpr int kPair = 2;                                  // pages a warp takes at a time
+constexpr int kStages8 = 2;                               // pairs in flight per warp
+constexpr int kPage8Bytes = 2 * kInt8CodeBytes;           // K then V of one (page, kv head)
+constexpr int kStage8Bytes = kPair * kPage8Bytes;
 constexpr int kWarp8Smem = kStages8 * kStage8Bytes;
 constexpr int kCta8Smem = kWarps * kWarp8Smem;
-// The weights p = 2^(s - m) enter PV in fp16 as p * 2^14: 11 significant bits down to
-// p = 2^-28, and at most 16384. The running maximum is kept as m - 14, which makes
-// (m - 14, l 2^14, acc 2^14) the same softmax state.
+// The weights p = 2^(s - m) enter PV in fp16 as p * 2^14 * vs / 2^vref, vref the exponent of
+// the largest value scale so far (at most 2^14; 11 significant bits down to 2^-14). The
+// running maximum is kept as m - 14, which makes (m - 14, l 2^14, acc 2^14) the same state.
 constexpr float kLift8 = 14.0f;
 
-template <int F>
-__global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
+// One warp's share of a batch. NT groups of 8 query rows share each page's operands.
+//   QK^T  INT8: integer MMAs on the codes as they are; the query as 23-bit fixed point (its
+//         largest element below 2^22 steps) in three limbs, so that a logit is exact to 2^-23
+//         of its largest products. e4m3: fp16 MMAs, codes converted, the query a power of two
+//         from its bf16 value; both exact but for the fp32 sums.
+//   PV    fp16 MMAs on the converted codes, fp32 accumulators.
+// Bound by the reading of the pages; two pages (32 positions) per softmax step, so that the
+// cross-lane maximum, the waits and the copies' bookkeeping are paid once for 8 KB.
+template <int F, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kernel(
     CacheView c, Queries qs, Outputs out, float *__restrict__ partials, int32_t *err) {
+  constexpr int ROWS = kCols * NT;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitSmem split;
   __shared__ uint64_t bars_all[kWarps][kStages8];
@@ -270,13 +282,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
   auto items = [&](const Seq8 &s) { return static_cast<long long>(s.units) * s.pages * H; };
   const int me = blockIdx.x * kWarps + warp;
   const Share share = take_share(B, me, gridDim.x * kWarps, kMinShare, split, [&](int i, bool check) {
-    return items(seq_of(c, qs, i, check && blockIdx.x == 0 ? err : nullptr));
+    return items(seq_of(c, qs, ROWS, i, check && blockIdx.x == 0 ? err : nullptr));
   });
   const long long t_begin = share.begin, t_end = share.end;
   if (t_begin >= t_end) return;
   int b = share.b;
   long long seq_first = share.seq_first;  // first item of sequence b
-  Seq8 sq = seq_of(c, qs, b, nullptr);
+  Seq8 sq = seq_of(c, qs, ROWS, b, nullptr);
 
   uint32_t parity = 0;
   const int mi = lane >> 3, r8 = lane & 7;
@@ -285,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
   for (long long t = t_begin; t < t_end;) {
     while (t >= seq_first + items(sq)) {
       seq_first += items(sq);
-      sq = seq_of(c, qs, ++b, nullptr);
+      sq = seq_of(c, qs, ROWS, ++b, nullptr);
     }
     // unit (h, u) of the sequence: its pages pg0 .. pg1-1 are this warp's
     const long long in_seq = t - seq_first;
@@ -294,65 +306,57 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
     const int pg1 = static_cast<int>(min(static_cast<long long>(sq.pages), pg0 + (t_end - t)));
     const int h = unit / sq.units, u = unit - h * sq.units;
     const bool whole = pg0 == 0 && pg1 == sq.pages;
-    const int np = sq.L > 0 ? pg1 - pg0 : 0;
+    const int np = sq.L > 0 ? pg1 - pg0 : 0, pairs = (np + kPair - 1) / kPair;
     const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages + pg0;
 
-    // page ids and scales of 32 pages at a time, page k in lane k % 32
-    int pid = -1;
-    float ks_l = 0.f, vs_l = 0.f;
-    auto load_pages = [&](int k0) {
-      pid = -1;
-      ks_l = vs_l = 0.f;
+    // page ids and scales of 32 pages at a time, page k in lane k % 32; the ids of the next 32
+    // are there early, for the copies that start ahead
+    int pid = -1, pid_next = -1, block0 = 0;
+    float ks_l = 0.f, cv_l = 0.f, vref = -30.f;
+    auto load_ids = [&](int k0) {
+      int p = -1;
       if (k0 + lane < np) {
-        pid = pt[k0 + lane];
-        if (pid < 0 || pid >= c.num_pages) {
+        p = pt[k0 + lane];
+        if (p < 0 || p >= c.num_pages) {
           set_err(err, KV4_DEVERR_PAGE_ID);
-          pid = -1;  // the page's positions are left out
-        } else {
-          ks_l = __half2float(__ushort_as_half(c.k_params[static_cast<size_t>(pid) * H + h]));
-          vs_l = __half2float(__ushort_as_half(c.v_params[static_cast<size_t>(pid) * H + h]));
+          p = -1;  // the page's positions are left out
         }
       }
+      return p;
     };
-    int pid_next = -1;  // ids of the 32 pages after those (their copies start early)
-    auto load_next = [&](int k0) {
-      pid_next = -1;
-      if (k0 + lane < np) {
-        pid_next = pt[k0 + lane];
-        if (pid_next < 0 || pid_next >= c.num_pages) pid_next = -1;
-      }
-    };
-    int block0 = 0;  // first page of pid's 32
-    auto issue = [&](int k) {
-      const int p_now = __shfl_sync(0xffffffffu, pid, k & 31);
-      const int p_nxt = __shfl_sync(0xffffffffu, pid_next, k & 31);
-      const int pk = k - block0 < 32 ? p_now : p_nxt;
-      const int st = k % kStages8;
+    auto issue = [&](int j) {  // the copies of pair j
+      const int k = kPair * j, st = j % kStages8;
+      const int from = k - block0 < 32 ? pid : pid_next;
+      const int p0 = __shfl_sync(0xffffffffu, from, k & 31), p1 = __shfl_sync(0xffffffffu, from, (k & 31) + 1);
       if (lane == 0) {
         uint8_t *dst = stage0 + st * kStage8Bytes;
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&bars[st], pk < 0 ? 0 : kStage8Bytes);
-        if (pk >= 0) {
-          const size_t off = (static_cast<size_t>(pk) * H + h) * kInt8CodeBytes;
+        mbar_arrive_expect_tx(&bars[st], ((p0 >= 0) + (p1 >= 0)) * kPage8Bytes);
+        if (p0 >= 0) {
+          const size_t off = (static_cast<size_t>(p0) * H + h) * kInt8CodeBytes;
           bulk_g2s(dst, c.k_codes + off, kInt8CodeBytes, &bars[st]);
           bulk_g2s(dst + kInt8CodeBytes, c.v_codes + off, kInt8CodeBytes, &bars[st]);
         }
+        if (p1 >= 0) {
+          const size_t off = (static_cast<size_t>(p1) * H + h) * kInt8CodeBytes;
+          bulk_g2s(dst + kPage8Bytes, c.k_codes + off, kInt8CodeBytes, &bars[st]);
+          bulk_g2s(dst + kPage8Bytes + kInt8CodeBytes, c.v_codes + off, kInt8CodeBytes, &bars[st]);
+        }
       }
     };
-    load_pages(0);
-    load_next(32);
-    int issued = min(np, kStages8);
-    for (int k = 0; k < issued; ++k) issue(k);
+    pid = load_ids(0);
+    int issued = min(pairs, kStages8);
+    for (int j = 0; j < issued; ++j) issue(j);
+    pid_next = load_ids(32);
 
-    // ---- query fragments: column gid = query row u * 8 + gid, scaled by a power of two to
-    // [2^14, 2^15) at its largest element, so that its bf16 elements are exact in fp16 (what
-    // is under 2^-31 of the largest loses bits that no logit shows) ----
+    // ---- query operands: column gid of group g = query row u * ROWS + 8g + gid ----
     const int rows = sq.n * G;
-    const int r = u * kCols + gid;
-    uint32_t qb[8][2];
-    float kq[2];
-    int lim[2];  // last position the columns 2tig, 2tig + 1 see
-    {
+    uint32_t q8[NT][F == kFmtInt8 ? 3 : 1][F == kFmtInt8 ? 4 : 8][2];
+    float kq[NT][2];
+    int lim[NT][2], lim_least = sq.L - 1;  // last position the columns 2tig, 2tig + 1 see
+#pragma unroll
+    for (int g = 0; g < NT; ++g) {
+      const int r = u * ROWS + 8 * g + gid;
       const bool live = r < rows;
       const uint16_t *qrow = qs.q + (static_cast<size_t>(sq.row0 + r / G) * H * G + h * G + r % G) * kHeadDim;
       float qv[8][4];
@@ -364,154 +368,277 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block8_attn_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(qv[cc][i]));
       }
-      const float step = half_range_step(amax);
-      const float inv = 1.0f / step;               // a power of two: exact
+      // the largest element over half_range_step is in [2^14, 2^15): 2^7 times finer for INT8
+      const float step = F == kFmtInt8 ? half_range_step(amax) * 0.0078125f : half_range_step(amax);
+      const float inv = 1.0f / step;  // a power of two: exact
 #pragma unroll
       for (int cc = 0; cc < 8; ++cc) {
-        qb[cc][0] = pack_h2(qv[cc][0] * inv, qv[cc][1] * inv);
-        qb[cc][1] = pack_h2(qv[cc][2] * inv, qv[cc][3] * inv);
+        if constexpr (F == kFmtInt8) {
+          uint32_t w[3] = {0u, 0u, 0u};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int qi = __float2int_rn(qv[cc][i] * inv);
+            w[0] |= (static_cast<uint32_t>(qi) & 0xFFu) << (8 * i);
+            w[1] |= (static_cast<uint32_t>(qi >> 8) & 0xFFu) << (8 * i);
+            w[2] |= (static_cast<uint32_t>(qi >> 16) & 0xFFu) << (8 * i);
+          }
+#pragma unroll
+          for (int x = 0; x < 3; ++x) q8[g][x][cc >> 1][cc & 1] = w[x];
+        } else {
+          q8[g][0][cc][0] = pack_h2(qv[cc][0] * inv, qv[cc][1] * inv);
+          q8[g][0][cc][1] = pack_h2(qv[cc][2] * inv, qv[cc][3] * inv);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        kq[e] = __shfl_sync(0xffffffffu, step, 4 * (2 * tig + e)) * kScaleLog2;
-        const int rc = u * kCols + 2 * tig + e;
-        lim[e] = rc < rows ? sq.L - sq.n + rc / G : -1;
+        kq[g][e] = __shfl_sync(0xffffffffu, step, 4 * (2 * tig + e)) * kScaleLog2;
+        const int rc = u * ROWS + 8 * g + 2 * tig + e;
+        lim[g][e] = rc < rows ? sq.L - sq.n + rc / G : -1;
+        lim_least = rc < rows ? min(lim_least, lim[g][e]) : lim_least;
       }
     }
-    float m[2] = {kNegBig, kNegBig}, l[2] = {0.f, 0.f};
-    float o[8][4];
+    lim_least = __reduce_min_sync(0xffffffffu, lim_least);
+    float m[NT][2], l[NT][2];
+    float o[NT][8][4];
 #pragma unroll
-    for (int cc = 0; cc < 8; ++cc) o[cc][0] = o[cc][1] = o[cc][2] = o[cc][3] = 0.f;
+    for (int g = 0; g < NT; ++g) {
+      m[g][0] = m[g][1] = kNegBig;
+      l[g][0] = l[g][1] = 0.f;
+#pragma unroll
+      for (int cc = 0; cc < 8; ++cc) o[g][cc][0] = o[g][cc][1] = o[g][cc][2] = o[g][cc][3] = 0.f;
+    }
 
     bool dead = false;
-    for (int j = 0; j < np; ++j) {
-      if (j - block0 == 32) {
-        block0 += 32;
-        load_pages(block0);
-        load_next(block0 + 32);
+    for (int j = 0; j < pairs; ++j) {
+      const int k = kPair * j;
+      if ((k & 31) == 0) {  // the next 32 pages' scales
+        if (k > 0) {
+          block0 = k;
+          pid = pid_next;
+          pid_next = load_ids(k + 32);
+        }
+        ks_l = cv_l = 0.f;
+        if (pid >= 0) {
+          ks_l = __half2float(__ushort_as_half(c.k_params[static_cast<size_t>(pid) * H + h]));
+          cv_l = __half2float(__ushort_as_half(c.v_params[static_cast<size_t>(pid) * H + h]));
+        }
+        // fp16 scales are non-negative: their order is that of their fp32 bits
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(cv_l));
+        const float e = static_cast<float>(static_cast<int>(top >> 23) - 126);  // all below 2^e
+        if (e > vref) {
+          const float f = fast_exp2(vref - e);
+#pragma unroll
+          for (int g = 0; g < NT; ++g)
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[g][cc][i] *= f;
+          vref = e;
+        }
+        cv_l *= fast_exp2(-vref);
       }
       const int st = j % kStages8;
       if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u)) {
         if (lane == 0) set_err(err, KV4_DEVERR_TIMEOUT);
-        for (int k = j; k < issued; ++k)  // let its copies in flight land before it ends
-          mbar_wait_bounded(&bars[k % kStages8], (parity >> (k % kStages8)) & 1u, kWaitLimit * 16u);
+        for (int i = j; i < issued; ++i)  // let its copies in flight land before it ends
+          mbar_wait_bounded(&bars[i % kStages8], (parity >> (i % kStages8)) & 1u, kWaitLimit * 16u);
         dead = true;
         break;
       }
       parity ^= 1u << st;
-      const bool bad = __shfl_sync(0xffffffffu, pid, j & 31) < 0;
-      const float ks = __shfl_sync(0xffffffffu, ks_l, j & 31);
-      const float vs = __shfl_sync(0xffffffffu, vs_l, j & 31);
-      if (!bad) {
-        const uint32_t sa = smem_u32(stage0 + st * kStage8Bytes);
-        const int tok0 = (pg0 + j) * kPage;
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t sa = smem_u32(stage0 + st * kStage8Bytes);
+      const int tok0 = (pg0 + k) * kPage;
+      float s[NT][kPair][2][2], cv[kPair];
+      bool there[kPair];  // the page was copied
 #pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
-          uint32_t kw[4];
-          ldsm_x4(kw, sa + pr * 512 + ld8);
+      for (int pp = 0; pp < kPair; ++pp) {
+        there[pp] = __shfl_sync(0xffffffffu, pid, (k & 31) + pp) >= 0;
+        const float ks = __shfl_sync(0xffffffffu, ks_l, (k & 31) + pp);
+        cv[pp] = __shfl_sync(0xffffffffu, cv_l, (k & 31) + pp);
+        float d[NT][4];
+        const uint32_t sk = sa + pp * kPage8Bytes + ld8;
+        if constexpr (F == kFmtInt8) {
+          int32_t a2[NT][4] = {}, a1[NT][4] = {}, a0[NT][4] = {};
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t a01, a23, a45, a67;
-            code_pairs<F, false>(kw[2 * hf], a01, a45);
-            code_pairs<F, false>(kw[2 * hf + 1], a23, a67);
-            mma_f16(d, a01, a23, a45, a67, qb[2 * pr + hf][0], qb[2 * pr + hf][1]);
+          for (int x = 0; x < 4; ++x) {
+            uint32_t kw[4];
+            ldsm_x4(kw, sk + x * 512);
+#pragma unroll
+            for (int g = 0; g < NT; ++g) {
+              mma_s8s8(a2[g], kw[0], kw[1], kw[2], kw[3], q8[g][2][x][0], q8[g][2][x][1]);
+              mma_s8u8(a1[g], kw[0], kw[1], kw[2], kw[3], q8[g][1][x][0], q8[g][1][x][1]);
+              mma_s8u8(a0[g], kw[0], kw[1], kw[2], kw[3], q8[g][0][x][0], q8[g][0][x][1]);
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < NT; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // (the low limbs' sums stay below 2^31: 255 * 127 * 128 * 257)
+              d[g][i] = fmaf(static_cast<float>(a2[g][i]), 65536.f, static_cast<float>(a1[g][i] * 256 + a0[g][i]));
+        } else {
+#pragma unroll
+          for (int g = 0; g < NT; ++g) d[g][0] = d[g][1] = d[g][2] = d[g][3] = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t kw[4];
+            ldsm_x4(kw, sk + x * 512);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t a01, a23, a45, a67;
+              code_pairs<F, false>(kw[2 * hf], a01, a45);
+              code_pairs<F, false>(kw[2 * hf + 1], a23, a67);
+#pragma unroll
+              for (int g = 0; g < NT; ++g)
+                mma_f16(d[g], a01, a23, a45, a67, q8[g][0][2 * x + hf][0], q8[g][0][2 * x + hf][1]);
+            }
           }
         }
-        float s[2][2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
+        for (int g = 0; g < NT; ++g) {
+          const float f0 = ks * kq[g][0], f1 = ks * kq[g][1];
+          s[g][pp][0][0] = d[g][0] * f0;
+          s[g][pp][0][1] = d[g][1] * f1;
+          s[g][pp][1][0] = d[g][2] * f0;
+          s[g][pp][1][1] = d[g][3] * f1;
+        }
+      }
+      const bool tail = tok0 + kPair * kPage > sq.L || !there[0] || !there[1];
+      if (tail || tok0 + kPair * kPage - 1 > lim_least) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            s[hf][e] = tok0 + gid + 8 * hf <= lim[e] ? d[2 * hf + e] * (ks * kq[e]) : -CUDART_INF_F;
-        float a[2];
-        softmax_step(s, m, l, a, kLift8);
-        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+        for (int g = 0; g < NT; ++g)
+#pragma unroll
+          for (int pp = 0; pp < kPair; ++pp)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!there[pp] || tok0 + kPage * pp + 8 * hf + gid > lim[g][e]) s[g][pp][hf][e] = -CUDART_INF_F;
+      }
+      uint32_t pb[NT][kPair][2];  // the weights as B operands
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        float al[2];
+        bool moved = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(s[g][0][0][e], s[g][0][1][e]), fmaxf(s[g][1][0][e], s[g][1][1][e]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[g][e], x - kLift8);  // running maximum kept as max - 14
+          al[e] = fast_exp2(m[g][e] - mn);
+          moved |= mn != m[g][e];
+          m[g][e] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int pp = 0; pp < kPair; ++pp)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              s[g][pp][hf][e] = fast_exp2(s[g][pp][hf][e] - mn);
+              sum += s[g][pp][hf][e];
+            }
+          l[g][e] = fmaf(l[g][e], al[e], sum);
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+          const float2 a2 = make_float2(al[0], al[1]);
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc) {
-            o[cc][0] *= a[0]; o[cc][1] *= a[1]; o[cc][2] *= a[0]; o[cc][3] *= a[1];
+            const float2 x = fmul2(make_float2(o[g][cc][0], o[g][cc][1]), a2);
+            const float2 y = fmul2(make_float2(o[g][cc][2], o[g][cc][3]), a2);
+            o[g][cc][0] = x.x; o[g][cc][1] = x.y; o[g][cc][2] = y.x; o[g][cc][3] = y.y;
           }
         }
         // P (tokens x columns) to the B operand (columns' tokens in pairs)
-        const uint32_t b01 = transpose8x8(pack_h2(s[0][0], s[0][1]));
-        const uint32_t b23 = transpose8x8(pack_h2(s[1][0], s[1][1]));
-        // the slots behind the length may hold anything (e4m3 NaN codes): zero them
+#pragma unroll
+        for (int pp = 0; pp < kPair; ++pp)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            pb[g][pp][hf] = transpose8x8(pack_h2(s[g][pp][hf][0] * cv[pp], s[g][pp][hf][1] * cv[pp]));
+      }
+#pragma unroll
+      for (int pp = 0; pp < kPair; ++pp) {
+        // e4m3: the slots behind the length, and a page that was not copied, may hold NaN codes
         uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;  // tokens 2tig, +1 and 8 + those
-        if (tok0 + kPage > sq.L) {
-          const int left = sq.L - tok0;
+        if (F == kFmtE4m3 && tail) {
+          const int left = there[pp] ? sq.L - tok0 - kPage * pp : 0;
           keep_lo = (2 * tig < left ? 0xFFFFu : 0u) | (2 * tig + 1 < left ? 0xFFFF0000u : 0u);
           keep_hi = (2 * tig + 8 < left ? 0xFFFFu : 0u) | (2 * tig + 9 < left ? 0xFFFF0000u : 0u);
         }
 #pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
+        for (int x = 0; x < 4; ++x) {
           uint32_t vw[4];
-          ldsm_x4_t(vw, sa + kInt8CodeBytes + pr * 512 + ld8);
+          ldsm_x4_t(vw, sa + pp * kPage8Bytes + kInt8CodeBytes + x * 512 + ld8);
+          if (F == kFmtE4m3 && tail) {
+            vw[0] &= keep_lo; vw[1] &= keep_hi; vw[2] &= keep_lo; vw[3] &= keep_hi;
+          }
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t a01, a23, a45, a67;
-            code_pairs<F, true>(vw[2 * hf] & keep_lo, a01, a23);
-            code_pairs<F, true>(vw[2 * hf + 1] & keep_hi, a45, a67);
-            float t4[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(t4, a01, a23, a45, a67, b01, b23);
-            float (&oo)[4] = o[2 * pr + hf];
+            code_pairs<F, true>(vw[2 * hf], a01, a23);
+            code_pairs<F, true>(vw[2 * hf + 1], a45, a67);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) oo[i] = fmaf(vs, t4[i], oo[i]);
+            for (int g = 0; g < NT; ++g)
+              mma_f16(o[g][2 * x + hf], a01, a23, a45, a67, pb[g][pp][0], pb[g][pp][1]);
           }
         }
       }
       __syncwarp();
-      if (issued < np) issue(issued++);  // the stage is free again
+      if (issued < pairs) issue(issued++);  // the stage is free again
     }
     if (dead) return;
 
+    const float undo = fast_exp2(vref);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int g = 0; g < NT; ++g)
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int col = 2 * tig + e, rc = u * kCols + col;
-      if (whole) {
+        for (int off = 4; off < 32; off <<= 1) l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], off);
+        const int col = 8 * g + 2 * tig + e, rc = u * ROWS + col;
         if (rc >= rows) continue;
-        const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
-        const float inv = l[e] > 0.f ? 1.0f / l[e] : 0.f;
+        if (whole) {
+          const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
+          const float inv = l[g][e] > 0.f ? undo / l[g][e] : 0.f;
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {  // C rows gid, gid + 8: dims 16cc + 2gid, + 1
-          const float x = o[cc][e] * inv, y = o[cc][2 + e] * inv;
-          *reinterpret_cast<__nv_bfloat162 *>(out.out + qr * kHeadDim + 16 * cc + 2 * gid) =
-              __floats2bfloat162_rn(x, y);
-          if (out.out_f32)
-            *reinterpret_cast<float2 *>(out.out_f32 + qr * kHeadDim + 16 * cc + 2 * gid) = make_float2(x, y);
+          for (int cc = 0; cc < 8; ++cc) {  // C rows gid, gid + 8: dims 16cc + 2gid, + 1
+            const float x = o[g][cc][e] * inv, y = o[g][cc][2 + e] * inv;
+            *reinterpret_cast<__nv_bfloat162 *>(out.out + qr * kHeadDim + 16 * cc + 2 * gid) =
+                __floats2bfloat162_rn(x, y);
+            if (out.out_f32)
+              *reinterpret_cast<float2 *>(out.out_f32 + qr * kHeadDim + 16 * cc + 2 * gid) = make_float2(x, y);
+          }
+          if (out.lse && gid == 0) out.lse[qr] = l[g][e] > 0.f ? m[g][e] * kLn2 + logf(l[g][e]) : -CUDART_INF_F;
+        } else {
+          float *rec = partials + (static_cast<size_t>(2 * me + (t == t_begin ? 0 : 1)) * ROWS + col) *
+                                      kRecordFloats;
+#pragma unroll
+          for (int cc = 0; cc < 8; ++cc)
+            st_rec(reinterpret_cast<float2 *>(rec + 16 * cc + 2 * gid),
+                   make_float2(o[g][cc][e] * undo, o[g][cc][2 + e] * undo));
+          if (gid == 0) st_rec(reinterpret_cast<float2 *>(rec + kHeadDim), make_float2(m[g][e], l[g][e]));
         }
-        if (out.lse && gid == 0) out.lse[qr] = l[e] > 0.f ? m[e] * kLn2 + logf(l[e]) : -CUDART_INF_F;
-      } else {
-        float *rec = partials + (static_cast<size_t>(2 * me + (t == t_begin ? 0 : 1)) * kCols + col) *
-                                    kRecordFloats;
-#pragma unroll
-        for (int cc = 0; cc < 8; ++cc)
-          st_rec(reinterpret_cast<float2 *>(rec + 16 * cc + 2 * gid), make_float2(o[cc][e], o[cc][2 + e]));
-        if (gid == 0) st_rec(reinterpret_cast<float2 *>(rec + kHeadDim), make_float2(m[e], l[e]));
       }
-    }
     t += pg1 - pg0;
   }
 }
 
 // Where warp blockIdx.x + 1's share starts inside a unit that starts in the share before it,
 // the block joins that unit's records (a unit over more warps is the first such warp's to join).
+template <int NT>
 __global__ void __launch_bounds__(kSplitThreads) block8_merge_kernel(CacheView c, Queries qs, Outputs out,
                                                                      const float *__restrict__ partials,
                                                                      int attn_warps) {
+  constexpr int ROWS = kCols * NT;
   __shared__ SplitSmem split;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = c.gqa, H = c.num_kv_heads, me = blockIdx.x + 1;
   long long T;
   const Share share = take_share(c.num_seqs, me, attn_warps, kMinShare, split, [&](int i, bool) {
-    const Seq8 s = seq_of(c, qs, i, nullptr);
+    const Seq8 s = seq_of(c, qs, ROWS, i, nullptr);
     return static_cast<long long>(s.units) * s.pages * H;
   }, &T);
   if (share.begin >= share.end) return;
-  const Seq8 sq = seq_of(c, qs, share.b, nullptr);
+  const Seq8 sq = seq_of(c, qs, ROWS, share.b, nullptr);
   const long long in_seq = share.begin - share.seq_first;
   const int unit = static_cast<int>(in_seq / sq.pages);
   const int pg0 = static_cast<int>(in_seq - static_cast<long long>(unit) * sq.pages);
@@ -521,10 +648,10 @@ __global__ void __launch_bounds__(kSplitThreads) block8_merge_kernel(CacheView c
   if (sh.owner(t0) != me - 1) return;
   const int w1 = sh.owner(t0 + sq.pages - 1);
   const int h = unit / sq.units, u = unit - h * sq.units;
-  for (int col = warp; col < kCols && u * kCols + col < sq.n * G; col += kSplitThreads / 32) {
-    const int r = u * kCols + col;
+  for (int col = warp; col < ROWS && u * ROWS + col < sq.n * G; col += kSplitThreads / 32) {
+    const int r = u * ROWS + col;
     const size_t qr = static_cast<size_t>(sq.row0 + r / G) * H * G + h * G + r % G;
-    join_records(partials, kCols, col, me - 1, w1, [&](int w) { return sh.begin(w) >= t0 ? 0 : 1; }, out, qr,
+    join_records(partials, ROWS, col, me - 1, w1, [&](int w) { return sh.begin(w) >= t0 ? 0 : 1; }, out, qr,
                  lane);
   }
 }
@@ -554,47 +681,57 @@ cudaError_t launch_block8_append(int fmt, const CacheView &c, const uint16_t *k_
                          : launch_block8_append_t<kFmtE4m3>(c, k_new, v_new, indptr, total_new, err, s);
 }
 
-// Warps of the attention grid for a batch of at most T_max items.
+// Warps of the attention grid for a batch of at most t_max items.
 static int attn_warps(long long t_max) {
   const long long w = std::max(1LL, std::min<long long>(kAttnWarps, t_max / kMinShare));
   return static_cast<int>((w + kWarps - 1) / kWarps * kWarps);
 }
 
-static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, int G) {
-  const long long units = (static_cast<long long>(total_q) * G + kCols - 1) / kCols + num_seqs;
+static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, int G, int rows) {
+  const long long units = (static_cast<long long>(total_q) * G + rows - 1) / rows + num_seqs;
   return units * H * std::max(1, (max_seq_len + kPage - 1) / kPage);
 }
 
+// Two records of each warp, of the larger of the two unit sizes.
+static size_t warp_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G) {
+  size_t bytes = 0;
+  for (int rows = kCols; rows <= 2 * kCols; rows += kCols) {
+    const size_t n = 2u * attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G, rows));
+    bytes = std::max(bytes, (n * rows * kRecordFloats * sizeof(float) + 255) / 256 * 256);
+  }
+  return bytes;
+}
+
 size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_seq_len, int H, int G) {
-  const size_t n = 2u * attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G));
-  const size_t bytes = (n * kCols * kRecordFloats * sizeof(float) + 255) / 256 * 256;
+  const size_t bytes = warp_workspace_bytes(num_seqs, total_q, max_seq_len, H, G);
   if (static_cast<long long>(max_q_len) * G <= kWarpRows) return bytes;
   return std::max(bytes, tile_workspace_bytes(num_seqs, total_q, max_seq_len, H, G));
 }
 
-template <int F>
-static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, int ctas,
+template <int F, int NT>
+static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, int max_seq_len,
                                         const Outputs &out, float *partials, int32_t *err,
                                         cudaStream_t s) {
   static PerDevice grids;
   int most = 0;
   cudaError_t e = once_per_device(grids, [](int dev, int *g) {
-    cudaError_t r = cudaFuncSetAttribute(block8_attn_kernel<F>,
+    cudaError_t r = cudaFuncSetAttribute(block8_attn_kernel<F, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kCta8Smem);
     int sms = 0, per_sm = 0;
     if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (r == cudaSuccess)
-      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block8_attn_kernel<F>, kWarps * 32,
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block8_attn_kernel<F, NT>, kWarps * 32,
                                                         kCta8Smem);
     *g = sms * (per_sm > 0 ? per_sm : 1);
     return r;
   }, &most);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(ctas, most);
-  block8_attn_kernel<F><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, err);
+  const long long bound = items_bound(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa, kCols * NT);
+  const int grid = std::min(attn_warps(bound) / kWarps, most);
+  block8_attn_kernel<F, NT><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, err);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  block8_merge_kernel<<<grid * kWarps - 1, kSplitThreads, 0, s>>>(c, qs, out, partials, grid * kWarps);
+  block8_merge_kernel<NT><<<grid * kWarps - 1, kSplitThreads, 0, s>>>(c, qs, out, partials, grid * kWarps);
   return cudaGetLastError();
 }
 
@@ -602,13 +739,15 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
                                     const int32_t *q_indptr, int total_q, int max_q_len,
                                     int max_seq_len, const Outputs &out, void *workspace,
                                     int32_t *err, cudaStream_t s) {
-  const int ctas = attn_warps(items_bound(c.num_seqs, total_q, max_seq_len, c.num_kv_heads, c.gqa)) / kWarps;
-  float *partials = static_cast<float *>(workspace);
   const Queries qs{q, q_indptr, total_q, max_q_len};
-  if (static_cast<long long>(max_q_len) * c.gqa > kWarpRows)
-    return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, err, s);
-  return fmt == kFmtInt8 ? launch_block8_attn_t<kFmtInt8>(c, qs, ctas, out, partials, err, s)
-                         : launch_block8_attn_t<kFmtE4m3>(c, qs, ctas, out, partials, err, s);
+  const long long rows = static_cast<long long>(max_q_len) * c.gqa;
+  if (rows > kWarpRows) return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, err, s);
+  float *p = static_cast<float *>(workspace);
+  if (fmt == kFmtInt8)
+    return rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1>(c, qs, max_seq_len, out, p, err, s)
+                         : launch_block8_attn_t<kFmtInt8, 2>(c, qs, max_seq_len, out, p, err, s);
+  return rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1>(c, qs, max_seq_len, out, p, err, s)
+                       : launch_block8_attn_t<kFmtE4m3, 2>(c, qs, max_seq_len, out, p, err, s);
 }
 
 }  // namespace kv4

@@ -80,23 +80,44 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &a, uint32_t &b)
 
 // Joins the partial records (max in log2 units, sum, weighted values) of one row of a unit that
 // workers w0 .. w1 share, in that order, and writes the row. Records: [2 per worker][rows][132];
-// slot(w): which of worker w's two.
+// slot(w): which of worker w's two. 32 records at a time: their maxima and sums by the lanes
+// first, so that the loads of the values wait for nothing but their own batch.
 template <class Slot>
 __device__ __forceinline__ void join_records(const float *__restrict__ partials, int rows, int x, int w0,
                                              int w1, Slot slot, const Outputs &out, size_t qr, int lane) {
   float mm = kNegBig, ll = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int w = w0; w <= w1; ++w) {
-    const float *rec = partials + ((2 * static_cast<size_t>(w) + slot(w)) * rows + x) * kRecordFloats;
-    const float2 ml = *reinterpret_cast<const float2 *>(rec + kHeadDim);
-    const float4 v = *reinterpret_cast<const float4 *>(rec + 4 * lane);
-    if (ml.y <= 0.f) continue;  // nothing visible there
-    const float mn = fmaxf(mm, ml.x);
-    const float a = fast_exp2(mm - mn), e = fast_exp2(ml.x - mn);
-    ll = ll * a + ml.y * e;
-    acc.x = acc.x * a + v.x * e; acc.y = acc.y * a + v.y * e;
-    acc.z = acc.z * a + v.z * e; acc.w = acc.w * a + v.w * e;
+  for (int w = w0; w <= w1; w += 32) {
+    const int n = min(32, w1 - w + 1);
+    size_t at = 0;
+    float2 ml = make_float2(kNegBig, 0.f);
+    if (lane < n) {
+      at = ((2 * static_cast<size_t>(w + lane) + slot(w + lane)) * rows + x) * kRecordFloats;
+      ml = *reinterpret_cast<const float2 *>(partials + at + kHeadDim);
+      if (ml.y <= 0.f) ml.x = kNegBig;  // nothing visible there
+    }
+    float mx = ml.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    const float mn = fmaxf(mm, mx);
+    const float a = fast_exp2(mm - mn);
+    const float e = ml.y > 0.f ? fast_exp2(ml.x - mn) : 0.f;
+    float sum = ml.y * e;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    ll = ll * a + sum;
+    acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
     mm = mn;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float f = __shfl_sync(0xffffffffu, e, i);
+      const size_t r = __shfl_sync(0xffffffffu, at, i);
+      const float4 v = *reinterpret_cast<const float4 *>(partials + r + 4 * lane);
+      if (f > 0.f) {
+        acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+      }
+    }
   }
   const float inv = ll > 0.f ? 1.0f / ll : 0.f;
   acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
@@ -114,6 +135,6 @@ cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs
 
 // Up to this many query rows (positions x query heads of a kv head) of a sequence the warp
 // kernel takes the call, beyond it the tile kernel.
-constexpr int kWarpRows = 8;
+constexpr int kWarpRows = 64;
 
 }  // namespace kv4

@@ -785,7 +785,7 @@ static cudaError_t launch_tile_t(const CacheView &c, const Queries &qs, int max_
 cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs, int max_seq_len,
                                   const Outputs &out, void *workspace, int32_t *err, cudaStream_t s) {
   float *p = static_cast<float *>(workspace);
-  const bool shared = static_cast<long long>(qs.max_n) * c.gqa > kTile;
+  const bool shared = true || static_cast<long long>(qs.max_n) * c.gqa > kTile;
   if (fmt == kFmtInt8)
     return shared ? launch_tile_t<kFmtInt8, true>(c, qs, max_seq_len, out, p, err, s)
                   : launch_tile_t<kFmtInt8, false>(c, qs, max_seq_len, out, p, err, s);

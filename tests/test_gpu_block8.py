@@ -156,15 +156,11 @@ class Model:
             ds = (130 * 2.0 ** -24 + 2.0 ** -21) * mag + 2.0 ** -21
             # output: weights off by e^ds, rounded to fp16 (2^-11), sums in fp32 over L rows
             to = (2.0 ** -11 + 2 * ds[..., None] + (K.shape[0] + 64) * 2.0 ** -24) * A + 1e-30
-            # a weight under 2^-28 of the largest is an fp16 subnormal of p * 2^14, rounded by at
-            # most 2^-25 there: 2^-39 of the largest weight for each row (the largest one's value
-            # may be 0 where A is then made of such weights alone)
-            to += 2.0 ** -39 * np.repeat(np.abs(V).sum(0), self.G, 0)
-            # more than 8 query rows of a kv head: the weights carry the value scales, p 2^7 vs /
-            # 2^e with 2^e at most twice the largest scale, and an fp16 subnormal of that is off by
-            # at most 2^-25: 2^-31 of the largest scale for each code
-            if max(n) * self.G > 8:
-                to += 2.0 ** -31 * np.repeat(self.code_sums(b), self.G, 0)
+            # the weights carry the value scales in fp16: p 2^14 vs / 2^e (up to 64 query rows of a
+            # kv head) or p 2^7 vs / 2^e, with 2^e at most twice the largest scale. A subnormal of
+            # that is off by at most 2^-25: 2^-38 or 2^-31 of the largest scale for each code (which
+            # shows where the largest weights' values are 0)
+            to += 2.0 ** (-38 if max(n) * self.G <= 64 else -31) * np.repeat(self.code_sums(b), self.G, 0)
             assert np.all(np.abs(o32[sl] - Or) <= to), (b, (np.abs(o32[sl] - Or) / to).max())
             assert np.all(np.abs(out[sl] - Or) <= to + 2.0 ** -8 * np.abs(Or)), b
             seen = np.isfinite(lr)
@@ -264,6 +260,10 @@ ATTEND = [
     ("chunk", [200, 77, 130], 1, 4, [130, 77, 33]),
     ("chunk-gqa8", [300, 20], 2, 8, [70, 20]),
     ("chunk-gqa3", [333, 257], 1, 3, [300, 1]),
+    ("rows-9-to-16", [900, 40, 33, 700], 2, 4, [4, 3, 1, 4]),
+    ("rows-17-to-64", [900, 40, 1500, 16], 2, 8, [8, 7, 3, 8]),
+    ("rows-65", [300, 65, 400], 2, 1, [65, 65, 2]),
+    ("rows-128", [300, 128, 400], 1, 4, [32, 32, 31]),
     ("prefill-ragged", [400, 1, 513], 2, 2, [400, 1, 257]),
 ]
 
@@ -346,7 +346,7 @@ def test_attention_refuses_bad_rows_and_lengths():
                                   ([65, 60], [0, 2, 4], 2, [2, 3]), ([-1, 60], [0, 2, 4], 2, [2, 3])):
         q = torch.randn((6, 4, 128), device="cuda").to(torch.bfloat16)
         out, lse = torch.full_like(q, 7.0), torch.full((6, 4), 7.0, device="cuda")
-        ws = torch.empty(kv4.block8_workspace_size(m.cfg, 2, 6, maxn, 60), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(kv4.block8_workspace_size(m.cfg, 2, 6, maxn, 65), dtype=torch.uint8, device="cuda")
         kv4.block8_attention(m.cache, m.batch(lens), q, out, ws, ints(ip), maxn, None, lse, m.err)
         torch.cuda.synchronize()
         assert int(m.err.item()) == 2
