@@ -454,9 +454,9 @@ kv4_status kv4_attention_weights(const kv4_config *cfg, const kv4_int4_pool *poo
  * keeps all; a longer one keeps `budget`: the S sinks, the R recent positions and the
  * budget - S - R of the rest with the largest totals (equal ones from the lowest position on;
  * NaN below everything, -0 equal to +0).
- *   batch:    seq_lens and num_seqs are read.
- *   acc:      fp32 [num_seqs][Hkv][acc_stride]; a sequence longer than acc_stride (or of a
- *             negative length) gets new_lens 0 and KV4_DEVERR_SEQ_LEN.
+ *   batch:    seq_lens, num_seqs and max_seq_len are read.
+ *   acc:      fp32 [num_seqs][Hkv][acc_stride]; a sequence longer than acc_stride or
+ *             max_seq_len (or of a negative length) gets new_lens 0 and KV4_DEVERR_SEQ_LEN.
  *   budget:   at least 1 and at least S + R.
  *   keep:     int32 [num_seqs][Hkv][budget], ascending, -1 behind the last.
  *   new_lens: int32 [num_seqs], min(seq_lens[b], budget); not the batch's seq_lens. */

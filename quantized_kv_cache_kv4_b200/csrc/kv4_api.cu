@@ -493,7 +493,7 @@ kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const
                             int32_t *err_flag, kv4_stream_t stream) {
   kv4_status st = check_config(cfg);
   if (st != KV4_OK) return st;
-  if (batch == nullptr || batch->num_seqs < 0 || acc_stride < 0 || budget < 1 ||
+  if (batch == nullptr || batch->num_seqs < 0 || batch->max_seq_len < 0 || acc_stride < 0 || budget < 1 ||
       budget < cfg->num_sinks + cfg->num_recent)
     return KV4_ERR_INVALID_ARG;
   if (batch->num_seqs == 0) return KV4_OK;
@@ -505,7 +505,7 @@ kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const
   v.num_kv_heads = cfg->num_kv_heads;
   v.num_sinks = cfg->num_sinks;
   v.num_recent = cfg->num_recent;
-  cudaError_t e = kv4::launch_select(v, acc, acc_stride, budget, keep, new_lens, err_flag,
+  cudaError_t e = kv4::launch_select(v, batch->max_seq_len, acc, acc_stride, budget, keep, new_lens, err_flag,
                                      reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
 }

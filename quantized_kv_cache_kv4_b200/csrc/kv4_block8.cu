@@ -88,55 +88,40 @@ __device__ __forceinline__ void rescale_block(uint8_t *block, int rows, float s_
   }
 }
 
-// New rows `first` .. first+n-1 (n <= 16 - slot) of one kv head into slots slot .. of block
-// (page, head) of one array. One warp; lane l holds dims 4l .. 4l+3.
-template <int F, int N>
-__device__ __forceinline__ void append_block(uint8_t *block, uint16_t *scale,
-                                             const uint16_t *__restrict__ rows, size_t row_stride,
-                                             int n, int slot, int lane) {
-  uint2 raw[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    raw[i] = i < n ? *reinterpret_cast<const uint2 *>(rows + i * row_stride + 4 * lane)
-                   : make_uint2(0u, 0u);
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float x[4];
-    unpack_bf16x4(raw[i], x);
-    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-  }
-  __half sh = block_scale<F>(warp_max(amax));
+// The scale of a block that gets rows of magnitude amax from slot `slot` on; the codes already
+// there are rounded again where it grows. (Lanes of one warp, all with the same arguments.)
+template <int F>
+__device__ __forceinline__ float grow_scale(uint8_t *block, uint16_t *scale, float amax, int slot, int lane) {
+  const __half sh = block_scale<F>(amax);
   float s = __half2float(sh);
-  const float s_old = slot > 0 ? __half2float(__ushort_as_half(*scale)) : 0.f;
-  if (slot > 0 && s <= s_old) {  // (a block's first slot starts its scale anew)
-    s = s_old;
-  } else {
+  if (slot > 0) {  // (a block's first slot starts its scale anew)
+    const float s_old = __half2float(__ushort_as_half(*scale));
+    if (s <= s_old) return s_old;
+    rescale_block<F>(block, slot, s_old, s, __frcp_rn(s), lane);
     __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale = __half_as_ushort(sh);
   }
-  const float y = s == 0.f ? 0.f : __frcp_rn(s);
-  if (slot > 0 && s > s_old) rescale_block<F>(block, slot, s_old, s, y, lane);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i >= n) break;
-    float x[4];
-    unpack_bf16x4(raw[i], x);
-    // [8 strips of 16 dims][16 slots][16 bytes]: lane l -> strip l / 4, bytes 4 (l % 4)
-    *reinterpret_cast<uint32_t *>(block + (lane >> 2) * (kPage * 16) + (slot + i) * 16 +
-                                  4 * (lane & 3)) = codes4<F>(x, s, y);
-  }
+  if (lane == 0) *scale = __half_as_ushort(sh);
+  return s;
 }
 
+__device__ __forceinline__ float amax4(const float (&x)[4]) {
+  return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+}
+
+// One warp per (sequence, kv head, K or V); lane l holds dims 4l .. 4l+3. Bound by its chain of
+// loads (length, page id, scale), so the row is asked for first.
 template <int F>
 __global__ void __launch_bounds__(256) block8_append_token_kernel(
     CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
     int32_t *err) {
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int H = c.num_kv_heads;
-  if (warp >= c.num_seqs * H) return;
-  const int b = warp / H, h = warp - b * H;
+  const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (warp >= 2LL * c.num_seqs * H) return;
+  const bool v = (warp & 1) != 0;
+  const int unit = static_cast<int>(warp >> 1), b = unit / H, h = unit - b * H;
+  const uint2 raw = *reinterpret_cast<const uint2 *>((v ? v_new : k_new) +
+                                                     static_cast<size_t>(unit) * kHeadDim + 4 * lane);
   const int L = c.seq_lens[b], pos = L - 1;
   if (pos < 0 || L > c.max_pages * kPage) {
     if (lane == 0) set_err(err, KV4_DEVERR_SEQ_LEN);
@@ -147,17 +132,38 @@ __global__ void __launch_bounds__(256) block8_append_token_kernel(
     if (lane == 0) set_err(err, KV4_DEVERR_PAGE_ID);
     return;
   }
+  const int slot = pos % kPage;
   const size_t blk = static_cast<size_t>(page) * H + h;
-  const size_t row = static_cast<size_t>(warp) * kHeadDim;
-  append_block<F, 1>(c.k_codes + blk * kInt8CodeBytes, c.k_params + blk, k_new + row, 0, 1,
-                     pos % kPage, lane);
-  append_block<F, 1>(c.v_codes + blk * kInt8CodeBytes, c.v_params + blk, v_new + row, 0, 1,
-                     pos % kPage, lane);
+  uint8_t *block = (v ? c.v_codes : c.k_codes) + blk * kInt8CodeBytes;
+  float x[4];
+  unpack_bf16x4(raw, x);
+  const float s = grow_scale<F>(block, (v ? c.v_params : c.k_params) + blk, warp_max(amax4(x)), slot, lane);
+  // [8 strips of 16 dims][16 slots][16 bytes]: lane l -> strip l / 4, bytes 4 (l % 4)
+  *reinterpret_cast<uint32_t *>(block + (lane >> 2) * (kPage * 16) + slot * 16 + 4 * (lane & 3)) =
+      codes4<F>(x, s, s == 0.f ? 0.f : __frcp_rn(s));
 }
 
-// A CTA looks over 16 rows; the first row of the call in each page leads that page's rows
-// (they may reach past the CTA's 16). One warp per (led page, kv head, K or V).
-constexpr int kRowsPerCta = 16;
+// 4 x 4 words over the four lanes of a group (lane % 4), transposed: lane t gets word t of each.
+__device__ __forceinline__ uint4 transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int t) {
+  // words of lanes t ^ 2 first, then of t ^ 1: after both, lane t holds (a, b, c, d)[t] of lanes 0-3
+  const bool hi2 = (t & 2) != 0, hi1 = (t & 1) != 0;
+  const uint32_t x = __shfl_xor_sync(0xffffffffu, hi2 ? a : c, 2);
+  const uint32_t y = __shfl_xor_sync(0xffffffffu, hi2 ? b : d, 2);
+  // lanes 0, 1: words 0, 1 of themselves (a, b) and of lanes 2, 3 (x, y); lanes 2, 3: words 2, 3
+  const uint32_t p0 = hi2 ? x : a, p1 = hi2 ? y : b;  // from lane t & 1
+  const uint32_t q0 = hi2 ? c : x, q1 = hi2 ? d : y;  // from lane (t & 1) + 2
+  const uint32_t u = __shfl_xor_sync(0xffffffffu, hi1 ? p0 : p1, 1);
+  const uint32_t w = __shfl_xor_sync(0xffffffffu, hi1 ? q0 : q1, 1);
+  return hi1 ? make_uint4(u, p1, w, q1) : make_uint4(p0, u, q0, w);
+}
+
+// CSR rows. A CTA looks over kRowsPerCta rows; the first row of the call in each page leads that
+// page's rows (they may reach past the CTA's). One warp per (led page, kv head, K or V): its rows
+// (up to 16 x 256 bytes) in registers, the block's largest magnitude, the codes, and full 64-byte
+// runs of each strip out. Bound by HBM (768 bytes of rows in for 384 of codes out); the search for
+// a row's sequence is shared by the CTA's ~4 pages and all heads (16 rows per CTA: 80 us, 64: see
+// the table of measurements for the call it was taken on).
+constexpr int kRowsPerCta = 64;
 template <int F>
 __global__ void __launch_bounds__(256) block8_append_rows_kernel(
     CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
@@ -166,11 +172,11 @@ __global__ void __launch_bounds__(256) block8_append_rows_kernel(
   __shared__ int n_lead;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H = c.num_kv_heads;
-  if (warp == 0) {
-    const int row = blockIdx.x * kRowsPerCta + lane;
-    int4 e = make_int4(0, 0, 0, 0);
-    bool leads = false;
-    if (lane < kRowsPerCta && row < total_new) {
+  if (threadIdx.x == 0) n_lead = 0;
+  __syncthreads();
+  if (threadIdx.x < kRowsPerCta) {
+    const int row = blockIdx.x * kRowsPerCta + threadIdx.x;
+    if (row < total_new) {
       int b, pos, L;
       locate_new_token(c.seq_lens, c.num_seqs, indptr, row, b, pos, L);
       const int i = row - indptr[b], n = indptr[b + 1] - indptr[b];
@@ -179,30 +185,51 @@ __global__ void __launch_bounds__(256) block8_append_rows_kernel(
           set_err(err, KV4_DEVERR_SEQ_LEN);
         } else if (i == 0 || pos % kPage == 0) {
           const int page = c.page_table[static_cast<size_t>(b) * c.max_pages + pos / kPage];
-          if (page < 0 || page >= c.num_pages) {
+          if (page < 0 || page >= c.num_pages)
             set_err(err, KV4_DEVERR_PAGE_ID);
-          } else {
-            leads = true;
-            e = make_int4(row, min(n - i, kPage - pos % kPage), pos % kPage, page);
-          }
+          else  // (the order of the led pages is of no consequence)
+            lead[atomicAdd(&n_lead, 1)] = make_int4(row, min(n - i, kPage - pos % kPage), pos % kPage, page);
         }
       }
     }
-    const unsigned m = __ballot_sync(0xffffffffu, leads);
-    if (leads) lead[__popc(m & ((1u << lane) - 1u))] = e;
-    if (lane == 0) n_lead = __popc(m);
   }
   __syncthreads();
   const int tasks = n_lead * H * 2;
+  const size_t stride = static_cast<size_t>(H) * kHeadDim;
   for (int t = warp; t < tasks; t += blockDim.x >> 5) {
     const int4 e = lead[t / (2 * H)];
-    const int r = t % (2 * H), h = r >> 1;
+    const int r = t % (2 * H), h = r >> 1, n = e.y, slot = e.z;
     const bool v = (r & 1) != 0;
     const size_t blk = static_cast<size_t>(e.w) * H + h;
-    const size_t stride = static_cast<size_t>(H) * kHeadDim;
-    append_block<F, 16>((v ? c.v_codes : c.k_codes) + blk * kInt8CodeBytes,
-                        (v ? c.v_params : c.k_params) + blk,
-                        (v ? v_new : k_new) + e.x * stride + h * kHeadDim, stride, e.y, e.z, lane);
+    const uint16_t *rows = (v ? v_new : k_new) + e.x * stride + h * kHeadDim + 4 * lane;
+    uint2 raw[kPage];
+#pragma unroll
+    for (int i = 0; i < kPage; ++i)
+      raw[i] = i < n ? *reinterpret_cast<const uint2 *>(rows + i * stride) : make_uint2(0u, 0u);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPage; ++i) {
+      float x[4];
+      unpack_bf16x4(raw[i], x);
+      amax = fmaxf(amax, amax4(x));
+    }
+    uint8_t *block = (v ? c.v_codes : c.k_codes) + blk * kInt8CodeBytes;
+    const float s = grow_scale<F>(block, (v ? c.v_params : c.k_params) + blk, warp_max(amax), slot, lane);
+    const float y = s == 0.f ? 0.f : __frcp_rn(s);
+    uint8_t *strip = block + (lane >> 2) * (kPage * 16) + slot * 16;
+#pragma unroll
+    for (int q = 0; q < kPage; q += 4) {
+      if (q >= n) break;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[4];
+        unpack_bf16x4(raw[q + i], x);
+        w[i] = codes4<F>(x, s, y);
+      }
+      const uint4 row = transpose4(w[0], w[1], w[2], w[3], lane & 3);  // row q + lane % 4
+      if (q + (lane & 3) < n) *reinterpret_cast<uint4 *>(strip + (q + (lane & 3)) * 16) = row;
+    }
   }
 }
 
@@ -265,7 +292,8 @@ constexpr float kLift8 = 14.0f;
 // cross-lane maximum, the waits and the copies' bookkeeping are paid once for 8 KB.
 template <int F, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kernel(
-    CacheView c, Queries qs, Outputs out, float *__restrict__ partials, int32_t *err) {
+    CacheView c, Queries qs, Outputs out, float *__restrict__ partials, Crossing *__restrict__ notes,
+    int32_t *err) {
   constexpr int ROWS = kCols * NT;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitSmem split;
@@ -285,7 +313,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
     return items(seq_of(c, qs, ROWS, i, check && blockIdx.x == 0 ? err : nullptr));
   });
   const long long t_begin = share.begin, t_end = share.end;
-  if (t_begin >= t_end) return;
+  if (t_begin >= t_end) {
+    if (lane == 0) notes[me].rows = 0;
+    return;
+  }
   int b = share.b;
   long long seq_first = share.seq_first;  // first item of sequence b
   Seq8 sq = seq_of(c, qs, ROWS, b, nullptr);
@@ -308,6 +339,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
     const bool whole = pg0 == 0 && pg1 == sq.pages;
     const int np = sq.L > 0 ? pg1 - pg0 : 0, pairs = (np + kPair - 1) / kPair;
     const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages + pg0;
+
+    if (t == t_begin && lane == 0)
+      notes[me] = crossing(Shares(split.scan[kSplitThreads], gridDim.x * kWarps, kMinShare), me, t_begin - pg0,
+                           sq.pages, pg0, sq.row0, h, u * ROWS, min(ROWS, sq.n * G - u * ROWS));
 
     // page ids and scales of 32 pages at a time, page k in lane k % 32; the ids of the next 32
     // are there early, for the copies that start ahead
@@ -622,36 +657,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
   }
 }
 
-// Where warp blockIdx.x + 1's share starts inside a unit that starts in the share before it,
-// the block joins that unit's records (a unit over more warps is the first such warp's to join).
+// Block blockIdx.x joins the unit that the share of warp blockIdx.x + 1 starts inside of, where
+// that warp is the unit's second (its note says so).
 template <int NT>
-__global__ void __launch_bounds__(kSplitThreads) block8_merge_kernel(CacheView c, Queries qs, Outputs out,
-                                                                     const float *__restrict__ partials,
-                                                                     int attn_warps) {
+__global__ void __launch_bounds__(256) block8_merge_kernel(Outputs out, const float *__restrict__ partials,
+                                                           const Crossing *__restrict__ notes, int H, int G) {
   constexpr int ROWS = kCols * NT;
-  __shared__ SplitSmem split;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = c.gqa, H = c.num_kv_heads, me = blockIdx.x + 1;
-  long long T;
-  const Share share = take_share(c.num_seqs, me, attn_warps, kMinShare, split, [&](int i, bool) {
-    const Seq8 s = seq_of(c, qs, ROWS, i, nullptr);
-    return static_cast<long long>(s.units) * s.pages * H;
-  }, &T);
-  if (share.begin >= share.end) return;
-  const Seq8 sq = seq_of(c, qs, ROWS, share.b, nullptr);
-  const long long in_seq = share.begin - share.seq_first;
-  const int unit = static_cast<int>(in_seq / sq.pages);
-  const int pg0 = static_cast<int>(in_seq - static_cast<long long>(unit) * sq.pages);
-  if (pg0 == 0) return;
-  const Shares sh(T, attn_warps, kMinShare);
-  const long long t0 = share.begin - pg0;
-  if (sh.owner(t0) != me - 1) return;
-  const int w1 = sh.owner(t0 + sq.pages - 1);
-  const int h = unit / sq.units, u = unit - h * sq.units;
-  for (int col = warp; col < ROWS && u * ROWS + col < sq.n * G; col += kSplitThreads / 32) {
-    const int r = u * ROWS + col;
-    const size_t qr = static_cast<size_t>(sq.row0 + r / G) * H * G + h * G + r % G;
-    join_records(partials, ROWS, col, me - 1, w1, [&](int w) { return sh.begin(w) >= t0 ? 0 : 1; }, out, qr,
+  wait_for_launch_before();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x + 1;
+  const Crossing x = notes[me];
+  for (int col = warp; col < x.rows; col += 8) {
+    const int r = x.first_row + col;
+    const size_t qr = static_cast<size_t>(x.row0 + r / G) * H * G + x.h * G + r % G;
+    // a warp's record of the unit is its first, but for the unit's first warp where the unit
+    // starts inside its share
+    join_records(partials, ROWS, col, me - 1, x.last, [&](int w) { return w == me - 1 ? x.slot0 : 0; }, out, qr,
                  lane);
   }
 }
@@ -664,7 +684,7 @@ static cudaError_t launch_block8_append_t(const CacheView &c, const uint16_t *k_
                                           const uint16_t *v_new, const int32_t *indptr,
                                           int32_t total_new, int32_t *err, cudaStream_t s) {
   if (indptr == nullptr) {
-    const long long warps = static_cast<long long>(c.num_seqs) * c.num_kv_heads;
+    const long long warps = 2LL * c.num_seqs * c.num_kv_heads;
     const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
     block8_append_token_kernel<F><<<blocks, 256, 0, s>>>(c, k_new, v_new, err);
   } else {
@@ -692,12 +712,12 @@ static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, 
   return units * H * std::max(1, (max_seq_len + kPage - 1) / kPage);
 }
 
-// Two records of each warp, of the larger of the two unit sizes.
+// A note and two records of each warp, of the larger of the two unit sizes.
 static size_t warp_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G) {
   size_t bytes = 0;
   for (int rows = kCols; rows <= 2 * kCols; rows += kCols) {
-    const size_t n = 2u * attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G, rows));
-    bytes = std::max(bytes, (n * rows * kRecordFloats * sizeof(float) + 255) / 256 * 256);
+    const size_t n = attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G, rows));
+    bytes = std::max(bytes, notes_bytes(n) + (2 * n * rows * kRecordFloats * sizeof(float) + 255) / 256 * 256);
   }
   return bytes;
 }
@@ -710,7 +730,7 @@ size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_
 
 template <int F, int NT>
 static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, int max_seq_len,
-                                        const Outputs &out, float *partials, int32_t *err,
+                                        const Outputs &out, void *workspace, int32_t *err,
                                         cudaStream_t s) {
   static PerDevice grids;
   int most = 0;
@@ -728,11 +748,14 @@ static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, i
   if (e != cudaSuccess) return e;
   const long long bound = items_bound(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa, kCols * NT);
   const int grid = std::min(attn_warps(bound) / kWarps, most);
-  block8_attn_kernel<F, NT><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, err);
+  Crossing *notes = static_cast<Crossing *>(workspace);
+  float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + notes_bytes(grid * kWarps));
+  block8_attn_kernel<F, NT><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, notes, err);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  block8_merge_kernel<NT><<<grid * kWarps - 1, kSplitThreads, 0, s>>>(c, qs, out, partials, grid * kWarps);
-  return cudaGetLastError();
+  return launch_after(block8_merge_kernel<NT>, dim3(grid * kWarps - 1), 256, s, out,
+                      static_cast<const float *>(partials), static_cast<const Crossing *>(notes), c.num_kv_heads,
+                      c.gqa);
 }
 
 cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t *q,
@@ -742,12 +765,11 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
   const Queries qs{q, q_indptr, total_q, max_q_len};
   const long long rows = static_cast<long long>(max_q_len) * c.gqa;
   if (rows > kWarpRows) return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, err, s);
-  float *p = static_cast<float *>(workspace);
   if (fmt == kFmtInt8)
-    return rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1>(c, qs, max_seq_len, out, p, err, s)
-                         : launch_block8_attn_t<kFmtInt8, 2>(c, qs, max_seq_len, out, p, err, s);
-  return rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1>(c, qs, max_seq_len, out, p, err, s)
-                       : launch_block8_attn_t<kFmtE4m3, 2>(c, qs, max_seq_len, out, p, err, s);
+    return rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1>(c, qs, max_seq_len, out, workspace, err, s)
+                         : launch_block8_attn_t<kFmtInt8, 2>(c, qs, max_seq_len, out, workspace, err, s);
+  return rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1>(c, qs, max_seq_len, out, workspace, err, s)
+                       : launch_block8_attn_t<kFmtE4m3, 2>(c, qs, max_seq_len, out, workspace, err, s);
 }
 
 }  // namespace kv4

@@ -78,6 +78,53 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &a, uint32_t &b)
   }
 }
 
+// A worker's note for the merge: its share starts inside a unit that starts in the share before
+// it, whose records workers (this one - 1) .. last hold (rows = 0: it does not).
+struct alignas(16) Crossing {
+  int rows;       // query rows of the unit
+  int first_row;  // its first among the sequence's
+  int row0, h;    // the sequence's first query row; the kv head
+  int last;       // last worker of the unit
+  int slot0;      // which of its two records the unit's first worker wrote
+  int pad[2];
+};
+
+// The note of worker `me`, whose share starts `inside` items after the unit's first item t0 of n.
+__device__ __forceinline__ Crossing crossing(const Shares &sh, int me, long long t0, int n, int inside, int row0,
+                                             int h, int first_row, int rows) {
+  Crossing x{};
+  if (inside > 0 && sh.begin(me - 1) <= t0) {
+    x.rows = rows;
+    x.first_row = first_row;
+    x.row0 = row0;
+    x.h = h;
+    x.last = sh.owner(t0 + n - 1);
+    x.slot0 = sh.begin(me - 1) == t0 ? 0 : 1;
+  }
+  return x;
+}
+
+inline size_t notes_bytes(size_t workers) { return (workers * sizeof(Crossing) + 255) / 256 * 256; }
+
+// A kernel that may be resident before the launch before it has ended, and waits for that here.
+__device__ __forceinline__ void wait_for_launch_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Joins the partial records (max in log2 units, sum, weighted values) of one row of a unit that
 // workers w0 .. w1 share, in that order, and writes the row. Records: [2 per worker][rows][132];
 // slot(w): which of worker w's two. 32 records at a time: their maxima and sums by the lanes
@@ -108,14 +155,20 @@ __device__ __forceinline__ void join_records(const float *__restrict__ partials,
     ll = ll * a + sum;
     acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
     mm = mn;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float f = __shfl_sync(0xffffffffu, e, i);
-      const size_t r = __shfl_sync(0xffffffffu, at, i);
-      const float4 v = *reinterpret_cast<const float4 *>(partials + r + 4 * lane);
-      if (f > 0.f) {
-        acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+    for (int i = 0; i < n; i += 8) {  // eight records' values in flight
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const size_t r = __shfl_sync(0xffffffffu, at, min(i + k, n - 1));
+        v[k] = *reinterpret_cast<const float4 *>(partials + r + 4 * lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = i + k < n ? __shfl_sync(0xffffffffu, e, i + k) : 0.f;
+        if (f > 0.f) {
+          acc.x = fmaf(v[k].x, f, acc.x); acc.y = fmaf(v[k].y, f, acc.y);
+          acc.z = fmaf(v[k].z, f, acc.z); acc.w = fmaf(v[k].w, f, acc.w);
+        }
       }
     }
   }

@@ -12,10 +12,8 @@
 //                          O += P V (P in TMEM); accumulators S and O in TMEM, 4 x 128 columns;
 //   convert warps (4)      load pages' codes and write them as fp16 (exact for both formats)
 //                          into the 128-byte-swizzled tiles the MMAs read.
-// SHARED: the pipelines hold rows 0-127 and 128-255 of one unit and read the same key tiles,
-// which are converted once (two stages). Otherwise each pipeline is a worker of its own, with
-// its own units, key tiles (one stage) and two of the convert warps: for sequences of at most
-// 128 rows, whose time is the reading of the cache.
+// The pipelines hold rows 0-127 and 128-255 of one unit and read the same key tiles, which are
+// converted once (two stages).
 //
 // Scales. A key block's scale multiplies its 16 logits, a value block's scale its 16 weights:
 // P = p 2^7 vs / 2^vref with vref the exponent of the largest value scale so far, so P is at
@@ -33,6 +31,7 @@
 namespace kv4 {
 
 constexpr int kTile = 128;               // rows of a pipeline, positions of a key tile
+constexpr int kUnitRows = 2 * kTile;     // query rows of a unit: both pipelines'
 constexpr int kTilePages = kTile / kPage;
 constexpr int kOperandBytes = kTile * kHeadDim * 2;  // one fp16 operand tile: 32 KB
 constexpr int kTileThreads = 512;        // 8 softmax, 4 convert and 2 MMA warps (and 2 idle)
@@ -130,30 +129,27 @@ struct Setmax {
 // ---------------------------------------------------------------------------
 // units and segments
 // ---------------------------------------------------------------------------
-template <int ROWS>
 struct SeqTiles : SeqRows {
   int units, per_head;  // units of a kv head, and their key tiles together
   int gqa;
   __device__ __forceinline__ int unit_tiles(int u) const {  // at least 1: an empty unit writes zeros
-    const int last = min(n - 1, ((u + 1) * ROWS - 1) / gqa);  // its last position
+    const int last = min(n - 1, ((u + 1) * kUnitRows - 1) / gqa);  // its last position
     return max(0, L - n + last) / kTile + 1;
   }
 };
 
-template <int ROWS>
-__device__ __forceinline__ SeqTiles<ROWS> tiles_of_seq(const CacheView &c, const Queries &qs, int b,
+__device__ __forceinline__ SeqTiles tiles_of_seq(const CacheView &c, const Queries &qs, int b,
                                                        int32_t *err) {
-  SeqTiles<ROWS> s;
+  SeqTiles s;
   static_cast<SeqRows &>(s) = rows_of(c, qs, b, err);
   s.gqa = c.gqa;
-  s.units = static_cast<int>((static_cast<long long>(s.n) * c.gqa + ROWS - 1) / ROWS);
+  s.units = static_cast<int>((static_cast<long long>(s.n) * c.gqa + kUnitRows - 1) / kUnitRows);
   s.per_head = 0;
   for (int u = 0; u < s.units; ++u) s.per_head += s.unit_tiles(u);
   return s;
 }
 
 // A worker's next run of key tiles of one unit.
-template <int ROWS>
 struct Segments {
   const CacheView &c;
   const Queries &qs;
@@ -161,20 +157,20 @@ struct Segments {
   long long at;
   int b;
   long long seq_first;
-  SeqTiles<ROWS> sq;
+  SeqTiles sq;
   // the segment: unit u of kv head h, its key tiles [k0, k1) of nt
   int h, u, k0, k1, nt;
   bool first;  // the worker's first
 
   __device__ __forceinline__ Segments(const CacheView &cc, const Queries &q, const Share &s)
       : c(cc), qs(q), share(s), at(s.begin), b(s.b), seq_first(s.seq_first) {
-    if (share.begin < share.end) sq = tiles_of_seq<ROWS>(c, qs, b, nullptr);
+    if (share.begin < share.end) sq = tiles_of_seq(c, qs, b, nullptr);
   }
   __device__ __forceinline__ bool next() {
     if (at >= share.end) return false;
     while (at >= seq_first + static_cast<long long>(c.num_kv_heads) * sq.per_head) {
       seq_first += static_cast<long long>(c.num_kv_heads) * sq.per_head;
-      sq = tiles_of_seq<ROWS>(c, qs, ++b, nullptr);
+      sq = tiles_of_seq(c, qs, ++b, nullptr);
     }
     const long long in_seq = at - seq_first;
     h = static_cast<int>(in_seq / sq.per_head);
@@ -192,8 +188,7 @@ struct Segments {
   }
 };
 
-// What a key tile's blocks are scaled by; a ring of four per pipeline (SHARED: of one ring), so
-// that a slot is written again only after the softmax threads have left it.
+// What a key tile's blocks are scaled by; a ring of four, so that a slot is written again only after the softmax threads have left it.
 struct alignas(16) TileScales {
   float ks[kTilePages];  // negative: the page is left out
   float cv[kTilePages];  // vs 2^(kPShift - vref)
@@ -210,7 +205,7 @@ struct Seg {
 constexpr int kSegRing = 4;
 
 struct TileBars {
-  uint64_t seg_full[2][kSegRing], seg_empty[2][kSegRing];
+  uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   uint64_t q_full[2], s_full[2], p_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
 };
@@ -232,16 +227,16 @@ __device__ __forceinline__ void mask_logits(uint32_t (&s)[4][32], const TileScal
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <int F, bool SHARED>
+template <int F>
 __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView c, Queries qs, Outputs out,
                                                                      float *__restrict__ partials,
+                                                                     Crossing *__restrict__ notes,
                                                                      int32_t *err) {
-  constexpr int ROWS = SHARED ? 2 * kTile : kTile;  // rows of a unit
   extern __shared__ uint8_t smem_raw[];
   __shared__ SplitSmem split;
   __shared__ TileBars bars;
-  __shared__ TileScales scales[2][4];
-  __shared__ Seg segs[2][kSegRing];
+  __shared__ TileScales scales[4];
+  __shared__ Seg segs[kSegRing];
   __shared__ uint32_t tmem_base_s;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,21 +244,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   // pipeline of this warp: softmax warps 0-3 and 4-7, MMA warps 12 and 13, scheduling warps 14
   // and 15; convert warps 8-11 serve both
   const int pipe = warp < 8 ? warp >> 2 : warp < 12 ? 0 : (warp - 12) & 1;
-  const int ring = SHARED ? 0 : pipe;  // of segments
+
 
   if (threadIdx.x == 0) {
+    for (int k = 0; k < kSegRing; ++k) {
+      mbar_init(&bars.seg_full[k], 1);
+      mbar_init(&bars.seg_empty[k], 14);  // warps that read it
+    }
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < kSegRing; ++k) {
-        mbar_init(&bars.seg_full[i][k], 1);
-        mbar_init(&bars.seg_empty[i][k], SHARED ? 14 : 9);  // warps that read it
-      }
       mbar_init(&bars.q_full[i], kTile);
       mbar_init(&bars.s_full[i], 2);  // the MMAs' completion, and the issuing thread itself
       mbar_init(&bars.p_full[i], kTile);
       mbar_init(&bars.k_full[i], 4);
       mbar_init(&bars.v_full[i], 4);
-      mbar_init(&bars.k_empty[i], SHARED ? 2 : 1);
-      mbar_init(&bars.v_empty[i], SHARED ? 2 : 1);
+      mbar_init(&bars.k_empty[i], 2);
+      mbar_init(&bars.v_empty[i], 2);
     }
     fence_barrier_init();
   }
@@ -273,11 +268,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
-  const int me = SHARED ? blockIdx.x : 2 * blockIdx.x + pipe;
-  const int workers = SHARED ? gridDim.x : 2 * gridDim.x;
+  const int me = blockIdx.x, workers = gridDim.x;
   auto items = [&](int i, bool check) {
     return static_cast<long long>(H) *
-           tiles_of_seq<ROWS>(c, qs, i, check && blockIdx.x == 0 ? err : nullptr).per_head;
+           tiles_of_seq(c, qs, i, check && blockIdx.x == 0 ? err : nullptr).per_head;
   };
   const Share share = take_share(c.num_seqs, me, workers, kTileMinShare, split, items);
   __syncthreads();
@@ -286,9 +280,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   const uint32_t tm_s = tmem + 256 * pipe, tm_o = tm_s + 128;
   uint8_t *q_tile = smem + pipe * kOperandBytes;
   uint8_t *k_tiles = smem + 2 * kOperandBytes, *v_tiles = smem + 4 * kOperandBytes;
-  auto stage_of = [&](int k) { return SHARED ? k & 1 : pipe; };   // of the worker's k-th tile
-  auto phase_of = [&](int k) { return SHARED ? (k >> 1) & 1 : k & 1; };
-  auto slot_of = [&](int k) -> TileScales & { return scales[SHARED ? 0 : pipe][k & 3]; };
+  auto stage_of = [](int k) { return k & 1; };  // of the worker's k-th tile
+  auto phase_of = [](int k) { return (k >> 1) & 1; };
+  auto slot_of = [&](int k) -> TileScales & { return scales[k & 3]; };
   auto wait = [&](uint64_t *bar, int parity) {
     if (mbar_wait_bounded(bar, parity, kTileWait)) return true;
     set_err(err, KV4_DEVERR_TIMEOUT);
@@ -297,28 +291,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   int kt = 0;      // tiles of the worker so far
   int seg_no = 0;  // segments read from the ring so far
   bool ok = true;  // no wait has given up
-  auto read_seg = [&](int r, int no, Seg &s) {  // all lanes of a warp; false: no more
+  auto read_seg = [&](int no, Seg &s) {  // all lanes of a warp; false: no more
     const int at = no & (kSegRing - 1);
-    ok = __all_sync(0xffffffffu, wait(&bars.seg_full[r][at], (no / kSegRing) & 1));
+    ok = __all_sync(0xffffffffu, wait(&bars.seg_full[at], (no / kSegRing) & 1));
     if (!ok) return false;
-    s = segs[r][at];
+    s = segs[at];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.seg_empty[r][at]);
+    if (lane == 0) mbar_arrive(&bars.seg_empty[at]);
     return s.b >= 0;
   };
 
   if (warp >= 14) {
     // ------------------------------- schedule -------------------------------
     Setmax<kMmaRegs>::dec();
-    if (lane == 0 && (!SHARED || pipe == 0)) {
-      Segments<ROWS> sg(c, qs, share);
+    if (lane == 0 && warp == 14) {
+      Segments sg(c, qs, share);
+      notes[me].rows = 0;
       for (int no = 0;; ++no) {
         const bool more = sg.next();
+        if (no == 0 && more)
+          notes[me] = crossing(Shares(split.scan[kSplitThreads], workers, kTileMinShare), me, share.begin - sg.k0,
+                               sg.nt, sg.k0, sg.sq.row0, sg.h, sg.u * kUnitRows,
+                               min(kUnitRows, sg.sq.n * G - sg.u * kUnitRows));
         const int at = no & (kSegRing - 1);
-        if (!wait(&bars.seg_empty[ring][at], ((no / kSegRing) & 1) ^ 1)) break;
-        segs[ring][at] = more ? Seg{sg.b, sg.h, sg.u, sg.k0, sg.k1, sg.nt, sg.first, sg.sq.L, sg.sq.n, sg.sq.row0}
+        if (!wait(&bars.seg_empty[at], ((no / kSegRing) & 1) ^ 1)) break;
+        segs[at] = more ? Seg{sg.b, sg.h, sg.u, sg.k0, sg.k1, sg.nt, sg.first, sg.sq.L, sg.sq.n, sg.sq.row0}
                               : Seg{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-        mbar_arrive(&bars.seg_full[ring][at]);
+        mbar_arrive(&bars.seg_full[at]);
         if (!more) break;
       }
     }
@@ -327,9 +326,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     // ------------------------------- MMA -------------------------------
     int seg = 0, pp = 0;  // live segments and phases of p_full so far
     Seg sg;
-    while (ok && read_seg(ring, seg_no++, sg)) {
+    while (ok && read_seg(seg_no++, sg)) {
       const int n = sg.k1 - sg.k0;
-      const bool live = sg.u * ROWS + (SHARED ? pipe * kTile : 0) < sg.n * G;
+      const bool live = sg.u * kUnitRows + pipe * kTile < sg.n * G;
       if (lane == 0) {
         if (!live) {  // no rows here: only let go of the shared tiles
           for (int j = 0; ok && j < n; ++j) {
@@ -388,56 +387,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   } else if (warp >= 8) {
     // ------------------------------- convert -------------------------------
     // One tile ahead in registers (its codes), two ahead its blocks' scales, three ahead its page
-    // ids: nothing waits for what it has just asked for. The workers' tiles in turn (SHARED: the
-    // one worker's); 128 threads, a 16-byte piece of each page each.
+    // ids: nothing waits for what it has just asked for. 128 threads, a 16-byte piece of each page
+    // each.
     Setmax<kConvertRegs>::dec();
     const int tid = threadIdx.x - 256;
     const int strip = tid >> 4, slot = tid & 15;
     struct Meta {
-      int w;          // worker (0 or 1), -1: no tile
-      int kt, k, L;   // the worker's tile number, its key tile, the length
+      int kt;         // the worker's tile number, -1: no tile
+      int k, L;       // the key tile, the length
       int h, pid;     // kv head; page (lane % 8) of the tile (-2: behind the length)
       uint16_t ks, vs;  // and its scales
       bool first;     // the segment's first tile
     };
-    Seg seg0, seg1;  // the workers' segments
-    int at0 = 0, end0 = 0, at1 = 0, end1 = 0, n0 = 0, n1 = 0, s0 = 0, s1 = 0;
-    bool more0 = true, more1 = !SHARED;
-    int turn = 0;
-    // the next tile of worker w: its segment, or nullptr
-    auto step = [&](int w, Seg &s, int &at, int &end, int &n_tiles, int &n_segs, bool &more, Meta &m) {
-      if (at == end) {
-        more = more && read_seg(w, n_segs++, s);
-        if (!more) return false;
-        at = s.k0;
-        end = s.k1;
-      }
-      m.w = w;
-      m.kt = n_tiles++;
-      m.first = at == s.k0;
-      m.k = at++;
-      m.L = s.L;
-      m.h = s.h;
-      return true;
-    };
+    Seg sg;
+    int at = 0, end = 0, n_tiles = 0;
+    bool more = true;
     auto ask_page = [&]() {  // the next tile and its page ids
-      Meta m{-1, 0, 0, 0, 0, -2, 0, 0, false};
-      int b = 0;
-      if constexpr (SHARED) {
-        if (step(0, seg0, at0, end0, n0, s0, more0, m)) b = seg0.b;
-      } else {
-        for (int t = 0; t < 2 && m.w < 0; ++t, turn ^= 1) {
-          if (turn == 0 && step(0, seg0, at0, end0, n0, s0, more0, m)) b = seg0.b;
-          else if (turn == 1 && step(1, seg1, at1, end1, n1, s1, more1, m)) b = seg1.b;
-        }
+      Meta m{-1, 0, 0, 0, -2, 0, 0, false};
+      if (at == end) {
+        more = more && read_seg(seg_no++, sg);
+        if (!more) return m;
+        at = sg.k0;
+        end = sg.k1;
       }
+      m.kt = n_tiles++;
+      m.first = at == sg.k0;
+      m.k = at++;
+      m.L = sg.L;
+      m.h = sg.h;
       const int page = m.k * kTilePages + (lane & 7);
-      if (m.w >= 0 && page < (m.L + kPage - 1) / kPage)
-        m.pid = __ldg(c.page_table + static_cast<size_t>(b) * c.max_pages + page);
+      if (page < (m.L + kPage - 1) / kPage)
+        m.pid = __ldg(c.page_table + static_cast<size_t>(sg.b) * c.max_pages + page);
       return m;
     };
     auto ask_scales = [&](Meta &m) {  // of its pages, and whether the ids are any
-      if (m.pid == -2 && (m.w < 0 || m.k * kTilePages + (lane & 7) >= (m.L + kPage - 1) / kPage)) return;
+      if (m.pid == -2 && (m.kt < 0 || m.k * kTilePages + (lane & 7) >= (m.L + kPage - 1) / kPage)) return;
       if (m.pid < 0 || m.pid >= c.num_pages) {
         set_err(err, KV4_DEVERR_PAGE_ID);
         m.pid = -1;
@@ -479,23 +463,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       fence_proxy_async_smem();
       __syncwarp();
     };
-    float vref0 = 0.f, vref1 = 0.f;
+    float vref = 0.f;
     uint4 kv[kTilePages] = {}, vv[kTilePages] = {};
     Meta cur = ask_page(), nxt = ask_page();
     ask_scales(cur);
     ask_scales(nxt);
     Meta nx2 = ask_page();
-    if (cur.w >= 0) {
+    if (cur.kt >= 0) {
       load(c.k_codes, cur, kv);
       load(c.v_codes, cur, vv);
     }
-    while (cur.w >= 0) {
-      const int st = SHARED ? cur.kt & 1 : cur.w;
-      const int free_phase = (SHARED ? (cur.kt >> 1) & 1 : cur.kt & 1) ^ 1;
+    while (cur.kt >= 0) {
+      const int st = stage_of(cur.kt), free_phase = phase_of(cur.kt) ^ 1;
       ok = __all_sync(0xffffffffu, wait(&bars.k_empty[st], free_phase));
       if (!ok) break;
       if (tid < 32) {  // the first convert warp writes the scales
-        TileScales &sl = scales[cur.w][cur.kt & 3];
+        TileScales &sl = slot_of(cur.kt);
         const float ks = cur.pid == -1 ? -1.f : __half2float(__ushort_as_half(cur.ks));
         const float vs = __half2float(__ushort_as_half(cur.vs));
         float top = vs;
@@ -504,7 +487,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         const unsigned bad = __ballot_sync(0xffffffffu, cur.pid == -1);
         int e = -24;
         if (top > 0.f) frexpf(top, &e);  // top < 2^e
-        float &vref = cur.w == 0 ? vref0 : vref1;
         const float before = cur.first ? static_cast<float>(e) : vref;
         vref = fmaxf(before, static_cast<float>(e));
         if (lane < kTilePages) {
@@ -519,12 +501,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       }
       put(k_tiles + st * kOperandBytes, cur, kv);
       if (lane == 0) mbar_arrive(&bars.k_full[st]);
-      if (nxt.w >= 0) load(c.k_codes, nxt, kv);
+      if (nxt.kt >= 0) load(c.k_codes, nxt, kv);
       ok = __all_sync(0xffffffffu, wait(&bars.v_empty[st], free_phase));
       if (!ok) break;
       put(v_tiles + st * kOperandBytes, cur, vv);
       if (lane == 0) mbar_arrive(&bars.v_full[st]);
-      if (nxt.w >= 0) load(c.v_codes, nxt, vv);
+      if (nxt.kt >= 0) load(c.v_codes, nxt, vv);
       cur = nxt;
       nxt = nx2;
       ask_scales(nxt);
@@ -538,9 +520,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     const uint32_t ts = tm_s + lane_off, to = tm_o + lane_off;
     int sp = 0;  // phases of s_full
     Seg sg;
-    while (ok && read_seg(ring, seg_no++, sg)) {
+    while (ok && read_seg(seg_no++, sg)) {
       const int n_tiles = sg.k1 - sg.k0;
-      const int r0 = sg.u * ROWS + (SHARED ? pipe * kTile : 0);
+      const int r0 = sg.u * kUnitRows + pipe * kTile;
       const int rows = sg.n * G;
       if (r0 >= rows) {  // (the MMA warp skips it too)
         kt += n_tiles;
@@ -673,8 +655,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       const bool whole = sg.k0 == 0 && sg.k1 == sg.nt;
       const float undo = fast_exp2(vref - kPShift);
       const float scale = whole ? (l > 0.f ? undo / l : 0.f) : undo;
-      float *rec = partials + (static_cast<size_t>(2 * me + (sg.first ? 0 : 1)) * ROWS +
-                               (SHARED ? pipe * kTile : 0) + row) * kRecordFloats;
+      float *rec = partials + (static_cast<size_t>(2 * me + (sg.first ? 0 : 1)) * kUnitRows +
+                               pipe * kTile + row) * kRecordFloats;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
@@ -714,83 +696,62 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   }
 }
 
-// Where worker blockIdx.x's share starts inside a unit that starts in the share before it, the
-// block joins that unit's records, in worker order (a unit over more workers is the first such
-// worker's to join). Rows over blockIdx.y and the warps.
-template <int ROWS>
-__global__ void __launch_bounds__(256) block8_tile_merge_kernel(CacheView c, Queries qs, Outputs out,
-                                                                const float *__restrict__ partials,
-                                                                int workers) {
-  __shared__ SplitSmem split;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = c.gqa, H = c.num_kv_heads, me = blockIdx.x + 1;
-  long long T;
-  const Share share = take_share(c.num_seqs, me, workers, kTileMinShare, split, [&](int i, bool) {
-    return static_cast<long long>(H) * tiles_of_seq<ROWS>(c, qs, i, nullptr).per_head;
-  }, &T);
-  Segments<ROWS> sg(c, qs, share);
-  if (!sg.next() || sg.k0 == 0) return;
-  const Shares sh(T, workers, kTileMinShare);
-  const long long t0 = share.begin - sg.k0;
-  if (sh.owner(t0) != me - 1) return;
-  const int w1 = sh.owner(t0 + sg.nt - 1);
-  const int last = min(ROWS, sg.sq.n * G - sg.u * ROWS);
-  for (int x = blockIdx.y * 8 + warp; x < last; x += gridDim.y * 8) {
-    const int r = sg.u * ROWS + x;
-    const size_t qr = static_cast<size_t>(sg.sq.row0 + r / G) * H * G + sg.h * G + r % G;
-    join_records(partials, ROWS, x, me - 1, w1, [&](int w) { return sh.begin(w) >= t0 ? 0 : 1; }, out, qr, lane);
+// Blocks (blockIdx.x, *) join the unit that the share of worker blockIdx.x + 1 starts inside of,
+// where that worker is the unit's second (its note says so); rows over blockIdx.y and the warps.
+__global__ void __launch_bounds__(256) block8_tile_merge_kernel(Outputs out, const float *__restrict__ partials,
+                                                                const Crossing *__restrict__ notes, int H, int G) {
+  wait_for_launch_before();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x + 1;
+  const Crossing x = notes[me];
+  for (int i = blockIdx.y * 8 + warp; i < x.rows; i += gridDim.y * 8) {
+    const int r = x.first_row + i;
+    const size_t qr = static_cast<size_t>(x.row0 + r / G) * H * G + x.h * G + r % G;
+    join_records(partials, kUnitRows, i, me - 1, x.last, [&](int w) { return w == me - 1 ? x.slot0 : 0; }, out, qr,
+                 lane);
   }
 }
 
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-// CTAs for at most this many key tiles, of units of `rows` rows.
-static int tile_ctas(int num_seqs, int total_q, int max_seq_len, int H, int G, int rows) {
-  const long long units = (static_cast<long long>(total_q) * G + rows - 1) / rows + num_seqs;
+// CTAs for at most this many key tiles.
+static int tile_ctas(int num_seqs, int total_q, int max_seq_len, int H, int G) {
+  const long long units = (static_cast<long long>(total_q) * G + kUnitRows - 1) / kUnitRows + num_seqs;
   const long long tiles = units * H * (max_seq_len / kTile + 1);
-  const int per_cta = rows == kTile ? 2 : 1;  // workers
-  return static_cast<int>(std::max(1LL, std::min<long long>(kTileCtas, (tiles + per_cta - 1) / per_cta)));
+  return static_cast<int>(std::max(1LL, std::min<long long>(kTileCtas, tiles)));
 }
 
 size_t tile_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G) {
-  // two records of 256 rows per CTA in either form
-  const size_t ctas = std::max(tile_ctas(num_seqs, total_q, max_seq_len, H, G, kTile),
-                               tile_ctas(num_seqs, total_q, max_seq_len, H, G, 2 * kTile));
-  return ctas * 2 * 2 * kTile * kRecordFloats * sizeof(float);
+  const size_t ctas = tile_ctas(num_seqs, total_q, max_seq_len, H, G);
+  return notes_bytes(ctas) + ctas * 2 * kUnitRows * kRecordFloats * sizeof(float);  // two records each
 }
 
-template <int F, bool SHARED>
+template <int F>
 static cudaError_t launch_tile_t(const CacheView &c, const Queries &qs, int max_seq_len, const Outputs &out,
-                                 float *partials, int32_t *err, cudaStream_t s) {
-  constexpr int ROWS = SHARED ? 2 * kTile : kTile;
+                                 void *workspace, int32_t *err, cudaStream_t s) {
   static PerDevice sms;
   int n_sm = 0;
   cudaError_t e = once_per_device(sms, [](int dev, int *g) {
-    cudaError_t r = cudaFuncSetAttribute(block8_tile_kernel<F, SHARED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    cudaError_t r = cudaFuncSetAttribute(block8_tile_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kTileSmem);
     return r == cudaSuccess ? cudaDeviceGetAttribute(g, cudaDevAttrMultiProcessorCount, dev) : r;
   }, &n_sm);
   if (e != cudaSuccess) return e;
-  const int ctas = std::min(n_sm, tile_ctas(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa, ROWS));
-  block8_tile_kernel<F, SHARED><<<ctas, kTileThreads, kTileSmem, s>>>(c, qs, out, partials, err);
+  const int ctas = std::min(n_sm, tile_ctas(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa));
+  Crossing *notes = static_cast<Crossing *>(workspace);
+  float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + notes_bytes(ctas));
+  block8_tile_kernel<F><<<ctas, kTileThreads, kTileSmem, s>>>(c, qs, out, partials, notes, err);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int workers = SHARED ? ctas : 2 * ctas;
-  if (workers > 1)
-    block8_tile_merge_kernel<ROWS><<<dim3(workers - 1, 4), 256, 0, s>>>(c, qs, out, partials, workers);
-  return cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  return launch_after(block8_tile_merge_kernel, dim3(ctas - 1, 8), 256, s, out,
+                      static_cast<const float *>(partials), static_cast<const Crossing *>(notes), c.num_kv_heads,
+                      c.gqa);
 }
 
 cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs, int max_seq_len,
                                   const Outputs &out, void *workspace, int32_t *err, cudaStream_t s) {
-  float *p = static_cast<float *>(workspace);
-  const bool shared = true || static_cast<long long>(qs.max_n) * c.gqa > kTile;
-  if (fmt == kFmtInt8)
-    return shared ? launch_tile_t<kFmtInt8, true>(c, qs, max_seq_len, out, p, err, s)
-                  : launch_tile_t<kFmtInt8, false>(c, qs, max_seq_len, out, p, err, s);
-  return shared ? launch_tile_t<kFmtE4m3, true>(c, qs, max_seq_len, out, p, err, s)
-                : launch_tile_t<kFmtE4m3, false>(c, qs, max_seq_len, out, p, err, s);
+  return fmt == kFmtInt8 ? launch_tile_t<kFmtInt8>(c, qs, max_seq_len, out, workspace, err, s)
+                         : launch_tile_t<kFmtE4m3>(c, qs, max_seq_len, out, workspace, err, s);
 }
 
 }  // namespace kv4

@@ -38,16 +38,30 @@ __device__ __forceinline__ Tiles tiles_of(const CacheView &c, int acc_stride, in
 }
 
 constexpr int kWMinShare = 4;  // tiles per warp, at least
-constexpr int kWStages = 8;
-constexpr int kWStageBytes = 2304;  // K codes (at most 2048), then K scales or parameters
-constexpr int kWWarpSmem = kWStages * kWStageBytes;
+constexpr int kWPair = 2;      // tiles of a stage
+constexpr int kWStages = 4;
+constexpr int kWTileBytes = 2304;  // K codes (at most 2048), then K scales or parameters
+constexpr int kWWarpSmem = kWStages * kWPair * kWTileBytes;
 constexpr int kWCtaSmem = kWarps * kWWarpSmem;
+
+// D = A B, the accumulators' start being zero without registers for it.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a01, uint32_t a23, uint32_t a45,
+                                             uint32_t a67, uint32_t b01, uint32_t b23) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a01), "r"(a23), "r"(a45), "r"(a67), "r"(b01), "r"(b23), "f"(0.f));
+}
 
 // One warp serves one kv head's G <= 8 query heads (MMA columns). The query is scaled by a
 // power of two to [2^14, 2^15) at its largest element and enters as fp16, in which its bf16
 // elements are exact; the codes are exact in fp16 too, so the only rounding of a logit is
 // the fp32 accumulation. INT4 codes enter as fp16 subnormals (c * 2^-24, or 16 c * 2^-24
-// for the odd dims, whose query elements carry the factor 1/16).
+// for the odd dims, whose query elements carry the factor 1/16); a group's scale and minimum
+// multiply its product and its query sum, s = kk sum_g (scale_g (q c)_g + min_g sum(q)_g / kk).
+// Bound by instruction issue and the reading of K: two tiles per wait and ring stage, and the
+// totals of a tile move as one load and one store of 16 lanes.
 __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     CacheView c, const uint16_t *__restrict__ q, const float *__restrict__ lse, const float *acc_in,
     float *acc_out, int acc_stride, int32_t *err) {
@@ -60,7 +74,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
   uint8_t *stage0 = smem + warp * kWWarpSmem;
   uint64_t *bars = bars_all[warp];
   if (lane == 0) {
-    for (int s = 0; s < kWStages; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < kWStages; ++s) mbar_init(&bars[s], kWPair);  // an arrival per tile
     fence_barrier_init();
   }
   const int me = blockIdx.x * kWarps + warp;
@@ -86,17 +100,19 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     const int h = static_cast<int>(in_seq / n_tiles);
     const int k0 = static_cast<int>(in_seq - static_cast<long long>(h) * n_tiles);
     const int k1 = static_cast<int>(min(static_cast<long long>(n_tiles), k0 + (share.end - t)));
-    const int L = ti.L, p0 = S / kPage;
+    const int pairs = (k1 - k0 + kWPair - 1) / kWPair;
+    const int L = ti.L, p0 = S / kPage, n4 = ti.int4_pages, n48 = ti.int4_pages + ti.sink;
     const int set = ti.sink ? (c.sink_idx ? c.sink_idx[b] : b) : 0;
     const int ring = ti.ring ? (c.ring_idx ? c.ring_idx[b] : b) : 0;
     const bool set_ok = set >= 0 && set < c.num_sink_sets, ring_ok = ring >= 0 && ring < c.num_rings;
+    if (lane == 0 && ((ti.sink && !set_ok) || (ti.ring && !ring_ok))) set_err(err, KV4_DEVERR_SIDE_IDX);
     const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages + p0;
 
-    // Whether tile k can be read (else its positions are left out), and its copies
+    // INT4 page ids of 32 tiles at a time, tile k0 + i in lane i % 32, and of the next 32
     int pid = -1, pid_next = -1, block0 = k0;
     auto load_pages = [&](int at) {
       int p = -1;
-      if (at + lane < min(k1, ti.int4_pages)) {
+      if (at + lane < min(k1, n4)) {
         p = pt[at + lane];
         if (p < 0 || p >= c.num_pages) {
           set_err(err, KV4_DEVERR_PAGE_ID);
@@ -105,39 +121,32 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
       }
       return p;
     };
-    // (K codes, K scales or parameters, bytes of each) of tile k; no bytes: it is left out
-    auto issue = [&](int k) {
-      const int a = __shfl_sync(0xffffffffu, pid, (k - block0) & 31);
-      const int z = __shfl_sync(0xffffffffu, pid_next, (k - block0) & 31);
-      if (lane != 0) return;
-      const int st = (k - k0) % kWStages;
-      uint8_t *dst = stage0 + st * kWStageBytes;
+    // Lane l < 2 copies tile 2j + l of the segment (K codes, then K scales or parameters); one
+    // that cannot be read only arrives, and its positions are left out
+    auto issue = [&](int j) {
+      const int k = k0 + kWPair * j + (lane & 1), at = (k - block0) & 31;
+      const int a = __shfl_sync(0xffffffffu, pid, at), z = __shfl_sync(0xffffffffu, pid_next, at);
+      if (lane >= kWPair) return;
+      const int st = j % kWStages;
+      uint8_t *dst = stage0 + (st * kWPair + lane) * kWTileBytes;
       const uint8_t *codes = nullptr;
       const void *par = nullptr;
       uint32_t nc = kInt8CodeBytes, np = kInt8ScaleBytes;
-      if (k < ti.int4_pages) {
+      if (k < n4) {
         const int p = k - block0 < 32 ? a : z;
-        if (p >= 0) {
+        if (p >= 0 && k < k1) {
           const size_t blk = static_cast<size_t>(p) * H + h;
           codes = c.k_codes + blk * kInt4CodeBytes;
           par = reinterpret_cast<const uint8_t *>(c.k_params) + blk * kInt4ParamBytes;
           nc = kInt4CodeBytes;
           np = kInt4ParamBytes;
         }
-      } else if (k < ti.int4_pages + ti.sink) {
-        if (set_ok) {
-          const size_t x = (static_cast<size_t>(set) * H + h) * c.sink_tiles + (k - ti.int4_pages);
-          codes = reinterpret_cast<const uint8_t *>(c.sink_k) + x * kInt8CodeBytes;
-          par = c.sink_ks + x * kPage;
-        } else {
-          set_err(err, KV4_DEVERR_SIDE_IDX);
-        }
-      } else if (ring_ok) {
-        const size_t x = (static_cast<size_t>(ring) * H + h) * c.ring_tiles + (k - ti.int4_pages - ti.sink);
-        codes = reinterpret_cast<const uint8_t *>(c.ring_k) + x * kInt8CodeBytes;
-        par = c.ring_ks + x * kPage;
-      } else {
-        set_err(err, KV4_DEVERR_SIDE_IDX);
+      } else if (k < n48 ? set_ok && k < k1 : ring_ok && k < k1) {
+        const bool sink = k < n48;
+        const size_t x = sink ? (static_cast<size_t>(set) * H + h) * c.sink_tiles + (k - n4)
+                              : (static_cast<size_t>(ring) * H + h) * c.ring_tiles + (k - n48);
+        codes = reinterpret_cast<const uint8_t *>(sink ? c.sink_k : c.ring_k) + x * kInt8CodeBytes;
+        par = (sink ? c.sink_ks : c.ring_ks) + x * kPage;
       }
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(&bars[st], codes ? nc + np : 0);
@@ -147,17 +156,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
       }
     };
     pid = load_pages(k0);
+    int issued = min(pairs, kWStages);
+    for (int j = 0; j < issued; ++j) issue(j);
     pid_next = load_pages(k0 + 32);
-    int issued = min(k1, k0 + kWStages);
-    for (int k = k0; k < issued; ++k) issue(k);
 
     // ---- query fragments, column gid = query head gid ----
     const bool live = gid < G;
     const uint16_t *qrow = q + (static_cast<size_t>(b) * H * G + h * G + gid) * kHeadDim;
     uint32_t q8[8][2];  // INT8 strip s: dims 16s + 4tig + (0,1), (2,3)
     uint32_t q4[4][4];  // INT4 group g: dims 32g + 8tig + (0,4), (2,6), then (1,5), (3,7) / 16
-    float qs[4][2];     // group sums of the columns 2tig, 2tig + 1 (true values)
-    float kq[2], ls[2];
+    float2 qs[4];       // group sums of the columns 2tig, 2tig + 1, over kk
+    float2 kq, kk, ls;  // logit factors of the INT8 and the INT4 products; lse in log2 units
     {
       float amax = 0.f;
       float v[4][8];
@@ -181,8 +190,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
         for (int i = 0; i < 8; ++i) sum += v[g][i];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[g][0] = __shfl_sync(0xffffffffu, sum, 4 * (2 * tig)) * kScaleLog2;
-        qs[g][1] = __shfl_sync(0xffffffffu, sum, 4 * (2 * tig + 1)) * kScaleLog2;
+        sum *= inv * (1.0f / kSubUnscale);  // powers of two
+        qs[g].x = __shfl_sync(0xffffffffu, sum, 4 * (2 * tig));
+        qs[g].y = __shfl_sync(0xffffffffu, sum, 4 * (2 * tig + 1));
         const float odd = inv * 0.0625f;
         q4[g][0] = pack_h2(v[g][0] * inv, v[g][4] * inv);
         q4[g][1] = pack_h2(v[g][2] * inv, v[g][6] * inv);
@@ -195,132 +205,114 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
         q8[s][0] = pack_h2(__uint_as_float(w.x << 16) * inv, __uint_as_float(w.x & 0xFFFF0000u) * inv);
         q8[s][1] = pack_h2(__uint_as_float(w.y << 16) * inv, __uint_as_float(w.y & 0xFFFF0000u) * inv);
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int col = 2 * tig + e;
-        kq[e] = __shfl_sync(0xffffffffu, step, 4 * col) * kScaleLog2;
-        // a column without a query weighs nothing
-        ls[e] = col < G ? lse[(static_cast<size_t>(b) * H + h) * G + col] * kLog2e : CUDART_INF_F;
-      }
+      kq.x = __shfl_sync(0xffffffffu, step, 4 * (2 * tig)) * kScaleLog2;
+      kq.y = __shfl_sync(0xffffffffu, step, 4 * (2 * tig + 1)) * kScaleLog2;
+      kk = make_float2(kq.x * kSubUnscale, kq.y * kSubUnscale);
+      // a column without a query weighs nothing
+      const float *ll = lse + (static_cast<size_t>(b) * H + h) * G;
+      ls.x = 2 * tig < G ? -ll[2 * tig] * kLog2e : -CUDART_INF_F;
+      ls.y = 2 * tig + 1 < G ? -ll[2 * tig + 1] * kLog2e : -CUDART_INF_F;
     }
     const size_t acc0 = (static_cast<size_t>(b) * H + h) * acc_stride;
+    const int mine = gid + 8 * (tig & 1);  // the slot whose total this lane moves (tig < 2)
 
     bool dead = false;
-    for (int k = k0; k < k1; ++k) {
-      if (k - block0 == 32) {
+    for (int j = 0; j < pairs && !dead; ++j) {
+      if (kWPair * j > 0 && ((kWPair * j) & 31) == 0) {
         block0 += 32;
         pid = pid_next;
         pid_next = load_pages(block0 + 32);
       }
-      // position of this lane's tokens (slots gid, gid + 8) and whether the tile holds them
-      int pos[2];
-      bool in[2];
-      bool ok;
-      if (k < ti.int4_pages) {
-        ok = __shfl_sync(0xffffffffu, pid, (k - block0) & 31) >= 0;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          pos[hf] = (p0 + k) * kPage + gid + 8 * hf;
-          in[hf] = pos[hf] >= S && pos[hf] < L - R;
-        }
-      } else if (k < ti.int4_pages + ti.sink) {
-        ok = set_ok;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          pos[hf] = (k - ti.int4_pages) * kPage + gid + 8 * hf;
-          in[hf] = pos[hf] < min(S, L);
-        }
-      } else {
-        ok = ring_ok;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int slot = (k - ti.int4_pages - ti.sink) * kPage + gid + 8 * hf;
-          // the last position p < L with p mod R = slot
-          const int back = slot < R ? (L - 1 - slot + R) % R : 0;
-          pos[hf] = L - 1 - back;
-          in[hf] = slot < R && pos[hf] >= max(S, L - R) && pos[hf] >= 0;
-        }
-      }
-      float old[2] = {0.f, 0.f};
-      if (tig == 0 && acc_in != nullptr)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          if (in[hf]) old[hf] = acc_in[acc0 + pos[hf]];
-      const int st = (k - k0) % kWStages;
+      const int st = j % kWStages;
       if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u)) {
         if (lane == 0) set_err(err, KV4_DEVERR_TIMEOUT);
-        for (int i = k; i < issued; ++i)
-          mbar_wait_bounded(&bars[(i - k0) % kWStages], (parity >> ((i - k0) % kWStages)) & 1u,
-                            kWaitLimit * 16u);
+        for (int i = j; i < issued; ++i)
+          mbar_wait_bounded(&bars[i % kWStages], (parity >> (i % kWStages)) & 1u, kWaitLimit * 16u);
         dead = true;
         break;
       }
       parity ^= 1u << st;
-      const uint8_t *sp = stage0 + st * kWStageBytes;
-      const uint32_t sa = smem_u32(sp);
-      float s[2][2];  // logits in log2 units, less lse
-      if (ok && k < ti.int4_pages) {
+#pragma unroll 1
+      for (int pp = 0; pp < kWPair; ++pp) {
+        const int k = k0 + kWPair * j + pp;
+        if (k >= k1) break;
+        const uint8_t *sp = stage0 + (st * kWPair + pp) * kWTileBytes;
+        const uint32_t sa = smem_u32(sp) + ld;
+        int pos;  // of this lane's total; whether it is one of the tile's, and the tile was read
+        bool in;
+        const bool copied = __shfl_sync(0xffffffffu, pid, (k - block0) & 31) >= 0;
+        if (k < n4) {
+          pos = (p0 + k) * kPage + mine;
+          in = pos >= S && pos < L - R && copied;
+        } else if (k < n48) {
+          pos = (k - n4) * kPage + mine;
+          in = pos < min(S, L) && set_ok;
+        } else {
+          const int slot = (k - n48) * kPage + mine;
+          const int lastp = L - 1, base = lastp - lastp % R + slot;  // the last p < L with p mod R = slot
+          pos = base > lastp ? base - R : base;
+          in = slot < R && pos >= max(S, L - R) && ring_ok;
+        }
+        in = in && tig < 2;
+        const float old = in && acc_in != nullptr ? acc_in[acc0 + pos] : 0.f;
+        float2 s[2];  // logits of the slots gid, gid + 8 in log2 units, less lse
+        if (k < n4) {
+          float2 z[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const uint4 par[2] = {*reinterpret_cast<const uint4 *>(sp + kInt8CodeBytes + gid * 16),
+                                *reinterpret_cast<const uint4 *>(sp + kInt8CodeBytes + (gid + 8) * 16)};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) s[hf][0] = -ls[0], s[hf][1] = -ls[1];
-        const uint4 par[2] = {*reinterpret_cast<const uint4 *>(sp + kInt8CodeBytes + gid * 16),
-                              *reinterpret_cast<const uint4 *>(sp + kInt8CodeBytes + (gid + 8) * 16)};
+          for (int gp = 0; gp < 2; ++gp) {  // two groups per ldmatrix
+            uint32_t w[4];
+            ldsm_x4(w, sa + gp * 512);
 #pragma unroll
-        for (int gp = 0; gp < 2; ++gp) {  // two groups per ldmatrix
-          uint32_t w[4];
-          ldsm_x4(w, sa + gp * 512 + ld);
+            for (int gg = 0; gg < 2; ++gg) {
+              const int g = 2 * gp + gg;
+              uint32_t lo[4], hi[4];
+              nib_pairs_v_sub(w[2 * gg], lo);
+              nib_pairs_v_sub(w[2 * gg + 1], hi);
+              float d[4];
+              mma_f16_zero(d, lo[0], hi[0], lo[2], hi[2], q4[g][0], q4[g][1]);
+              mma_f16(d, lo[1], hi[1], lo[3], hi[3], q4[g][2], q4[g][3]);
 #pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            const int g = 2 * gp + gg;
-            uint32_t lo[4], hi[4];
-            nib_pairs_v_sub(w[2 * gg], lo);
-            nib_pairs_v_sub(w[2 * gg + 1], hi);
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(d, lo[0], hi[0], lo[2], hi[2], q4[g][0], q4[g][1]);
-            mma_f16(d, lo[1], hi[1], lo[3], hi[3], q4[g][2], q4[g][3]);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t pw = g == 0 ? par[hf].x : g == 1 ? par[hf].y : g == 2 ? par[hf].z : par[hf].w;
-              const float2 sm = h2_to_f2(pw);  // (scale, min)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                s[hf][e] = fmaf(d[2 * hf + e] * (kSubUnscale * kq[e]), sm.x, s[hf][e]);
-                s[hf][e] = fmaf(qs[g][e], sm.y, s[hf][e]);
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t pw = g == 0 ? par[hf].x : g == 1 ? par[hf].y : g == 2 ? par[hf].z : par[hf].w;
+                const float2 sm = h2_to_f2(pw);  // (scale, min)
+                z[hf] = ffma2(make_float2(d[2 * hf], d[2 * hf + 1]), make_float2(sm.x, sm.x), z[hf]);
+                z[hf] = ffma2(qs[g], make_float2(sm.y, sm.y), z[hf]);
               }
             }
           }
-        }
-      } else if (ok) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+          s[0] = ffma2(z[0], kk, ls);
+          s[1] = ffma2(z[1], kk, ls);
+        } else {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
-          uint32_t w[4];
-          ldsm_x4(w, sa + pr * 512 + ld);
+          for (int pr = 0; pr < 4; ++pr) {
+            uint32_t w[4];
+            ldsm_x4(w, sa + pr * 512);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t ulo = w[2 * hf] ^ 0x80808080u, uhi = w[2 * hf + 1] ^ 0x80808080u;
+              mma_f16(d, s8_pair<0x4140>(ulo), s8_pair<0x4140>(uhi), s8_pair<0x4342>(ulo),
+                      s8_pair<0x4342>(uhi), q8[2 * pr + hf][0], q8[2 * pr + hf][1]);
+            }
+          }
+          const uint16_t *sc = reinterpret_cast<const uint16_t *>(sp + kInt8CodeBytes);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t ulo = w[2 * hf] ^ 0x80808080u, uhi = w[2 * hf + 1] ^ 0x80808080u;
-            mma_f16(d, s8_pair<0x4140>(ulo), s8_pair<0x4140>(uhi), s8_pair<0x4342>(ulo),
-                    s8_pair<0x4342>(uhi), q8[2 * pr + hf][0], q8[2 * pr + hf][1]);
+            const float ks = __half2float(__ushort_as_half(sc[gid + 8 * hf]));
+            s[hf] = ffma2(make_float2(d[2 * hf] * ks, d[2 * hf + 1] * ks), kq, ls);
           }
         }
-        const uint16_t *sc = reinterpret_cast<const uint16_t *>(sp + kInt8CodeBytes);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float ks = __half2float(__ushort_as_half(sc[gid + 8 * hf]));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) s[hf][e] = fmaf(d[2 * hf + e] * ks, kq[e], -ls[e]);
-        }
-      }
-      if (ok) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float w = fast_exp2(s[hf][0]) + fast_exp2(s[hf][1]);
-          w += __shfl_xor_sync(0xffffffffu, w, 1);
-          w += __shfl_xor_sync(0xffffffffu, w, 2);
-          if (tig == 0 && in[hf]) acc_out[acc0 + pos[hf]] = old[hf] + w;
-        }
+        float w0 = fast_exp2(s[0].x) + fast_exp2(s[0].y), w1 = fast_exp2(s[1].x) + fast_exp2(s[1].y);
+        // sums over the four lanes of a slot: one exchange gives each lane one of its two slots
+        const float give = (tig & 1) ? w0 : w1, keep = (tig & 1) ? w1 : w0;
+        float w = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+        w += __shfl_xor_sync(0xffffffffu, w, 2);
+        if (in) acc_out[acc0 + pos] = old + w;
       }
       __syncwarp();
-      if (issued < k1) issue(issued++);
+      if (issued < pairs) issue(issued++);
     }
     if (dead) return;
     t += k1 - k0;
@@ -330,8 +322,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
 // ---------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
-
 // Totals in their order as unsigned keys: NaN below everything, -0 as +0.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0u;
@@ -339,11 +329,152 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 
-// One CTA per (sequence, kv head). The k-th largest key of the candidates [S, L - R) by
-// four passes over 8 bits each; equal keys at the border are taken from the lowest position
-// on.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(
-    CacheView c, const float *__restrict__ acc, int acc_stride, int budget, int32_t *keep,
+// One CTA per (sequence, kv head); a thread holds K keys of the row in registers, striped over the
+// block (position i * 512 + thread), so the row is read once. The key at the border by digits of 8
+// bits from the top: a histogram of the candidates that agree with the digits so far (four copies
+// of it, by lane, against collisions of equal digits), until a digit's keys are all to be taken or
+// all four digits are known; then of the keys equal to the border the lowest positions. One scan
+// over the (stripe, warp) counts of taken and of equal keys gives every kept position its place.
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kHistCopies = 4;
+
+template <int K>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(CacheView c, int longest, const float *__restrict__ acc,
+                                                             int acc_stride, int budget, int32_t *keep,
+                                                             int32_t *new_lens, int32_t *err) {
+  __shared__ int hist[256 * kHistCopies];
+  __shared__ uint32_t cnt[K * kSelWarps];  // taken keys, equal keys << 16, of a stripe's warp
+  __shared__ uint32_t part[kSelWarps];
+  __shared__ uint32_t s_border;
+  __shared__ int s_need, s_done;
+  const int H = c.num_kv_heads, S = c.num_sinks, R = c.num_recent;
+  const int b = blockIdx.x / H, h = blockIdx.x - b * H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int L = c.seq_lens[b];
+  int32_t *out = keep + static_cast<size_t>(blockIdx.x) * budget;
+  const float *row = acc + static_cast<size_t>(blockIdx.x) * acc_stride;
+  if (L < 0 || L > longest) {  // (at most K * 512)
+    if (tid == 0) set_err(err, KV4_DEVERR_SEQ_LEN);
+    L = 0;
+  }
+  if (h == 0 && tid == 0) new_lens[b] = min(L, budget);
+  if (L <= budget) {
+    for (int j = tid; j < budget; j += kSelThreads) out[j] = j < L ? j : -1;
+    return;
+  }
+  const int lo = S, hi = L - R;  // candidates (hi - lo > budget - S - R)
+  int need = budget - S - R;     // how many of them stay
+  uint32_t key[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int p = i * kSelThreads + tid;
+    key[i] = p >= lo && p < hi ? __float_as_uint(__ldg(row + p)) : 0x7fc00000u;
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i) key[i] = order_key(__uint_as_float(key[i]));
+  uint32_t border = 0u;  // its digits so far
+  bool whole = false;    // every key from the border on is taken
+  for (int shift = 24; shift >= 0 && need > 0 && !whole; shift -= 8) {
+    for (int i = tid; i < 256 * kHistCopies; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int p = i * kSelThreads + tid;
+      if (p >= lo && p < hi && (shift == 24 || ((key[i] ^ border) >> ((shift + 8) & 31)) == 0u))
+        atomicAdd(&hist[((key[i] >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane l: digits 255 - 8l .. 248 - 8l, from the largest down
+      int n[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int4 v = *reinterpret_cast<const int4 *>(&hist[(255 - 8 * lane - i) * kHistCopies]);
+        n[i] = v.x + v.y + v.z + v.w;
+        sum += n[i];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      int above = incl - sum;
+      if (above < need && need <= incl) {
+        int at = -1, size = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (at < 0 && above + n[i] >= need) at = i, size = n[i];
+          if (at < 0) above += n[i];
+        }
+        s_border = border | (static_cast<uint32_t>(255 - 8 * lane - at) << shift);
+        s_need = need - above;
+        s_done = size == need - above;
+      }
+    }
+    __syncthreads();
+    border = s_border;
+    need = s_need;
+    whole = s_done != 0;
+  }
+  // taken: sinks, recents, keys above the border (from it on where `whole`); equal: keys at it
+  auto taken = [&](int i, int p) {
+    if (p < lo || p >= hi) return p < L;
+    return need > 0 && (whole ? key[i] >= border : key[i] > border);
+  };
+  auto equal = [&](int i, int p) { return need > 0 && !whole && p >= lo && p < hi && key[i] == border; };
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int p = i * kSelThreads + tid;
+    const unsigned mt = __ballot_sync(0xffffffffu, taken(i, p)), me = __ballot_sync(0xffffffffu, equal(i, p));
+    if (lane == 0) cnt[i * kSelWarps + warp] = __popc(mt) | (__popc(me) << 16);
+  }
+  __syncthreads();
+  // exclusive scan of the K * 16 counts, K / 32 rounded up of them per thread
+  constexpr int kPer = (K * kSelWarps + kSelThreads - 1) / kSelThreads;
+  uint32_t v[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = tid * kPer + i;
+    v[i] = at < K * kSelWarps ? cnt[at] : 0u;
+    sum += v[i];
+  }
+  uint32_t incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  uint32_t base = incl - sum;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) base += w < warp ? part[w] : 0u;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = tid * kPer + i;
+    if (at < K * kSelWarps) cnt[at] = base;
+    base += v[i];
+  }
+  __syncthreads();
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int p = i * kSelThreads + tid;
+    const bool t = taken(i, p), e = equal(i, p);
+    const unsigned mt = __ballot_sync(0xffffffffu, t), me = __ballot_sync(0xffffffffu, e);
+    const uint32_t before = cnt[i * kSelWarps + warp];
+    const int ties = static_cast<int>(before >> 16) + __popc(me & below);  // equal keys before this one
+    const int at = static_cast<int>(before & 0xffffu) + __popc(mt & below) + min(ties, need);
+    if ((t || (e && ties < need)) && at < budget) out[at] = p;
+  }
+}
+
+// Rows too long for the registers: the same selection, the row read again for each digit and in
+// order for the places.
+constexpr int kLongThreads = 1024;
+__global__ void __launch_bounds__(kLongThreads) select_long_kernel(
+    CacheView c, int longest, const float *__restrict__ acc, int acc_stride, int budget, int32_t *keep,
     int32_t *new_lens, int32_t *err) {
   __shared__ int hist[256];
   __shared__ int warp_cnt[2][32];
@@ -355,7 +486,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
   int L = c.seq_lens[b];
   int32_t *out = keep + static_cast<size_t>(blockIdx.x) * budget;
   const float *row = acc + static_cast<size_t>(blockIdx.x) * acc_stride;
-  const bool bad = L < 0 || L > acc_stride;
+  const bool bad = L < 0 || L > longest;
   if (bad) {
     if (threadIdx.x == 0) set_err(err, KV4_DEVERR_SEQ_LEN);
     L = 0;
@@ -483,30 +614,92 @@ __device__ __forceinline__ uint4 *row_piece(const CacheView &c, size_t blk, int 
   return reinterpret_cast<uint4 *>(par + slot * 8);
 }
 
-// A warp per (sequence, page of kept rows, kv head): lane l moves piece l / 16 + 2i of the
-// row in slot l % 16, so that every store instruction fills 256-byte runs.
-__global__ void __launch_bounds__(256) compact_kernel(CacheView c, Moves mv, int32_t *err) {
+// The recent window's INT8 copies: position p (before) is p - (L - n) afterwards, so slot p mod R
+// moves to slot (p - (L - n)) mod R, of the same ring or another. One CTA of 256 threads per
+// (sequence, kv head); all rows (at most 144, 16 pieces of 16 bytes each) are held in registers
+// before any is written.
+__device__ __forceinline__ void move_ring(const CacheView &c, const Moves &mv, int b, int h, int32_t *err) {
+  constexpr int kPieces = KV4_MAX_PROTECTED * 16 / 256;  // 9 per thread
+  const int H = c.num_kv_heads, S = c.num_sinks, R = c.num_recent;
+  const int L = c.seq_lens[b];
+  const int n = kept_rows(c, mv, b, L, nullptr);
+  const int lo = max(S, n - R);  // first position of the window afterwards
+  if (lo >= n) return;
+  const int from = c.ring_idx ? c.ring_idx[b] : b;
+  const int to = mv.dst_ring ? mv.dst_ring[b] : from;
+  if (from < 0 || from >= c.num_rings || to < 0 || to >= c.num_rings) {
+    if (threadIdx.x == 0) set_err(err, KV4_DEVERR_SIDE_IDX);
+    return;
+  }
+  const int gone = L - n, cnt = n - lo;
+  if (from == to && gone % R == 0) return;
+  const int32_t *keep = mv.keep + (static_cast<size_t>(b) * H + h) * mv.budget;
+  // the window must have been kept whole
+  const bool bad = threadIdx.x < cnt && keep[lo + threadIdx.x] != lo + static_cast<int>(threadIdx.x) + gone;
+  const size_t src = (static_cast<size_t>(from) * H + h) * c.ring_tiles;
+  const size_t dst = (static_cast<size_t>(to) * H + h) * c.ring_tiles;
+  const int s0 = (lo + gone) % R, d0 = lo % R;  // slots of the window's first row
+  const int x = threadIdx.x & 15;               // piece: 8 strips of K, 8 of V
+  const int8_t *codes = x < 8 ? c.ring_k : c.ring_v;
+  const uint16_t *scales = x < 8 ? c.ring_ks : c.ring_vs;
+  uint4 v[kPieces];
+  uint16_t sc[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int r = i * 16 + (threadIdx.x >> 4);
+    int slot = s0 + r;
+    slot -= slot >= R ? R : 0;
+    if (r < cnt) {
+      v[i] = *reinterpret_cast<const uint4 *>(codes + (src + slot / kPage) * kInt8CodeBytes +
+                                              (x & 7) * (kPage * 16) + (slot % kPage) * 16);
+      if ((x & 7) == 0) sc[i] = scales[src * kPage + slot];
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_err(err, KV4_DEVERR_KEEP);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int r = i * 16 + (threadIdx.x >> 4);
+    int slot = d0 + r;
+    slot -= slot >= R ? R : 0;
+    if (r < cnt) {
+      *reinterpret_cast<uint4 *>((x < 8 ? c.ring_k : c.ring_v) + (dst + slot / kPage) * kInt8CodeBytes +
+                                 (x & 7) * (kPage * 16) + (slot % kPage) * 16) = v[i];
+      if ((x & 7) == 0) (x < 8 ? c.ring_ks : c.ring_vs)[dst * kPage + slot] = sc[i];
+    }
+  }
+}
+
+// To other pages. Of a sequence's blocks the first H move its ring, a kv head each; the others have a
+// warp per (page of kept rows, kv head), where lane l moves piece l / 16 + 2i of the row in slot l % 16,
+// so that every store instruction fills 256-byte runs. Bound by HBM, where the rows of a page that
+// are kept share 32-byte sectors with the ones that are not.
+__global__ void __launch_bounds__(256) compact_kernel(CacheView c, Moves mv, int page_blocks, int32_t *err) {
   const int lane = threadIdx.x & 31;
   const int H = c.num_kv_heads;
-  const int per_seq = (mv.budget + kPage - 1) / kPage;
-  const long long task = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int h = static_cast<int>(task % H);
-  const long long rest = task / H;
-  const int dp = static_cast<int>(rest % per_seq);
-  const int b = static_cast<int>(rest / per_seq);
-  if (b >= c.num_seqs) return;
+  const int b = blockIdx.x / (H + page_blocks), at = blockIdx.x - b * (H + page_blocks);
+  if (at < H) {
+    if (c.num_recent > 0) move_ring(c, mv, b, at, err);
+    return;
+  }
+  const int task = (at - H) * 8 + (threadIdx.x >> 5);
+  const int dp = task / H, h = task - dp * H;
+  if (dp >= (mv.budget + kPage - 1) / kPage) return;
+  const size_t unit = static_cast<size_t>(b) * H + h;
+  const int j = dp * kPage + (lane & 15);
+  // (what the row's own loads need is asked for at once)
+  const int src = j < mv.budget ? mv.keep[unit * mv.budget + j] : -1;
+  const int dpage = dp < mv.dst_max_pages ? mv.dst_table[static_cast<size_t>(b) * mv.dst_max_pages + dp] : -1;
   const int L = c.seq_lens[b];
   const int n = kept_rows(c, mv, b, L, dp == 0 && h == 0 ? err : nullptr);
-  const int j = dp * kPage + (lane & 15);
   if (dp * kPage >= n) return;
-  const int dpage = mv.dst_table[static_cast<size_t>(b) * mv.dst_max_pages + dp];
   if (dpage < 0 || dpage >= c.num_pages) {
     if (lane == 0) set_err(err, KV4_DEVERR_PAGE_ID);
     return;
   }
   if (j >= n) return;
-  const size_t unit = static_cast<size_t>(b) * H + h;
-  const int src = mv.keep[unit * mv.budget + j];
   if (src < j || src >= L) {  // (ascending positions have src >= j)
     set_err(err, KV4_DEVERR_KEEP);
     return;
@@ -518,12 +711,19 @@ __global__ void __launch_bounds__(256) compact_kernel(CacheView c, Moves mv, int
   }
   const size_t sb = static_cast<size_t>(spage) * H + h, db = static_cast<size_t>(dpage) * H + h;
   const int half = lane >> 4;
+  const bool totals = mv.acc_in && half == 0;
+  const float a = totals ? mv.acc_in[unit * mv.in_stride + src] : 0.f;
   uint4 v[5];
 #pragma unroll
   for (int i = 0; i < 5; ++i) v[i] = *row_piece(c, sb, src % kPage, 2 * i + half);
 #pragma unroll
   for (int i = 0; i < 5; ++i) *row_piece(c, db, lane & 15, 2 * i + half) = v[i];
-  if (mv.acc_in && half == 0) mv.acc_out[unit * mv.out_stride + j] = mv.acc_in[unit * mv.in_stride + src];
+  if (totals) mv.acc_out[unit * mv.out_stride + j] = a;
+}
+
+__global__ void __launch_bounds__(256) ring_kernel(CacheView c, Moves mv, int32_t *err) {
+  const int H = c.num_kv_heads, b = blockIdx.x / H;
+  move_ring(c, mv, b, blockIdx.x - b * H, err);
 }
 
 // In the sequence's own pages: one CTA per (sequence, kv head), 16 rows per warp and round.
@@ -575,56 +775,6 @@ __global__ void __launch_bounds__(kInPlaceThreads) compact_in_place_kernel(Cache
   }
 }
 
-// The recent window's INT8 copies: position p (before) is p - (L - n) afterwards, so slot
-// p mod R moves to slot (p - (L - n)) mod R, of the same ring or another. One CTA per
-// (sequence, kv head); all rows are read before any is written.
-__global__ void __launch_bounds__(256) ring_kernel(CacheView c, Moves mv, int32_t *err) {
-  extern __shared__ __align__(16) uint8_t rows[];  // [2][R][128] codes, then [2][R] scales
-  const int H = c.num_kv_heads, S = c.num_sinks, R = c.num_recent;
-  const int b = blockIdx.x / H, h = blockIdx.x - b * H;
-  const int L = c.seq_lens[b];
-  const int n = kept_rows(c, mv, b, L, nullptr);
-  const int lo = max(S, n - R);  // first position of the window afterwards
-  if (lo >= n) return;
-  const int from = c.ring_idx ? c.ring_idx[b] : b;
-  const int to = mv.dst_ring ? mv.dst_ring[b] : from;
-  if (from < 0 || from >= c.num_rings || to < 0 || to >= c.num_rings) {
-    if (threadIdx.x == 0) set_err(err, KV4_DEVERR_SIDE_IDX);
-    return;
-  }
-  if (from == to && (L - n) % R == 0) return;
-  uint16_t *scales = reinterpret_cast<uint16_t *>(rows + 2 * R * kHeadDim);
-  const int32_t *keep = mv.keep + static_cast<size_t>(blockIdx.x) * mv.budget;
-  const size_t src = (static_cast<size_t>(from) * H + h) * c.ring_tiles;
-  const size_t dst = (static_cast<size_t>(to) * H + h) * c.ring_tiles;
-  const int cnt = n - lo;
-  bool bad = false;  // the window must have been kept whole
-  for (int i = threadIdx.x; i < cnt; i += blockDim.x) bad |= keep[lo + i] != lo + i + (L - n);
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) set_err(err, KV4_DEVERR_KEEP);
-    return;
-  }
-  for (int i = threadIdx.x; i < cnt * 16; i += blockDim.x) {  // 16-byte pieces: 8 of K, 8 of V
-    const int r = i >> 4, x = i & 15, slot = (lo + r + (L - n)) % R;
-    const int8_t *codes = x < 8 ? c.ring_k : c.ring_v;
-    const size_t tile = src + slot / kPage;
-    reinterpret_cast<uint4 *>(rows)[i] = *reinterpret_cast<const uint4 *>(
-        codes + tile * kInt8CodeBytes + (x & 7) * (kPage * 16) + (slot % kPage) * 16);
-    if (x == 0) scales[2 * r] = c.ring_ks[src * kPage + slot];
-    if (x == 8) scales[2 * r + 1] = c.ring_vs[src * kPage + slot];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < cnt * 16; i += blockDim.x) {
-    const int r = i >> 4, x = i & 15, slot = (lo + r) % R;
-    int8_t *codes = x < 8 ? c.ring_k : c.ring_v;
-    const size_t tile = dst + slot / kPage;
-    *reinterpret_cast<uint4 *>(codes + tile * kInt8CodeBytes + (x & 7) * (kPage * 16) + (slot % kPage) * 16) =
-        reinterpret_cast<const uint4 *>(rows)[i];
-    if (x == 0) c.ring_ks[dst * kPage + slot] = scales[2 * r];
-    if (x == 8) c.ring_vs[dst * kPage + slot] = scales[2 * r + 1];
-  }
-}
-
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
@@ -652,10 +802,19 @@ cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *
   return cudaGetLastError();
 }
 
-cudaError_t launch_select(const CacheView &c, const float *acc, int acc_stride, int budget,
+cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc, int acc_stride, int budget,
                           int32_t *keep, int32_t *new_lens, int32_t *err, cudaStream_t s) {
-  select_kernel<<<c.num_seqs * c.num_kv_heads, kSelThreads, 0, s>>>(c, acc, acc_stride, budget, keep,
-                                                                   new_lens, err);
+  const int units = c.num_seqs * c.num_kv_heads;
+  const int longest = max_seq_len < acc_stride ? max_seq_len : acc_stride;
+  // the fewest keys per thread that hold the longest row
+  if (longest <= 4 * kSelThreads)
+    select_kernel<4><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
+  else if (longest <= 12 * kSelThreads)
+    select_kernel<12><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
+  else if (longest <= 32 * kSelThreads)
+    select_kernel<32><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
+  else
+    select_long_kernel<<<units, kLongThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
   return cudaGetLastError();
 }
 
@@ -666,15 +825,15 @@ cudaError_t launch_compact(const CacheView &c, const int32_t *keep, int budget, 
   const Moves mv{keep, budget, new_lens, dst_table, dst_max_pages, dst_ring, acc_in, acc_out, in_stride, out_stride};
   const int units = c.num_seqs * c.num_kv_heads;
   if (dst_table) {
-    const long long warps = static_cast<long long>(units) * ((budget + kPage - 1) / kPage);
-    compact_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(c, mv, err);
-  } else {
-    compact_in_place_kernel<<<units, kInPlaceThreads, 0, s>>>(c, mv, err);
+    const int pages = (budget + kPage - 1) / kPage;
+    const int blocks = (pages * c.num_kv_heads + 7) / 8;
+    compact_kernel<<<static_cast<unsigned>(c.num_seqs) * (c.num_kv_heads + blocks), 256, 0, s>>>(c, mv, blocks, err);
+    return cudaGetLastError();
   }
+  compact_in_place_kernel<<<units, kInPlaceThreads, 0, s>>>(c, mv, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || c.num_recent == 0) return e;
-  const size_t smem = static_cast<size_t>(c.num_recent) * (2 * kHeadDim + 4);
-  ring_kernel<<<units, 256, smem, s>>>(c, mv, err);
+  ring_kernel<<<units, 256, 0, s>>>(c, mv, err);
   return cudaGetLastError();
 }
 

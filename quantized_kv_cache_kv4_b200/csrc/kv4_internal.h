@@ -162,7 +162,7 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
 cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
                            const float *acc_in, float *acc_out, int acc_stride, int32_t *err,
                            cudaStream_t s);
-cudaError_t launch_select(const CacheView &c, const float *acc, int acc_stride, int budget,
+cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc, int acc_stride, int budget,
                           int32_t *keep, int32_t *new_lens, int32_t *err, cudaStream_t s);
 cudaError_t launch_compact(const CacheView &c, const int32_t *keep, int budget,
                            const int32_t *new_lens, const int32_t *dst_table, int dst_max_pages,

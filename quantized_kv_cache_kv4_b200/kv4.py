@@ -424,42 +424,46 @@ def baseline_decode_attention(cache: BaselineCache, batch: BatchTensors, q: torc
 # 8-bit block-scaled cache
 # ----------------------------------------------------------------------------
 
-def _tensor(t, what, dtype, shape=None, optional=False):
-    """Device pointer of an argument whose type (one, or a tuple) and shape are checked (None
-    in a shape: any size)."""
-    if t is None and optional:
-        return None
+def _addr(t, what, dtype, shape):
+    """Address of a contiguous CUDA tensor of this type and shape (None in a shape: any size)."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what}: a tensor is wanted, not {type(t).__name__}")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} is wanted, not {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(
+    if t.shape != shape and (t.dim() != len(shape) or any(
             n is not None and n != m for n, m in zip(shape, t.shape))):
         raise ValueError(f"{what}: shape {tuple(shape)} is wanted, not {tuple(t.shape)}")
-    return _ptr(t)
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted "
+                         f"(got device={t.device}, contiguous={t.is_contiguous()})")
+    return t.data_ptr()
 
 
-def _on_device(fn, stream, *tensors):
-    """Calls fn(stream handle) with the tensors' device current: a launch goes to the current
+def _addr_or_null(t, what, dtype, shape):
+    return None if t is None else _addr(t, what, dtype, shape)
+
+
+def _launch(fn, args, err, stream, *tensors):
+    """fn(*args, err, stream) with the tensors' device current: a launch goes to the current
     device, whichever the caller left current."""
-    dev = None
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"kv4 arguments on different devices: {dev} and {t.device}")
-    if dev is None or dev.index == torch.cuda.current_device():
-        return fn(_stream(stream))
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"kv4 arguments on different devices: {tensors[0].device} and {t.device}")
+    e = _addr_or_null(err, "err", torch.int32, (1,))
+    if dev == torch.cuda.current_device():
+        return fn(*args, e, torch.cuda.current_stream(dev).cuda_stream if stream is None
+                  else stream.cuda_stream)
     with torch.cuda.device(dev):
-        return fn(_stream(stream))
+        return fn(*args, e, torch.cuda.current_stream(dev).cuda_stream if stream is None
+                  else stream.cuda_stream)
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class Block8Cache:
     """Device storage of one layer's 8-bit block-scaled cache (layout in kv4.h): codes
     [pages, Hkv, 8 strips, 16 slots, 16] as int8 (BLOCK8_INT8) or float8_e4m3fn
-    (BLOCK8_E4M3), scales float16 [pages, Hkv]."""
+    (BLOCK8_E4M3), scales float16 [pages, Hkv]. Its tensors are checked once, here."""
 
     fmt: int
     cfg: Config
@@ -467,19 +471,24 @@ class Block8Cache:
     v: torch.Tensor
     k_scales: torch.Tensor
     v_scales: torch.Tensor
+    pool: PagedPool = dataclasses.field(init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        if self.fmt not in _BLOCK8_DTYPES:
+            raise ValueError(f"unknown block8 format {self.fmt}")
+        code, pages, H = _BLOCK8_DTYPES[self.fmt], self.k.shape[0], self.cfg.num_kv_heads
+        codes, scales = (pages, H, 8, PAGE, 16), (pages, H)
+        object.__setattr__(self, "pool", PagedPool(
+            _addr(self.k, "k", code, codes), _addr(self.v, "v", code, codes),
+            _addr(self.k_scales, "k_scales", torch.float16, scales),
+            _addr(self.v_scales, "v_scales", torch.float16, scales), pages))
 
     @property
     def num_pages(self):
         return self.k.shape[0]
 
     def pool_struct(self) -> PagedPool:
-        if self.fmt not in _BLOCK8_DTYPES:
-            raise ValueError(f"unknown block8 format {self.fmt}")
-        pages, H = self.k.shape[0], self.cfg.num_kv_heads
-        code, shape = _BLOCK8_DTYPES[self.fmt], (pages, H, 8, PAGE, 16)
-        return PagedPool(_tensor(self.k, "k", code, shape), _tensor(self.v, "v", code, shape),
-                         _tensor(self.k_scales, "k_scales", torch.float16, (pages, H)),
-                         _tensor(self.v_scales, "v_scales", torch.float16, (pages, H)), pages)
+        return self.pool
 
 
 _BLOCK8_DTYPES = {BLOCK8_INT8: torch.int8, BLOCK8_E4M3: torch.float8_e4m3fn}
@@ -500,16 +509,13 @@ def block8_append(cache: Block8Cache, batch: BatchTensors, k_new: torch.Tensor,
                   v_new: torch.Tensor, new_indptr: torch.Tensor | None = None,
                   err: torch.Tensor | None = None, stream=None):
     """k_new, v_new: bf16 [rows, Hkv, 128]; new_indptr int32 [B+1] or None (one row per seq)."""
-    rows = (None, cache.cfg.num_kv_heads, HEAD_DIM)
-    k = _tensor(k_new, "k_new", torch.bfloat16, rows)
-    v = _tensor(v_new, "v_new", torch.bfloat16, k_new.shape)
-    B = batch.seq_lens.shape[0]
-    ip = _tensor(new_indptr, "new_indptr", torch.int32, (B + 1,), optional=True)
-    pool, bs = cache.pool_struct(), batch.struct()
-    st = _on_device(lambda s: _lib.kv4_block8_append(
-        cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(pool), ctypes.byref(bs), k, v, ip,
-        k_new.shape[0], _ptr(err), s), stream, cache.k, batch.seq_lens, k_new, v_new, new_indptr)
-    _check(st, "kv4_block8_append")
+    n, bs = k_new.shape[0], batch.struct()
+    rows = (n, cache.cfg.num_kv_heads, HEAD_DIM)
+    args = (cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(cache.pool), ctypes.byref(bs),
+            _addr(k_new, "k_new", torch.bfloat16, rows), _addr(v_new, "v_new", torch.bfloat16, rows),
+            _addr_or_null(new_indptr, "new_indptr", torch.int32, (bs.num_seqs + 1,)), n)
+    _check(_launch(_lib.kv4_block8_append, args, err, stream, cache.k, batch.seq_lens, k_new, v_new,
+                   new_indptr), "kv4_block8_append")
 
 
 def block8_workspace_size(cfg: Config, num_seqs: int, total_q: int, max_q_len: int,
@@ -528,19 +534,17 @@ def block8_attention(cache: Block8Cache, batch: BatchTensors, q: torch.Tensor, o
     """q, out: bf16 [rows, Hq, 128]; q_indptr int32 [B+1]: sequence b's rows are its last
     positions, at most max_q_len of them, causal (None: one per sequence); out_f32 fp32 like
     out; lse fp32 [rows, Hq]; workspace: uint8, block8_workspace_size(...) bytes."""
-    n, Hq = q.shape[0], cache.cfg.num_q_heads
-    B = batch.seq_lens.shape[0]
-    args = (_tensor(q, "q", torch.bfloat16, (None, Hq, HEAD_DIM)),
-            _tensor(q_indptr, "q_indptr", torch.int32, (B + 1,), optional=True), n, max_q_len,
-            _tensor(out, "out", torch.bfloat16, q.shape),
-            _tensor(out_f32, "out_f32", torch.float32, q.shape, optional=True),
-            _tensor(lse, "lse", torch.float32, (n, Hq), optional=True),
-            _tensor(workspace, "workspace", torch.uint8, (None,)), workspace.numel(), _ptr(err))
-    pool, bs = cache.pool_struct(), batch.struct()
-    st = _on_device(lambda s: _lib.kv4_block8_attention(
-        cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(pool), ctypes.byref(bs), *args, s), stream,
-        cache.k, batch.seq_lens, q, out, q_indptr, workspace)
-    _check(st, "kv4_block8_attention")
+    n, Hq, bs = q.shape[0], cache.cfg.num_q_heads, batch.struct()
+    rows = (n, Hq, HEAD_DIM)
+    args = (cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(cache.pool), ctypes.byref(bs),
+            _addr(q, "q", torch.bfloat16, rows),
+            _addr_or_null(q_indptr, "q_indptr", torch.int32, (bs.num_seqs + 1,)), n, max_q_len,
+            _addr(out, "out", torch.bfloat16, rows),
+            _addr_or_null(out_f32, "out_f32", torch.float32, rows),
+            _addr_or_null(lse, "lse", torch.float32, (n, Hq)),
+            _addr(workspace, "workspace", torch.uint8, (None,)), workspace.numel())
+    _check(_launch(_lib.kv4_block8_attention, args, err, stream, cache.k, batch.seq_lens, q, out,
+                   workspace, q_indptr, out_f32, lse), "kv4_block8_attention")
 
 
 # ----------------------------------------------------------------------------
@@ -553,33 +557,32 @@ def attention_weights(cache: Cache, batch: BatchTensors, q: torch.Tensor, lse: t
     """acc_out = acc_in + each position's attention weight in this decode step. q bf16
     [B, Hq, 128]; lse fp32 [B, Hq] as decode_attention wrote it; acc_in, acc_out fp32
     [B, Hkv, positions] (may be the same; None: zeros)."""
-    B, cfg = batch.seq_lens.shape[0], cache.cfg
-    total = (B, cfg.num_kv_heads, None)
-    args = (_tensor(q, "q", torch.bfloat16, (B, cfg.num_q_heads, HEAD_DIM)),
-            _tensor(lse, "lse", torch.float32, (B, cfg.num_q_heads)),
-            _tensor(acc_in, "acc_in", torch.float32, acc_out.shape, optional=True),
-            _tensor(acc_out, "acc_out", torch.float32, total), acc_out.shape[2], _ptr(err))
-    pool, side, bs = cache.pool_struct(), cache.side_struct(), batch.struct()
-    st = _on_device(lambda s: _lib.kv4_attention_weights(
-        ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(side), ctypes.byref(bs), *args, s),
-        stream, cache.k_codes, batch.seq_lens, q, lse, acc_in, acc_out)
-    _check(st, "kv4_attention_weights")
+    cfg, bs = cache.cfg, batch.struct()
+    B, stride = bs.num_seqs, acc_out.shape[-1]
+    total = (B, cfg.num_kv_heads, stride)
+    pool, side = cache.pool_struct(), cache.side_struct()
+    args = (ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(side), ctypes.byref(bs),
+            _addr(q, "q", torch.bfloat16, (B, cfg.num_q_heads, HEAD_DIM)),
+            _addr(lse, "lse", torch.float32, (B, cfg.num_q_heads)),
+            _addr_or_null(acc_in, "acc_in", torch.float32, total),
+            _addr(acc_out, "acc_out", torch.float32, total), stride)
+    _check(_launch(_lib.kv4_attention_weights, args, err, stream, cache.k_codes, batch.seq_lens, q,
+                   lse, acc_out, acc_in), "kv4_attention_weights")
 
 
 def evict_select(cfg: Config, batch: BatchTensors, acc: torch.Tensor, keep: torch.Tensor,
                  new_lens: torch.Tensor, err: torch.Tensor | None = None, stream=None):
     """The positions to keep: acc fp32 [B, Hkv, positions]; keep int32 [B, Hkv, budget]
     (ascending, -1 behind the last) and new_lens int32 [B] are written."""
-    B, H = batch.seq_lens.shape[0], cfg.num_kv_heads
-    args = (_tensor(acc, "acc", torch.float32, (B, H, None)), acc.shape[2], keep.shape[-1],
-            _tensor(keep, "keep", torch.int32, (B, H, None)),
-            _tensor(new_lens, "new_lens", torch.int32, (B,)), _ptr(err))
-    if keep.shape[-1] > 0 and new_lens.data_ptr() == batch.seq_lens.data_ptr() and B:
-        raise ValueError("new_lens must not be the batch's seq_lens")
     bs = batch.struct()
-    st = _on_device(lambda s: _lib.kv4_evict_select(ctypes.byref(cfg), ctypes.byref(bs), *args, s),
-                    stream, acc, batch.seq_lens, keep, new_lens)
-    _check(st, "kv4_evict_select")
+    B, H, stride, budget = bs.num_seqs, cfg.num_kv_heads, acc.shape[-1], keep.shape[-1]
+    if B and new_lens.data_ptr() == bs.seq_lens:
+        raise ValueError("new_lens must not be the batch's seq_lens")
+    args = (ctypes.byref(cfg), ctypes.byref(bs), _addr(acc, "acc", torch.float32, (B, H, stride)), stride,
+            budget, _addr(keep, "keep", torch.int32, (B, H, budget)),
+            _addr(new_lens, "new_lens", torch.int32, (B,)))
+    _check(_launch(_lib.kv4_evict_select, args, err, stream, acc, batch.seq_lens, keep, new_lens),
+           "kv4_evict_select")
 
 
 def evict_compact(cache: Cache, batch: BatchTensors, keep: torch.Tensor, new_lens: torch.Tensor,
@@ -590,20 +593,17 @@ def evict_compact(cache: Cache, batch: BatchTensors, keep: torch.Tensor, new_len
     """Moves the kept rows (keep, new_lens as evict_select wrote them) to the front of the pages
     of dst_page_table int32 [B, pages] (None: the sequence's own), the recent window's INT8
     copies to ring dst_ring_idx int32 [B] (None: its own), and the totals to acc_out."""
-    B, cfg = batch.seq_lens.shape[0], cache.cfg
-    H = cfg.num_kv_heads
-    args = (_tensor(keep, "keep", torch.int32, (B, H, None)), keep.shape[2],
-            _tensor(new_lens, "new_lens", torch.int32, (B,)),
-            _tensor(dst_page_table, "dst_page_table", torch.int32, (B, None), optional=True),
-            0 if dst_page_table is None else dst_page_table.shape[1],
-            _tensor(dst_ring_idx, "dst_ring_idx", torch.int32, (B,), optional=True),
-            _tensor(acc_in, "acc_in", torch.float32, (B, H, None), optional=True),
-            0 if acc_in is None else acc_in.shape[2],
-            _tensor(acc_out, "acc_out", torch.float32, (B, H, None), optional=True),
-            0 if acc_out is None else acc_out.shape[2], _ptr(err))
-    pool, side, bs = cache.pool_struct(), cache.side_struct(), batch.struct()
-    st = _on_device(lambda s: _lib.kv4_evict_compact(
-        ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(side), ctypes.byref(bs), *args, s),
-        stream, cache.k_codes, batch.seq_lens, keep, new_lens, dst_page_table, dst_ring_idx,
-        acc_in, acc_out)
-    _check(st, "kv4_evict_compact")
+    cfg, bs = cache.cfg, batch.struct()
+    B, H, budget = bs.num_seqs, cfg.num_kv_heads, keep.shape[-1]
+    pages = 0 if dst_page_table is None else dst_page_table.shape[-1]
+    s_in, s_out = (0 if t is None else t.shape[-1] for t in (acc_in, acc_out))
+    pool, side = cache.pool_struct(), cache.side_struct()
+    args = (ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(side), ctypes.byref(bs),
+            _addr(keep, "keep", torch.int32, (B, H, budget)), budget,
+            _addr(new_lens, "new_lens", torch.int32, (B,)),
+            _addr_or_null(dst_page_table, "dst_page_table", torch.int32, (B, pages)), pages,
+            _addr_or_null(dst_ring_idx, "dst_ring_idx", torch.int32, (B,)),
+            _addr_or_null(acc_in, "acc_in", torch.float32, (B, H, s_in)), s_in,
+            _addr_or_null(acc_out, "acc_out", torch.float32, (B, H, s_out)), s_out)
+    _check(_launch(_lib.kv4_evict_compact, args, err, stream, cache.k_codes, batch.seq_lens, keep,
+                   new_lens, dst_page_table, dst_ring_idx, acc_in, acc_out), "kv4_evict_compact")

@@ -129,16 +129,14 @@ def test_binding_refuses_wrong_types_and_shapes(kv4):
     that are not on a GPU."""
     import torch
     t = torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    for dtype, shape in ((torch.float32, (2, 2, 128)), (torch.bfloat16, (2, 3, 128)), (torch.bfloat16, (2, 2)),
+                         (torch.bfloat16, (2, 2, None))):  # (the last: host memory)
+        with pytest.raises(ValueError):
+            kv4._addr(t, "x", dtype, shape)
     with pytest.raises(ValueError):
-        kv4._tensor(t, "x", torch.float32)
-    with pytest.raises(ValueError):
-        kv4._tensor(t, "x", torch.bfloat16, (2, 3, 128))
-    with pytest.raises(ValueError):
-        kv4._tensor(t, "x", torch.bfloat16, (2, 2))
-    with pytest.raises(ValueError):
-        kv4._tensor(t, "x", torch.bfloat16, (2, 2, None))  # host memory
-    with pytest.raises(ValueError):
-        kv4._tensor(None, "x", torch.bfloat16)
-    assert kv4._tensor(None, "x", torch.bfloat16, optional=True) is None
+        kv4._addr(None, "x", torch.bfloat16, (2, 2, 128))
+    assert kv4._addr_or_null(None, "x", torch.bfloat16, (2, 2, 128)) is None
     with pytest.raises(ValueError):
         kv4.allocate_block8_cache(5, kv4.make_config(8, 2, 0, 0), 4, device="cpu")
+    with pytest.raises(ValueError):
+        kv4.allocate_block8_cache(kv4.BLOCK8_INT8, kv4.make_config(8, 2, 0, 0), 4, device="cpu")
