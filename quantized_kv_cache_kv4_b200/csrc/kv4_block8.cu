@@ -165,7 +165,7 @@ __device__ __forceinline__ uint4 transpose4(uint32_t a, uint32_t b, uint32_t c, 
 // the table of measurements for the call it was taken on).
 constexpr int kRowsPerCta = 64;
 template <int F>
-__global__ void __launch_bounds__(256) block8_append_rows_kernel(
+__global__ void __launch_bounds__(256, 3) block8_append_rows_kernel(
     CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
     const int32_t *__restrict__ indptr, int32_t total_new, int32_t *err) {
   __shared__ int4 lead[kRowsPerCta];  // (first row, rows, slot, page)
@@ -206,13 +206,14 @@ __global__ void __launch_bounds__(256) block8_append_rows_kernel(
 #pragma unroll
     for (int i = 0; i < kPage; ++i)
       raw[i] = i < n ? *reinterpret_cast<const uint2 *>(rows + i * stride) : make_uint2(0u, 0u);
-    float amax = 0.f;
+    __nv_bfloat162 top = __float2bfloat162_rn(0.f);  // of |x|, on pairs
 #pragma unroll
     for (int i = 0; i < kPage; ++i) {
-      float x[4];
-      unpack_bf16x4(raw[i], x);
-      amax = fmaxf(amax, amax4(x));
+      const uint32_t a = raw[i].x & 0x7fff7fffu, z = raw[i].y & 0x7fff7fffu;
+      top = __hmax2(top, __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                 *reinterpret_cast<const __nv_bfloat162 *>(&z)));
     }
+    const float amax = fmaxf(__low2float(top), __high2float(top));
     uint8_t *block = (v ? c.v_codes : c.k_codes) + blk * kInt8CodeBytes;
     const float s = grow_scale<F>(block, (v ? c.v_params : c.k_params) + blk, warp_max(amax), slot, lane);
     const float y = s == 0.f ? 0.f : __frcp_rn(s);

@@ -38,10 +38,11 @@ __device__ __forceinline__ Tiles tiles_of(const CacheView &c, int acc_stride, in
 }
 
 constexpr int kWMinShare = 4;  // tiles per warp, at least
-constexpr int kWPair = 2;      // tiles of a stage
 constexpr int kWStages = 4;
-constexpr int kWTileBytes = 2304;  // K codes (at most 2048), then K scales or parameters
-constexpr int kWWarpSmem = kWStages * kWPair * kWTileBytes;
+// a stage: the K codes of two kv heads (INT8: 2 x 2048 bytes), then their scales or parameters
+constexpr int kWOffPar = 2 * kInt8CodeBytes;
+constexpr int kWStageBytes = kWOffPar + 2 * kInt4ParamBytes;
+constexpr int kWWarpSmem = kWStages * kWStageBytes;
 constexpr int kWCtaSmem = kWarps * kWWarpSmem;
 
 // D = A B, the accumulators' start being zero without registers for it.
@@ -54,32 +55,36 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a01, uint32
       : "r"(a01), "r"(a23), "r"(a45), "r"(a67), "r"(b01), "r"(b23), "f"(0.f));
 }
 
-// One warp serves one kv head's G <= 8 query heads (MMA columns). The query is scaled by a
-// power of two to [2^14, 2^15) at its largest element and enters as fp16, in which its bf16
-// elements are exact; the codes are exact in fp16 too, so the only rounding of a logit is
-// the fp32 accumulation. INT4 codes enter as fp16 subnormals (c * 2^-24, or 16 c * 2^-24
-// for the odd dims, whose query elements carry the factor 1/16); a group's scale and minimum
-// multiply its product and its query sum, s = kk sum_g (scale_g (q c)_g + min_g sum(q)_g / kk).
-// Bound by instruction issue and the reading of K: two tiles per wait and ring stage, and the
-// totals of a tile move as one load and one store of 16 lanes.
+// A warp serves HPW kv heads, the MMA's 8 columns split between them: with G <= 4 query heads
+// each two heads fill them (a head's operand is zero in the other's columns, so that both heads'
+// products meet in one accumulator), and the scaling, exponentials and bookkeeping of a tile are
+// paid once for both. The query is scaled by a power of two to [2^14, 2^15) at its largest element
+// and enters as fp16, in which its bf16 elements are exact; the codes are exact in fp16 too, so the
+// only rounding of a logit is the fp32 accumulation. INT4 codes enter as fp16 subnormals (c * 2^-24,
+// or 16 c * 2^-24 for the odd dims, whose query elements carry the factor 1/16); a group's scale and
+// minimum multiply its product and its query sum, s = kk sum_g (scale_g (q c)_g + min_g sum(q)_g / kk).
+// Bound by instruction issue and the reading of K.
+template <int HPW>
 __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     CacheView c, const uint16_t *__restrict__ q, const float *__restrict__ lse, const float *acc_in,
     float *acc_out, int acc_stride, int32_t *err) {
+  constexpr int CPH = 8 / HPW;  // columns per head
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitSmem split;
   __shared__ uint64_t bars_all[kWarps][kWStages];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = c.gqa, H = c.num_kv_heads, S = c.num_sinks, R = c.num_recent;
+  const int slots = (H + HPW - 1) / HPW;
   uint8_t *stage0 = smem + warp * kWWarpSmem;
   uint64_t *bars = bars_all[warp];
   if (lane == 0) {
-    for (int s = 0; s < kWStages; ++s) mbar_init(&bars[s], kWPair);  // an arrival per tile
+    for (int s = 0; s < kWStages; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
   const int me = blockIdx.x * kWarps + warp;
   const Share share = take_share(c.num_seqs, me, gridDim.x * kWarps, kWMinShare, split, [&](int i, bool check) {
-    return static_cast<long long>(H) *
+    return static_cast<long long>(slots) *
            tiles_of(c, acc_stride, i, check && blockIdx.x == 0 ? err : nullptr).n();
   });
   if (share.begin >= share.end) return;
@@ -91,16 +96,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
   const int ld = ((mi >> 1) * 256) + (mi & 1) * 128 + r8 * 16;  // two 16-byte strips of 16 slots
 
   for (long long t = share.begin; t < share.end;) {
-    while (t >= seq_first + static_cast<long long>(H) * ti.n()) {
-      seq_first += static_cast<long long>(H) * ti.n();
+    while (t >= seq_first + static_cast<long long>(slots) * ti.n()) {
+      seq_first += static_cast<long long>(slots) * ti.n();
       ti = tiles_of(c, acc_stride, ++b, nullptr);
     }
     const long long in_seq = t - seq_first;
     const int n_tiles = ti.n();
-    const int h = static_cast<int>(in_seq / n_tiles);
-    const int k0 = static_cast<int>(in_seq - static_cast<long long>(h) * n_tiles);
+    const int h = static_cast<int>(in_seq / n_tiles) * HPW;  // first of the warp's heads
+    const int k0 = static_cast<int>(in_seq - static_cast<long long>(h / HPW) * n_tiles);
     const int k1 = static_cast<int>(min(static_cast<long long>(n_tiles), k0 + (share.end - t)));
-    const int pairs = (k1 - k0 + kWPair - 1) / kWPair;
+    const int heads = min(HPW, H - h);
     const int L = ti.L, p0 = S / kPage, n4 = ti.int4_pages, n48 = ti.int4_pages + ti.sink;
     const int set = ti.sink ? (c.sink_idx ? c.sink_idx[b] : b) : 0;
     const int ring = ti.ring ? (c.ring_idx ? c.ring_idx[b] : b) : 0;
@@ -121,52 +126,51 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
       }
       return p;
     };
-    // Lane l < 2 copies tile 2j + l of the segment (K codes, then K scales or parameters); one
-    // that cannot be read only arrives, and its positions are left out
-    auto issue = [&](int j) {
-      const int k = k0 + kWPair * j + (lane & 1), at = (k - block0) & 31;
+    // Tile k's K codes, and its parameters or scales, of the warp's heads: an INT4 page's heads are
+    // adjacent, a side tile's are not. A tile that cannot be read only arrives, and its positions
+    // are left out.
+    auto issue = [&](int k) {
+      const int at = (k - block0) & 31;
       const int a = __shfl_sync(0xffffffffu, pid, at), z = __shfl_sync(0xffffffffu, pid_next, at);
-      if (lane >= kWPair) return;
-      const int st = j % kWStages;
-      uint8_t *dst = stage0 + (st * kWPair + lane) * kWTileBytes;
-      const uint8_t *codes = nullptr;
-      const void *par = nullptr;
-      uint32_t nc = kInt8CodeBytes, np = kInt8ScaleBytes;
+      if (lane != 0) return;
+      const int st = (k - k0) % kWStages;
+      uint8_t *dst = stage0 + st * kWStageBytes;
+      fence_proxy_async_smem();
       if (k < n4) {
         const int p = k - block0 < 32 ? a : z;
-        if (p >= 0 && k < k1) {
-          const size_t blk = static_cast<size_t>(p) * H + h;
-          codes = c.k_codes + blk * kInt4CodeBytes;
-          par = reinterpret_cast<const uint8_t *>(c.k_params) + blk * kInt4ParamBytes;
-          nc = kInt4CodeBytes;
-          np = kInt4ParamBytes;
+        mbar_arrive_expect_tx(&bars[st], p < 0 ? 0 : heads * (kInt4CodeBytes + kInt4ParamBytes));
+        if (p < 0) return;
+        const size_t blk = static_cast<size_t>(p) * H + h;
+        bulk_g2s(dst, c.k_codes + blk * kInt4CodeBytes, heads * kInt4CodeBytes, &bars[st]);
+        bulk_g2s(dst + kWOffPar, reinterpret_cast<const uint8_t *>(c.k_params) + blk * kInt4ParamBytes,
+                 heads * kInt4ParamBytes, &bars[st]);
+      } else {
+        const bool sink = k < n48, there = sink ? set_ok : ring_ok;
+        mbar_arrive_expect_tx(&bars[st], there ? heads * (kInt8CodeBytes + kInt8ScaleBytes) : 0);
+        if (!there) return;
+        for (int i = 0; i < heads; ++i) {
+          const size_t x = sink ? (static_cast<size_t>(set) * H + h + i) * c.sink_tiles + (k - n4)
+                                : (static_cast<size_t>(ring) * H + h + i) * c.ring_tiles + (k - n48);
+          bulk_g2s(dst + i * kInt8CodeBytes, (sink ? c.sink_k : c.ring_k) + x * kInt8CodeBytes, kInt8CodeBytes,
+                   &bars[st]);
+          bulk_g2s(dst + kWOffPar + i * kInt8ScaleBytes, (sink ? c.sink_ks : c.ring_ks) + x * kPage,
+                   kInt8ScaleBytes, &bars[st]);
         }
-      } else if (k < n48 ? set_ok && k < k1 : ring_ok && k < k1) {
-        const bool sink = k < n48;
-        const size_t x = sink ? (static_cast<size_t>(set) * H + h) * c.sink_tiles + (k - n4)
-                              : (static_cast<size_t>(ring) * H + h) * c.ring_tiles + (k - n48);
-        codes = reinterpret_cast<const uint8_t *>(sink ? c.sink_k : c.ring_k) + x * kInt8CodeBytes;
-        par = (sink ? c.sink_ks : c.ring_ks) + x * kPage;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive_expect_tx(&bars[st], codes ? nc + np : 0);
-      if (codes) {
-        bulk_g2s(dst, codes, nc, &bars[st]);
-        bulk_g2s(dst + kInt8CodeBytes, par, np, &bars[st]);
       }
     };
     pid = load_pages(k0);
-    int issued = min(pairs, kWStages);
-    for (int j = 0; j < issued; ++j) issue(j);
+    int issued = min(k1, k0 + kWStages);
+    for (int k = k0; k < issued; ++k) issue(k);
     pid_next = load_pages(k0 + 32);
 
-    // ---- query fragments, column gid = query head gid ----
-    const bool live = gid < G;
-    const uint16_t *qrow = q + (static_cast<size_t>(b) * H * G + h * G + gid) * kHeadDim;
+    // ---- query fragments: column gid = (head gid / CPH, query gid % CPH) ----
+    const int head_b = gid / CPH, head_c = (2 * tig) / CPH;  // of the B and of the C columns
+    const bool live = gid % CPH < G && head_b < heads;
+    const uint16_t *qrow = q + (static_cast<size_t>(b) * H * G + (h + head_b) * G + gid % CPH) * kHeadDim;
     uint32_t q8[8][2];  // INT8 strip s: dims 16s + 4tig + (0,1), (2,3)
     uint32_t q4[4][4];  // INT4 group g: dims 32g + 8tig + (0,4), (2,6), then (1,5), (3,7) / 16
     float2 qs[4];       // group sums of the columns 2tig, 2tig + 1, over kk
-    float2 kq, kk, ls;  // logit factors of the INT8 and the INT4 products; lse in log2 units
+    float2 kq, kk, ls;  // logit factors of the INT8 and the INT4 products; -lse in log2 units
     {
       float amax = 0.f;
       float v[4][8];
@@ -209,110 +213,133 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
       kq.y = __shfl_sync(0xffffffffu, step, 4 * (2 * tig + 1)) * kScaleLog2;
       kk = make_float2(kq.x * kSubUnscale, kq.y * kSubUnscale);
       // a column without a query weighs nothing
-      const float *ll = lse + (static_cast<size_t>(b) * H + h) * G;
-      ls.x = 2 * tig < G ? -ll[2 * tig] * kLog2e : -CUDART_INF_F;
-      ls.y = 2 * tig + 1 < G ? -ll[2 * tig + 1] * kLog2e : -CUDART_INF_F;
+      const int j = (2 * tig) % CPH;
+      const float *ll = lse + (static_cast<size_t>(b) * H + h + head_c) * G + j;
+      ls.x = head_c < heads && j < G ? -ll[0] * kLog2e : -CUDART_INF_F;
+      ls.y = head_c < heads && j + 1 < G ? -ll[1] * kLog2e : -CUDART_INF_F;
     }
-    const size_t acc0 = (static_cast<size_t>(b) * H + h) * acc_stride;
-    const int mine = gid + 8 * (tig & 1);  // the slot whose total this lane moves (tig < 2)
+    // the slot whose total this lane moves (HPW = 1: lanes of tig < 2 move all)
+    const int mine = gid + 8 * (tig & 1);
+    const bool moves = HPW == 1 ? tig < 2 : head_c < heads;
+    const size_t acc0 = (static_cast<size_t>(b) * H + h + (HPW == 1 ? 0 : min(head_c, heads - 1))) * acc_stride;
+    const int par_at = kWOffPar + min(head_c, heads - 1) * kInt4ParamBytes;
 
     bool dead = false;
-    for (int j = 0; j < pairs && !dead; ++j) {
-      if (kWPair * j > 0 && ((kWPair * j) & 31) == 0) {
+    for (int k = k0; k < k1; ++k) {
+      if (k - block0 == 32) {
         block0 += 32;
         pid = pid_next;
         pid_next = load_pages(block0 + 32);
       }
-      const int st = j % kWStages;
+      int pos;  // of this lane's total; whether it is one of the tile's, and the tile was read
+      bool in;
+      const bool copied = __shfl_sync(0xffffffffu, pid, (k - block0) & 31) >= 0;
+      if (k < n4) {
+        pos = (p0 + k) * kPage + mine;
+        in = pos >= S && pos < L - R && copied;
+      } else if (k < n48) {
+        pos = (k - n4) * kPage + mine;
+        in = pos < min(S, L) && set_ok;
+      } else {
+        const int slot = (k - n48) * kPage + mine;
+        const int lastp = L - 1, base = lastp - lastp % R + slot;  // the last p < L with p mod R = slot
+        pos = base > lastp ? base - R : base;
+        in = slot < R && pos >= max(S, L - R) && ring_ok;
+      }
+      in = in && moves;
+      const float old = in && acc_in != nullptr ? acc_in[acc0 + pos] : 0.f;
+      const int st = (k - k0) % kWStages;
       if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u)) {
         if (lane == 0) set_err(err, KV4_DEVERR_TIMEOUT);
-        for (int i = j; i < issued; ++i)
-          mbar_wait_bounded(&bars[i % kWStages], (parity >> (i % kWStages)) & 1u, kWaitLimit * 16u);
+        for (int i = k; i < issued; ++i)
+          mbar_wait_bounded(&bars[(i - k0) % kWStages], (parity >> ((i - k0) % kWStages)) & 1u,
+                            kWaitLimit * 16u);
         dead = true;
         break;
       }
       parity ^= 1u << st;
-#pragma unroll 1
-      for (int pp = 0; pp < kWPair; ++pp) {
-        const int k = k0 + kWPair * j + pp;
-        if (k >= k1) break;
-        const uint8_t *sp = stage0 + (st * kWPair + pp) * kWTileBytes;
-        const uint32_t sa = smem_u32(sp) + ld;
-        int pos;  // of this lane's total; whether it is one of the tile's, and the tile was read
-        bool in;
-        const bool copied = __shfl_sync(0xffffffffu, pid, (k - block0) & 31) >= 0;
-        if (k < n4) {
-          pos = (p0 + k) * kPage + mine;
-          in = pos >= S && pos < L - R && copied;
-        } else if (k < n48) {
-          pos = (k - n4) * kPage + mine;
-          in = pos < min(S, L) && set_ok;
-        } else {
-          const int slot = (k - n48) * kPage + mine;
-          const int lastp = L - 1, base = lastp - lastp % R + slot;  // the last p < L with p mod R = slot
-          pos = base > lastp ? base - R : base;
-          in = slot < R && pos >= max(S, L - R) && ring_ok;
-        }
-        in = in && tig < 2;
-        const float old = in && acc_in != nullptr ? acc_in[acc0 + pos] : 0.f;
-        float2 s[2];  // logits of the slots gid, gid + 8 in log2 units, less lse
-        if (k < n4) {
-          float2 z[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const uint4 par[2] = {*reinterpret_cast<const uint4 *>(sp + kInt8CodeBytes + gid * 16),
-                                *reinterpret_cast<const uint4 *>(sp + kInt8CodeBytes + (gid + 8) * 16)};
+      const uint8_t *sp = stage0 + st * kWStageBytes;
+      const uint32_t sa = smem_u32(sp) + ld;
+      float2 s[2];  // logits of the slots gid, gid + 8 in log2 units, less lse
+      if (k < n4) {
+        float z[2][2] = {};
+        const uint4 par[2] = {*reinterpret_cast<const uint4 *>(sp + par_at + gid * 16),
+                              *reinterpret_cast<const uint4 *>(sp + par_at + (gid + 8) * 16)};
 #pragma unroll
-          for (int gp = 0; gp < 2; ++gp) {  // two groups per ldmatrix
+        for (int gp = 0; gp < 2; ++gp) {  // two groups per ldmatrix
+          float d[2][4];
+#pragma unroll
+          for (int hs = 0; hs < HPW; ++hs) {
+            if (hs > 0 && heads < HPW) break;
             uint32_t w[4];
-            ldsm_x4(w, sa + gp * 512);
+            ldsm_x4(w, sa + hs * kInt4CodeBytes + gp * 512);
 #pragma unroll
             for (int gg = 0; gg < 2; ++gg) {
               const int g = 2 * gp + gg;
-              uint32_t lo[4], hi[4];
+              uint32_t lo[4], hi[4], bq[4];
               nib_pairs_v_sub(w[2 * gg], lo);
               nib_pairs_v_sub(w[2 * gg + 1], hi);
-              float d[4];
-              mma_f16_zero(d, lo[0], hi[0], lo[2], hi[2], q4[g][0], q4[g][1]);
-              mma_f16(d, lo[1], hi[1], lo[3], hi[3], q4[g][2], q4[g][3]);
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t pw = g == 0 ? par[hf].x : g == 1 ? par[hf].y : g == 2 ? par[hf].z : par[hf].w;
-                const float2 sm = h2_to_f2(pw);  // (scale, min)
-                z[hf] = ffma2(make_float2(d[2 * hf], d[2 * hf + 1]), make_float2(sm.x, sm.x), z[hf]);
-                z[hf] = ffma2(qs[g], make_float2(sm.y, sm.y), z[hf]);
-              }
+              for (int i = 0; i < 4; ++i) bq[i] = HPW == 1 || head_b == hs ? q4[g][i] : 0u;
+              if (hs == 0) mma_f16_zero(d[gg], lo[0], hi[0], lo[2], hi[2], bq[0], bq[1]);
+              else mma_f16(d[gg], lo[0], hi[0], lo[2], hi[2], bq[0], bq[1]);
+              mma_f16(d[gg], lo[1], hi[1], lo[3], hi[3], bq[2], bq[3]);
             }
           }
-          s[0] = ffma2(z[0], kk, ls);
-          s[1] = ffma2(z[1], kk, ls);
-        } else {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg) {
+            const int g = 2 * gp + gg;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t pw = g == 0 ? par[hf].x : g == 1 ? par[hf].y : g == 2 ? par[hf].z : par[hf].w;
+              const float2 sm = h2_to_f2(pw);  // (scale, min)
+              z[hf][0] = fmaf(d[gg][2 * hf], sm.x, z[hf][0]);
+              z[hf][1] = fmaf(d[gg][2 * hf + 1], sm.x, z[hf][1]);
+              z[hf][0] = fmaf(qs[g].x, sm.y, z[hf][0]);
+              z[hf][1] = fmaf(qs[g].y, sm.y, z[hf][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          s[hf].x = fmaf(z[hf][0], kk.x, ls.x);
+          s[hf].y = fmaf(z[hf][1], kk.y, ls.y);
+        }
+      } else {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int hs = 0; hs < HPW; ++hs) {
+          if (hs > 0 && heads < HPW) break;
 #pragma unroll
           for (int pr = 0; pr < 4; ++pr) {
             uint32_t w[4];
-            ldsm_x4(w, sa + pr * 512);
+            ldsm_x4(w, sa + hs * kInt8CodeBytes + pr * 512);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const uint32_t ulo = w[2 * hf] ^ 0x80808080u, uhi = w[2 * hf + 1] ^ 0x80808080u;
-              mma_f16(d, s8_pair<0x4140>(ulo), s8_pair<0x4140>(uhi), s8_pair<0x4342>(ulo),
-                      s8_pair<0x4342>(uhi), q8[2 * pr + hf][0], q8[2 * pr + hf][1]);
+              const bool on = HPW == 1 || head_b == hs;
+              mma_f16(d, s8_pair<0x4140>(ulo), s8_pair<0x4140>(uhi), s8_pair<0x4342>(ulo), s8_pair<0x4342>(uhi),
+                      on ? q8[2 * pr + hf][0] : 0u, on ? q8[2 * pr + hf][1] : 0u);
             }
           }
-          const uint16_t *sc = reinterpret_cast<const uint16_t *>(sp + kInt8CodeBytes);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float ks = __half2float(__ushort_as_half(sc[gid + 8 * hf]));
-            s[hf] = ffma2(make_float2(d[2 * hf] * ks, d[2 * hf + 1] * ks), kq, ls);
-          }
         }
-        float w0 = fast_exp2(s[0].x) + fast_exp2(s[0].y), w1 = fast_exp2(s[1].x) + fast_exp2(s[1].y);
-        // sums over the four lanes of a slot: one exchange gives each lane one of its two slots
-        const float give = (tig & 1) ? w0 : w1, keep = (tig & 1) ? w1 : w0;
-        float w = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-        w += __shfl_xor_sync(0xffffffffu, w, 2);
-        if (in) acc_out[acc0 + pos] = old + w;
+        const uint16_t *sc =
+            reinterpret_cast<const uint16_t *>(sp + kWOffPar + min(head_c, heads - 1) * kInt8ScaleBytes);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float ks = __half2float(__ushort_as_half(sc[gid + 8 * hf]));
+          s[hf].x = fmaf(d[2 * hf] * ks, kq.x, ls.x);
+          s[hf].y = fmaf(d[2 * hf + 1] * ks, kq.y, ls.y);
+        }
       }
+      const float w0 = fast_exp2(s[0].x) + fast_exp2(s[0].y), w1 = fast_exp2(s[1].x) + fast_exp2(s[1].y);
+      // sums over a head's lanes of a slot: one exchange gives each lane one of its two slots
+      const float give = (tig & 1) ? w0 : w1, keep = (tig & 1) ? w1 : w0;
+      float w = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+      if (HPW == 1) w += __shfl_xor_sync(0xffffffffu, w, 2);
+      if (in) acc_out[acc0 + pos] = old + w;
       __syncwarp();
-      if (issued < pairs) issue(issued++);
+      if (issued < k1) issue(issued++);
     }
     if (dead) return;
     t += k1 - k0;
@@ -322,9 +349,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
 // ---------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------
-// Totals in their order as unsigned keys: NaN below everything, -0 as +0.
+// Totals in their order as unsigned keys from 1 on: NaN below everything, -0 as +0.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0u;
+  if (x != x) return 1u;
   const uint32_t u = __float_as_uint(x + 0.0f);  // -0 + 0 = +0
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
@@ -340,9 +367,9 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kHistCopies = 4;
 
 template <int K>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(CacheView c, int longest, const float *__restrict__ acc,
-                                                             int acc_stride, int budget, int32_t *keep,
-                                                             int32_t *new_lens, int32_t *err) {
+__global__ void __launch_bounds__(kSelThreads, K <= 16 ? 3 : 2) select_kernel(
+    CacheView c, int longest, const float *__restrict__ acc, int acc_stride, int budget, int32_t *keep,
+    int32_t *new_lens, int32_t *err) {
   __shared__ int hist[256 * kHistCopies];
   __shared__ uint32_t cnt[K * kSelWarps];  // taken keys, equal keys << 16, of a stripe's warp
   __shared__ uint32_t part[kSelWarps];
@@ -365,25 +392,25 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(CacheView c, int lo
   }
   const int lo = S, hi = L - R;  // candidates (hi - lo > budget - S - R)
   int need = budget - S - R;     // how many of them stay
-  uint32_t key[K];
+  uint32_t key[K];               // 0: no candidate
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int p = i * kSelThreads + tid;
-    key[i] = p >= lo && p < hi ? __float_as_uint(__ldg(row + p)) : 0x7fc00000u;
+    key[i] = 0u;
+    if (p >= lo && p < hi) key[i] = order_key(__ldg(row + p));
   }
-#pragma unroll
-  for (int i = 0; i < K; ++i) key[i] = order_key(__uint_as_float(key[i]));
   uint32_t border = 0u;  // its digits so far
   bool whole = false;    // every key from the border on is taken
   for (int shift = 24; shift >= 0 && need > 0 && !whole; shift -= 8) {
-    for (int i = tid; i < 256 * kHistCopies; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < 64 * kHistCopies; i += kSelThreads)
+      reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
+    // a key agrees with the border's digits where key - border is below the digits' step
+    const uint32_t span = shift == 24 ? 0xffffffffu : (1u << (shift + 8)) - 1u;
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const int p = i * kSelThreads + tid;
-      if (p >= lo && p < hi && (shift == 24 || ((key[i] ^ border) >> ((shift + 8) & 31)) == 0u))
+    for (int i = 0; i < K; ++i)
+      if (key[i] != 0u && key[i] - border <= span)
         atomicAdd(&hist[((key[i] >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
-    }
     __syncthreads();
     if (warp == 0) {  // lane l: digits 255 - 8l .. 248 - 8l, from the largest down
       int n[8], sum = 0;
@@ -417,29 +444,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(CacheView c, int lo
     need = s_need;
     whole = s_done != 0;
   }
-  // taken: sinks, recents, keys above the border (from it on where `whole`); equal: keys at it
-  auto taken = [&](int i, int p) {
-    if (p < lo || p >= hi) return p < L;
-    return need > 0 && (whole ? key[i] >= border : key[i] > border);
-  };
-  auto equal = [&](int i, int p) { return need > 0 && !whole && p >= lo && p < hi && key[i] == border; };
+  // taken: sinks, recents, keys above the border (from it on where `whole`); equal: keys at it.
+  // With no key to take, none is above the largest.
+  const uint32_t above = need == 0 ? 0xffffffffu : whole ? border - 1u : border;  // (a key is >= 1)
+  const bool ties = need > 0 && !whole;
+  uint32_t my_t = 0u, my_e = 0u;  // stripe `lane` of the warp: who is taken, who is equal
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int p = i * kSelThreads + tid;
-    const unsigned mt = __ballot_sync(0xffffffffu, taken(i, p)), me = __ballot_sync(0xffffffffu, equal(i, p));
-    if (lane == 0) cnt[i * kSelWarps + warp] = __popc(mt) | (__popc(me) << 16);
+    const bool kept = p < L && (p < lo || p >= hi);
+    const unsigned mt = __ballot_sync(0xffffffffu, kept || key[i] > above);
+    const unsigned me = __ballot_sync(0xffffffffu, ties && key[i] == border);
+    if (lane == i) my_t = mt, my_e = me;
   }
+  if (lane < K) cnt[lane * kSelWarps + warp] = __popc(my_t) | (__popc(my_e) << 16);
   __syncthreads();
-  // exclusive scan of the K * 16 counts, K / 32 rounded up of them per thread
-  constexpr int kPer = (K * kSelWarps + kSelThreads - 1) / kSelThreads;
-  uint32_t v[kPer], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int at = tid * kPer + i;
-    v[i] = at < K * kSelWarps ? cnt[at] : 0u;
-    sum += v[i];
-  }
-  uint32_t incl = sum;
+  // exclusive scan of the K * 16 counts, at most one per thread
+  const uint32_t mine = tid < K * kSelWarps ? cnt[tid] : 0u;
+  uint32_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
@@ -447,26 +469,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(CacheView c, int lo
   }
   if (lane == 31) part[warp] = incl;
   __syncthreads();
-  uint32_t base = incl - sum;
+  uint32_t base = incl - mine;
 #pragma unroll
   for (int w = 0; w < kSelWarps; ++w) base += w < warp ? part[w] : 0u;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int at = tid * kPer + i;
-    if (at < K * kSelWarps) cnt[at] = base;
-    base += v[i];
-  }
+  if (tid < K * kSelWarps) cnt[tid] = base;
   __syncthreads();
+  const uint32_t before = lane < K ? cnt[lane * kSelWarps + warp] : 0u;
   const unsigned below = (1u << lane) - 1u;
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < K; ++i) {
-    const int p = i * kSelThreads + tid;
-    const bool t = taken(i, p), e = equal(i, p);
-    const unsigned mt = __ballot_sync(0xffffffffu, t), me = __ballot_sync(0xffffffffu, e);
-    const uint32_t before = cnt[i * kSelWarps + warp];
-    const int ties = static_cast<int>(before >> 16) + __popc(me & below);  // equal keys before this one
-    const int at = static_cast<int>(before & 0xffffu) + __popc(mt & below) + min(ties, need);
-    if ((t || (e && ties < need)) && at < budget) out[at] = p;
+    const unsigned mt = __shfl_sync(0xffffffffu, my_t, i), me = __shfl_sync(0xffffffffu, my_e, i);
+    if ((mt | me) == 0u) continue;
+    const uint32_t bf = __shfl_sync(0xffffffffu, before, i);
+    const int eq = static_cast<int>(bf >> 16) + __popc(me & below);  // equal keys before this one
+    const int at = static_cast<int>(bf & 0xffffu) + __popc(mt & below) + min(eq, need);
+    const bool t = (mt >> lane) & 1u, e = (me >> lane) & 1u;
+    if ((t || (e && eq < need)) && at < budget) out[at] = i * kSelThreads + tid;
   }
 }
 
@@ -778,28 +796,35 @@ __global__ void __launch_bounds__(kInPlaceThreads) compact_in_place_kernel(Cache
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
-                           const float *acc_in, float *acc_out, int acc_stride, int32_t *err,
-                           cudaStream_t s) {
+template <int HPW>
+static cudaError_t launch_weights_t(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
+                                    const float *acc_in, float *acc_out, int acc_stride, int32_t *err,
+                                    cudaStream_t s) {
   static PerDevice grids;
   int most = 0;
   cudaError_t e = once_per_device(grids, [](int dev, int *g) {
-    cudaError_t r = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t r = cudaFuncSetAttribute(weights_kernel<HPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kWCtaSmem);
     int sms = 0, per_sm = 0;
     if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (r == cudaSuccess)
-      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, weights_kernel, kWarps * 32, kWCtaSmem);
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, weights_kernel<HPW>, kWarps * 32, kWCtaSmem);
     *g = sms * (per_sm > 0 ? per_sm : 1);
     return r;
   }, &most);
   if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>(c.num_seqs) * c.num_kv_heads *
+  const long long tiles = static_cast<long long>(c.num_seqs) * ((c.num_kv_heads + HPW - 1) / HPW) *
                           (max_seq_len / kPage + 2 + c.sink_tiles + c.ring_tiles);
   const long long want = (tiles / kWMinShare + kWarps) / kWarps;
   const int grid = static_cast<int>(want < most ? want : most);
-  weights_kernel<<<grid, kWarps * 32, kWCtaSmem, s>>>(c, q, lse, acc_in, acc_out, acc_stride, err);
+  weights_kernel<HPW><<<grid, kWarps * 32, kWCtaSmem, s>>>(c, q, lse, acc_in, acc_out, acc_stride, err);
   return cudaGetLastError();
+}
+
+cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
+                           const float *acc_in, float *acc_out, int acc_stride, int32_t *err, cudaStream_t s) {
+  return c.gqa <= 4 ? launch_weights_t<2>(c, max_seq_len, q, lse, acc_in, acc_out, acc_stride, err, s)
+                    : launch_weights_t<1>(c, max_seq_len, q, lse, acc_in, acc_out, acc_stride, err, s);
 }
 
 cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc, int acc_stride, int budget,
@@ -809,8 +834,8 @@ cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc,
   // the fewest keys per thread that hold the longest row
   if (longest <= 4 * kSelThreads)
     select_kernel<4><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
-  else if (longest <= 12 * kSelThreads)
-    select_kernel<12><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
+  else if (longest <= 16 * kSelThreads)
+    select_kernel<16><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
   else if (longest <= 32 * kSelThreads)
     select_kernel<32><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
   else
