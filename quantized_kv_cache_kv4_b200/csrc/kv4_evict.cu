@@ -356,21 +356,36 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 
+// The 32 x 32 bit matrix whose row l is lane l's word, transposed: lane i gets bit i of every lane.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t v, int lane) {
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    // the columns whose number has bit j clear
+    const uint32_t m = j == 16 ? 0x0000ffffu : j == 8 ? 0x00ff00ffu : j == 4 ? 0x0f0f0f0fu : j == 2 ? 0x33333333u
+                                                                                                  : 0x55555555u;
+    const uint32_t x = __shfl_xor_sync(0xffffffffu, v, j);
+    v = (lane & j) ? (v & ~m) | ((x >> j) & m) : (v & m) | ((x & m) << j);
+  }
+  return v;
+}
+
 // One CTA per (sequence, kv head); a thread holds K keys of the row in registers, striped over the
-// block (position i * 512 + thread), so the row is read once. The key at the border by digits of 8
-// bits from the top: a histogram of the candidates that agree with the digits so far (four copies
-// of it, by lane, against collisions of equal digits), until a digit's keys are all to be taken or
-// all four digits are known; then of the keys equal to the border the lowest positions. One scan
-// over the (stripe, warp) counts of taken and of equal keys gives every kept position its place.
+// block (position i * 512 + thread), so the row is read once. Sinks and recent positions have the
+// largest key of all, so that the `budget` largest keys are what stays. The key at the border by
+// digits of 11, 11 and 10 bits from the top: a histogram of the keys that agree with the digits so
+// far, its sums from the largest digit down, until a digit's keys are all to be taken or all three
+// digits are known; then of the keys equal to the border the lowest positions. One scan over the
+// (stripe, warp) counts of taken and of equal keys gives every kept position its place. Bound by
+// the integer pipe: about 30 of its instructions per key.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kHistCopies = 4;
+constexpr int kBins = 2048;  // four per thread
 
 template <int K>
-__global__ void __launch_bounds__(kSelThreads, K <= 16 ? 3 : 2) select_kernel(
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(
     CacheView c, int longest, const float *__restrict__ acc, int acc_stride, int budget, int32_t *keep,
     int32_t *new_lens, int32_t *err) {
-  __shared__ int hist[256 * kHistCopies];
+  __shared__ __align__(16) int hist[kBins];
   __shared__ uint32_t cnt[K * kSelWarps];  // taken keys, equal keys << 16, of a stripe's warp
   __shared__ uint32_t part[kSelWarps];
   __shared__ uint32_t s_border;
@@ -390,74 +405,77 @@ __global__ void __launch_bounds__(kSelThreads, K <= 16 ? 3 : 2) select_kernel(
     for (int j = tid; j < budget; j += kSelThreads) out[j] = j < L ? j : -1;
     return;
   }
-  const int lo = S, hi = L - R;  // candidates (hi - lo > budget - S - R)
-  int need = budget - S - R;     // how many of them stay
-  uint32_t key[K];               // 0: no candidate
+  int need = budget;
+  uint32_t key[K];  // 0: no position
+#pragma unroll
+  for (int i = 0; i < K; ++i)  // (the index kept in the row, so that no load waits for a branch)
+    key[i] = __float_as_uint(__ldg(row + min(i * kSelThreads + tid, L - 1)));
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int p = i * kSelThreads + tid;
-    key[i] = 0u;
-    if (p >= lo && p < hi) key[i] = order_key(__ldg(row + p));
+    key[i] = order_key(__uint_as_float(key[i]));
+    // (whole stripes of candidates need no look at their positions)
+    if (i * kSelThreads < S || (i + 1) * kSelThreads > L - R)
+      key[i] = p >= L ? 0u : p < S || p >= L - R ? 0xffffffffu : key[i];
   }
   uint32_t border = 0u;  // its digits so far
   bool whole = false;    // every key from the border on is taken
-  for (int shift = 24; shift >= 0 && need > 0 && !whole; shift -= 8) {
-    for (int i = tid; i < 64 * kHistCopies; i += kSelThreads)
-      reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
+#pragma unroll
+  for (int digit = 0; digit < 3; ++digit) {
+    if (whole) break;
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    // a key agrees with the border's digits where key - border is below the digits' step
-    const uint32_t span = shift == 24 ? 0xffffffffu : (1u << (shift + 8)) - 1u;
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-      if (key[i] != 0u && key[i] - border <= span)
-        atomicAdd(&hist[((key[i] >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
+    for (int i = 0; i < K; ++i) {
+      // a key agrees with the border's digits where key - border is below the digits' step
+      const uint32_t off = key[i] - border;
+      const bool agrees = digit == 0 ? key[i] != 0u : off < (digit == 1 ? 1u << 21 : 1u << 10);
+      if (agrees) atomicAdd(&hist[off >> shift], 1);
+    }
     __syncthreads();
-    if (warp == 0) {  // lane l: digits 255 - 8l .. 248 - 8l, from the largest down
-      int n[8], sum = 0;
+    const int first = kBins - 4 - 4 * tid;  // this thread's bins, the largest digits first
+    const int4 v = *reinterpret_cast<const int4 *>(&hist[first]);
+    const int n[4] = {v.w, v.z, v.y, v.x};
+    const int sum = n[0] + n[1] + n[2] + n[3];
+    int incl = sum;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int4 v = *reinterpret_cast<const int4 *>(&hist[(255 - 8 * lane - i) * kHistCopies]);
-        n[i] = v.x + v.y + v.z + v.w;
-        sum += n[i];
-      }
-      int incl = sum;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int above = incl - sum;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-      }
-      int above = incl - sum;
-      if (above < need && need <= incl) {
-        int at = -1, size = 0;
+    for (int w = 0; w < kSelWarps; ++w) above += w < warp ? static_cast<int>(part[w]) : 0;
+    if (above < need && need <= above + sum) {
+      int at = -1, size = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (at < 0 && above + n[i] >= need) at = i, size = n[i];
-          if (at < 0) above += n[i];
-        }
-        s_border = border | (static_cast<uint32_t>(255 - 8 * lane - at) << shift);
-        s_need = need - above;
-        s_done = size == need - above;
+      for (int i = 0; i < 4; ++i) {
+        if (at < 0 && above + n[i] >= need) at = i, size = n[i];
+        if (at < 0) above += n[i];
       }
+      s_border = border + (static_cast<uint32_t>(first + 3 - at) << shift);
+      s_need = need - above;
+      s_done = size == need - above;
     }
     __syncthreads();
     border = s_border;
     need = s_need;
     whole = s_done != 0;
   }
-  // taken: sinks, recents, keys above the border (from it on where `whole`); equal: keys at it.
-  // With no key to take, none is above the largest.
-  const uint32_t above = need == 0 ? 0xffffffffu : whole ? border - 1u : border;  // (a key is >= 1)
-  const bool ties = need > 0 && !whole;
-  uint32_t my_t = 0u, my_e = 0u;  // stripe `lane` of the warp: who is taken, who is equal
+  // taken: keys above the border (from it on where `whole`, and a key is at least 1); equal: at it
+  const uint32_t above = whole ? border - 1u : border;
+  uint32_t own_t = 0u, own_e = 0u;  // bit i: this thread's key of stripe i
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int p = i * kSelThreads + tid;
-    const bool kept = p < L && (p < lo || p >= hi);
-    const unsigned mt = __ballot_sync(0xffffffffu, kept || key[i] > above);
-    const unsigned me = __ballot_sync(0xffffffffu, ties && key[i] == border);
-    if (lane == i) my_t = mt, my_e = me;
-  }
-  if (lane < K) cnt[lane * kSelWarps + warp] = __popc(my_t) | (__popc(my_e) << 16);
+  for (int i = 0; i < K; ++i) own_t |= key[i] > above ? 1u << i : 0u;
+  if (!whole)
+#pragma unroll
+    for (int i = 0; i < K; ++i) own_e |= key[i] == border ? 1u << i : 0u;
+  // lane i: the warp's 32 keys of stripe i
+  const uint32_t all_t = transpose_bits(own_t, lane), all_e = whole ? 0u : transpose_bits(own_e, lane);
+  if (lane < K) cnt[lane * kSelWarps + warp] = __popc(all_t) | (__popc(all_e) << 16);
   __syncthreads();
   // exclusive scan of the K * 16 counts, at most one per thread
   const uint32_t mine = tid < K * kSelWarps ? cnt[tid] : 0u;
@@ -476,15 +494,24 @@ __global__ void __launch_bounds__(kSelThreads, K <= 16 ? 3 : 2) select_kernel(
   __syncthreads();
   const uint32_t before = lane < K ? cnt[lane * kSelWarps + warp] : 0u;
   const unsigned below = (1u << lane) - 1u;
+  // (a place is below `budget`: the taken keys and the first `need` equal ones are that many)
+  if (whole) {
+    const int first = static_cast<int>(before & 0xffffu);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const unsigned m = __shfl_sync(0xffffffffu, all_t, i);
+      const int at = __shfl_sync(0xffffffffu, first, i) + __popc(m & below);
+      if (own_t & (1u << i)) out[at] = i * kSelThreads + tid;
+    }
+  } else {
 #pragma unroll 4
-  for (int i = 0; i < K; ++i) {
-    const unsigned mt = __shfl_sync(0xffffffffu, my_t, i), me = __shfl_sync(0xffffffffu, my_e, i);
-    if ((mt | me) == 0u) continue;
-    const uint32_t bf = __shfl_sync(0xffffffffu, before, i);
-    const int eq = static_cast<int>(bf >> 16) + __popc(me & below);  // equal keys before this one
-    const int at = static_cast<int>(bf & 0xffffu) + __popc(mt & below) + min(eq, need);
-    const bool t = (mt >> lane) & 1u, e = (me >> lane) & 1u;
-    if ((t || (e && eq < need)) && at < budget) out[at] = i * kSelThreads + tid;
+    for (int i = 0; i < K; ++i) {
+      const unsigned mt = __shfl_sync(0xffffffffu, all_t, i), me = __shfl_sync(0xffffffffu, all_e, i);
+      const uint32_t bf = __shfl_sync(0xffffffffu, before, i);
+      const int eq = static_cast<int>(bf >> 16) + __popc(me & below);  // equal keys before this one
+      const int at = static_cast<int>(bf & 0xffffu) + __popc(mt & below) + min(eq, need);
+      if (((mt >> lane) & 1u) || (((me >> lane) & 1u) && eq < need)) out[at] = i * kSelThreads + tid;
+    }
   }
 }
 
