@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(256, 3) block8_append_rows_kernel(
 constexpr int kAttnCtas = 148 * 3;            // resident CTAs of the largest grid
 constexpr int kAttnWarps = kAttnCtas * kWarps;
 constexpr int kMinShare = 4;                  // pages per warp, at least
+constexpr int kUnitCtas = 296;                // CTAs up to which units get clusters of their own
 constexpr int kCols = 8;                      // query rows of a unit (MMA N)
 
 struct Seq8 : SeqRows {
@@ -291,10 +292,14 @@ constexpr float kLift8 = 14.0f;
 //   PV    fp16 MMAs on the converted codes, fp32 accumulators.
 // Bound by the reading of the pages; two pages (32 positions) per softmax step, so that the
 // cross-lane maximum, the waits and the copies' bookkeeping are paid once for 8 KB.
-template <int F, int NT>
+//
+// UNIT: few units, each given to the warps of a cluster (`parts` of them, equal runs of its pages),
+// which join their records themselves behind a cluster barrier: no scan of the batch and no merge
+// launch. `per_head`: units of a kv head of a sequence, at most.
+template <int F, int NT, bool UNIT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kernel(
-    CacheView c, Queries qs, Outputs out, float *__restrict__ partials, Crossing *__restrict__ notes,
-    int32_t *err) {
+    CacheView c, Queries qs, Outputs out, float *partials, Crossing *__restrict__ notes, int parts,
+    int per_head, int32_t *err) {
   constexpr int ROWS = kCols * NT;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitSmem split;
@@ -310,38 +315,54 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
   }
   auto items = [&](const Seq8 &s) { return static_cast<long long>(s.units) * s.pages * H; };
   const int me = blockIdx.x * kWarps + warp;
-  const Share share = take_share(B, me, gridDim.x * kWarps, kMinShare, split, [&](int i, bool check) {
-    return items(seq_of(c, qs, ROWS, i, check && blockIdx.x == 0 ? err : nullptr));
-  });
-  const long long t_begin = share.begin, t_end = share.end;
-  if (t_begin >= t_end) {
-    if (lane == 0) notes[me].rows = 0;
-    return;
+  Share share{0, 1, 0, 0};
+  const int unit0 = UNIT ? me / parts : 0, part = UNIT ? me - unit0 * parts : 0;
+  if constexpr (!UNIT) {
+    share = take_share(B, me, gridDim.x * kWarps, kMinShare, split, [&](int i, bool check) {
+      return items(seq_of(c, qs, ROWS, i, check && blockIdx.x == 0 ? err : nullptr));
+    });
+    if (share.begin >= share.end) {
+      if (lane == 0) notes[me].rows = 0;
+      return;
+    }
+  } else {
+    share.b = unit0 / (H * per_head);
   }
+  const long long t_begin = share.begin, t_end = share.end;
   int b = share.b;
   long long seq_first = share.seq_first;  // first item of sequence b
-  Seq8 sq = seq_of(c, qs, ROWS, b, nullptr);
+  Seq8 sq = seq_of(c, qs, ROWS, b, UNIT && part == 0 && unit0 % (H * per_head) == 0 ? err : nullptr);
+  if (UNIT && unit0 % per_head >= sq.units) return;  // (the whole cluster)
 
   uint32_t parity = 0;
   const int mi = lane >> 3, r8 = lane & 7;
   // ldmatrix lane addresses of two strips: (strip 2pr | slots 0-7), (| slots 8-15), strip 2pr+1
   const int ld8 = ((mi >> 1) * 256) + (mi & 1) * 128 + r8 * 16;
   for (long long t = t_begin; t < t_end;) {
-    while (t >= seq_first + items(sq)) {
-      seq_first += items(sq);
-      sq = seq_of(c, qs, ROWS, ++b, nullptr);
+    int h, u, pg0, pg1;  // unit u of kv head h; its pages pg0 .. pg1-1 are this warp's
+    if constexpr (UNIT) {
+      const int in_seq = unit0 % (H * per_head);
+      h = in_seq / per_head;
+      u = in_seq - h * per_head;
+      pg0 = static_cast<int>(static_cast<long long>(sq.pages) * part / parts);
+      pg1 = static_cast<int>(static_cast<long long>(sq.pages) * (part + 1) / parts);
+    } else {
+      while (t >= seq_first + items(sq)) {
+        seq_first += items(sq);
+        sq = seq_of(c, qs, ROWS, ++b, nullptr);
+      }
+      const long long in_seq = t - seq_first;
+      const int unit = static_cast<int>(in_seq / sq.pages);
+      pg0 = static_cast<int>(in_seq - static_cast<long long>(unit) * sq.pages);
+      pg1 = static_cast<int>(min(static_cast<long long>(sq.pages), pg0 + (t_end - t)));
+      h = unit / sq.units;
+      u = unit - h * sq.units;
     }
-    // unit (h, u) of the sequence: its pages pg0 .. pg1-1 are this warp's
-    const long long in_seq = t - seq_first;
-    const int unit = static_cast<int>(in_seq / sq.pages);
-    const int pg0 = static_cast<int>(in_seq - static_cast<long long>(unit) * sq.pages);
-    const int pg1 = static_cast<int>(min(static_cast<long long>(sq.pages), pg0 + (t_end - t)));
-    const int h = unit / sq.units, u = unit - h * sq.units;
-    const bool whole = pg0 == 0 && pg1 == sq.pages;
+    const bool whole = !UNIT && pg0 == 0 && pg1 == sq.pages;
     const int np = sq.L > 0 ? pg1 - pg0 : 0, pairs = (np + kPair - 1) / kPair;
     const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages + pg0;
 
-    if (t == t_begin && lane == 0)
+    if (!UNIT && t == t_begin && lane == 0)
       notes[me] = crossing(Shares(split.scan[kSplitThreads], gridDim.x * kWarps, kMinShare), me, t_begin - pg0,
                            sq.pages, pg0, sq.row0, h, u * ROWS, min(ROWS, sq.n * G - u * ROWS));
 
@@ -621,7 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
       __syncwarp();
       if (issued < pairs) issue(issued++);  // the stage is free again
     }
-    if (dead) return;
+    if (!UNIT && dead) return;
 
     const float undo = fast_exp2(vref);
 #pragma unroll
@@ -631,7 +652,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], off);
         const int col = 8 * g + 2 * tig + e, rc = u * ROWS + col;
-        if (rc >= rows) continue;
+        if (rc >= rows || dead) continue;
         if (whole) {
           const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
           const float inv = l[g][e] > 0.f ? undo / l[g][e] : 0.f;
@@ -645,7 +666,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
           }
           if (out.lse && gid == 0) out.lse[qr] = l[g][e] > 0.f ? m[g][e] * kLn2 + logf(l[g][e]) : -CUDART_INF_F;
         } else {
-          float *rec = partials + (static_cast<size_t>(2 * me + (t == t_begin ? 0 : 1)) * ROWS + col) *
+          float *rec = partials + (static_cast<size_t>(2 * me + (UNIT || t == t_begin ? 0 : 1)) * ROWS + col) *
                                       kRecordFloats;
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc)
@@ -654,6 +675,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
           if (gid == 0) st_rec(reinterpret_cast<float2 *>(rec + kHeadDim), make_float2(m[g][e], l[g][e]));
         }
       }
+    if constexpr (UNIT) {
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+      for (int col = part; col < min(ROWS, rows - u * ROWS); col += parts) {
+        const int r = u * ROWS + col;
+        const size_t qr = static_cast<size_t>(sq.row0 + r / G) * H * G + h * G + r % G;
+        join_records(partials, ROWS, col, me - part, me - part + parts - 1, [](int) { return 0; }, out, qr, lane);
+      }
+      return;
+    }
     t += pg1 - pg0;
   }
 }
@@ -713,45 +743,87 @@ static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, 
   return units * H * std::max(1, (max_seq_len + kPage - 1) / kPage);
 }
 
-// A note and two records of each warp, of the larger of the two unit sizes.
-static size_t warp_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G) {
+// A note and two records of each warp, of the larger of the two unit sizes; or, for few units, two
+// records of each warp of their clusters (at most kUnitCtas CTAs, so bounded by the units alone).
+static size_t warp_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_seq_len, int H, int G) {
   size_t bytes = 0;
   for (int rows = kCols; rows <= 2 * kCols; rows += kCols) {
     const size_t n = attn_warps(items_bound(num_seqs, total_q, max_seq_len, H, G, rows));
-    bytes = std::max(bytes, notes_bytes(n) + (2 * n * rows * kRecordFloats * sizeof(float) + 255) / 256 * 256);
+    const long long units = static_cast<long long>(num_seqs) * H *
+                            ((static_cast<long long>(max_q_len) * G + rows - 1) / rows);
+    const size_t u = static_cast<size_t>(std::min<long long>(kUnitCtas, 8 * units)) * kWarps;
+    const size_t record = 2u * rows * kRecordFloats * sizeof(float);
+    bytes = std::max(bytes, std::max(notes_bytes(n) + n * record, u * record));
   }
-  return bytes;
+  return (bytes + 255) / 256 * 256;
 }
 
 size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_seq_len, int H, int G) {
-  const size_t bytes = warp_workspace_bytes(num_seqs, total_q, max_seq_len, H, G);
+  const size_t bytes = warp_workspace_bytes(num_seqs, total_q, max_q_len, max_seq_len, H, G);
   if (static_cast<long long>(max_q_len) * G <= kWarpRows) return bytes;
   return std::max(bytes, tile_workspace_bytes(num_seqs, total_q, max_seq_len, H, G));
+}
+
+// Resident CTAs of a form of the attention kernel on the current device.
+template <int F, int NT, bool UNIT>
+static cudaError_t resident_ctas(int *most) {
+  static PerDevice grids;
+  return once_per_device(grids, [](int dev, int *g) {
+    cudaError_t r = cudaFuncSetAttribute(block8_attn_kernel<F, NT, UNIT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCta8Smem);
+    int sms = 0, per_sm = 0;
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (r == cudaSuccess)
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block8_attn_kernel<F, NT, UNIT>,
+                                                        kWarps * 32, kCta8Smem);
+    *g = sms * (per_sm > 0 ? per_sm : 1);
+    return r;
+  }, most);
+}
+
+// CTAs of a cluster that takes one unit (0: the batch is split by pages instead). A cluster's warps
+// get two pages at least of the longest sequence.
+static int unit_cluster(int num_seqs, int max_q_len, int max_seq_len, int H, int G, int rows) {
+  const long long units = static_cast<long long>(num_seqs) * H *
+                          ((static_cast<long long>(max_q_len) * G + rows - 1) / rows);
+  if (units > kUnitCtas) return 0;
+  const int pages = (max_seq_len + kPage - 1) / kPage;
+  int ctas = 1;
+  while (ctas < 8 && units * ctas * 2 <= kUnitCtas && pages >= 2 * kWarps * ctas * kPair) ctas *= 2;
+  return ctas;
 }
 
 template <int F, int NT>
 static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, int max_seq_len,
                                         const Outputs &out, void *workspace, int32_t *err,
                                         cudaStream_t s) {
-  static PerDevice grids;
   int most = 0;
-  cudaError_t e = once_per_device(grids, [](int dev, int *g) {
-    cudaError_t r = cudaFuncSetAttribute(block8_attn_kernel<F, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCta8Smem);
-    int sms = 0, per_sm = 0;
-    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (r == cudaSuccess)
-      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block8_attn_kernel<F, NT>, kWarps * 32,
-                                                        kCta8Smem);
-    *g = sms * (per_sm > 0 ? per_sm : 1);
-    return r;
-  }, &most);
+  constexpr int ROWS = kCols * NT;
+  if (const int ctas = unit_cluster(c.num_seqs, qs.max_n, max_seq_len, c.num_kv_heads, c.gqa, ROWS)) {
+    cudaError_t e = resident_ctas<F, NT, true>(&most);  // (sets the kernel's attributes)
+    if (e != cudaSuccess) return e;
+    const int per_head = (qs.max_n * c.gqa + ROWS - 1) / ROWS;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(c.num_seqs) * c.num_kv_heads * per_head * ctas);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = kCta8Smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, block8_attn_kernel<F, NT, true>, c, qs, out, static_cast<float *>(workspace),
+                              static_cast<Crossing *>(nullptr), ctas * kWarps, per_head, err);
+  }
+  cudaError_t e = resident_ctas<F, NT, false>(&most);
   if (e != cudaSuccess) return e;
-  const long long bound = items_bound(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa, kCols * NT);
+  const long long bound = items_bound(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa, ROWS);
   const int grid = std::min(attn_warps(bound) / kWarps, most);
   Crossing *notes = static_cast<Crossing *>(workspace);
   float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + notes_bytes(grid * kWarps));
-  block8_attn_kernel<F, NT><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, notes, err);
+  block8_attn_kernel<F, NT, false><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, notes, 0, 0, err);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(block8_merge_kernel<NT>, dim3(grid * kWarps - 1), 256, s, out,

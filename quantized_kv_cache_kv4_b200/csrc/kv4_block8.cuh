@@ -71,10 +71,10 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &a, uint32_t &b)
     b = V ? s8_pair<0x4341>(u) : s8_pair<0x4342>(u);
   } else {
     const uint32_t u = V ? prmt(w, 0u, 0x3120) : w;
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u & 0xFFFFu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16), __NV_E4M3);
-    a = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
-    b = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(u));
   }
 }
 
@@ -130,7 +130,7 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned thread
 // slot(w): which of worker w's two. 32 records at a time: their maxima and sums by the lanes
 // first, so that the loads of the values wait for nothing but their own batch.
 template <class Slot>
-__device__ __forceinline__ void join_records(const float *__restrict__ partials, int rows, int x, int w0,
+__device__ __forceinline__ void join_records(const float *partials, int rows, int x, int w0,
                                              int w1, Slot slot, const Outputs &out, size_t qr, int lane) {
   float mm = kNegBig, ll = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -140,7 +140,7 @@ __device__ __forceinline__ void join_records(const float *__restrict__ partials,
     float2 ml = make_float2(kNegBig, 0.f);
     if (lane < n) {
       at = ((2 * static_cast<size_t>(w + lane) + slot(w + lane)) * rows + x) * kRecordFloats;
-      ml = *reinterpret_cast<const float2 *>(partials + at + kHeadDim);
+      ml = __ldcg(reinterpret_cast<const float2 *>(partials + at + kHeadDim));
       if (ml.y <= 0.f) ml.x = kNegBig;  // nothing visible there
     }
     float mx = ml.x;
@@ -160,7 +160,7 @@ __device__ __forceinline__ void join_records(const float *__restrict__ partials,
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const size_t r = __shfl_sync(0xffffffffu, at, min(i + k, n - 1));
-        v[k] = *reinterpret_cast<const float4 *>(partials + r + 4 * lane);
+        v[k] = __ldcg(reinterpret_cast<const float4 *>(partials + r + 4 * lane));
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
