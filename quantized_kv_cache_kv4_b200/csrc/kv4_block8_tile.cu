@@ -62,25 +62,35 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// 1 in one lane of the warp, the same one each time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// Issued by the lane whose `one` is set; the whole warp calls it.
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
       : "memory");
 }
 // The barrier gets one arrival when every MMA this thread has issued so far is done.
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t one, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)), "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -324,65 +334,67 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   } else if (warp >= 12) {
     Setmax<kMmaRegs>::dec();
     // ------------------------------- MMA -------------------------------
+    // The warp goes through this together and one lane issues: descriptors and barrier addresses are
+    // then the warp's (uniform registers), not to be moved there for each instruction.
     int seg = 0, pp = 0;  // live segments and phases of p_full so far
+    const uint32_t one = elect_one();
+    const uint64_t qd = smem_desc(smem_u32(q_tile));
+    const uint64_t kd0 = smem_desc(smem_u32(k_tiles)), vd0 = smem_desc(smem_u32(v_tiles));
+    auto all = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    // S (or the last O) is there; the thread's own arrival hands on what it has seen of the convert
+    // warps' writes (the tile's scales)
+    auto done = [&]() {
+      mma_commit(one, &bars.s_full[pipe]);
+      if (one) mbar_arrive(&bars.s_full[pipe]);
+    };
+    auto qk = [&](int k) {
+      const int st = stage_of(k);
+      ok = all(&bars.k_full[st], phase_of(k));
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t kd = kd0 + static_cast<uint64_t>((st * kOperandBytes) >> 4);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {  // 16 dims: 32 bytes of a row; the halves 16 KB apart
+        const uint64_t off = static_cast<uint64_t>(((x >> 2) * 16384 + (x & 3) * 32) >> 4);
+        mma_ss(one, tm_s, qd + off, kd + off, kIdescQK, x > 0);
+      }
+      mma_commit(one, &bars.k_empty[st]);
+      done();
+    };
     Seg sg;
     while (ok && read_seg(seg_no++, sg)) {
-      const int n = sg.k1 - sg.k0;
-      const bool live = sg.u * kUnitRows + pipe * kTile < sg.n * G;
-      if (lane == 0) {
-        if (!live) {  // no rows here: only let go of the shared tiles
-          for (int j = 0; ok && j < n; ++j) {
-            const int st = stage_of(kt + j), ph = phase_of(kt + j);
-            ok = wait(&bars.k_full[st], ph);
-            mbar_arrive(&bars.k_empty[st]);
-            ok = ok && wait(&bars.v_full[st], ph);
-            mbar_arrive(&bars.v_empty[st]);
-          }
-        } else {
-          const uint64_t qd = smem_desc(smem_u32(q_tile));
-          // S (or the last O) is there; the thread's own arrival hands on what it has seen of
-          // the convert warps' writes (the tile's scales)
-          auto done = [&]() {
-            mma_commit(&bars.s_full[pipe]);
-            mbar_arrive(&bars.s_full[pipe]);
-          };
-          auto qk = [&](int k) {
-            const int st = stage_of(k);
-            ok = ok && wait(&bars.k_full[st], phase_of(k));
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t kd = smem_desc(smem_u32(k_tiles + st * kOperandBytes));
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {  // 16 dims: 32 bytes of a row; the halves 16 KB apart
-              const uint64_t off = static_cast<uint64_t>(((x >> 2) * 16384 + (x & 3) * 32) >> 4);
-              mma_ss(tm_s, qd + off, kd + off, kIdescQK, x > 0);
-            }
-            mma_commit(&bars.k_empty[st]);
-            done();
-          };
-          ok = wait(&bars.q_full[pipe], seg & 1);
+      const int n = __reduce_max_sync(0xffffffffu, sg.k1 - sg.k0);  // (uniform, and known to be)
+      const bool live = __all_sync(0xffffffffu, sg.u * kUnitRows + pipe * kTile < sg.n * G);
+      if (!live) {  // no rows here: only let go of the shared tiles
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = stage_of(kt + j), ph = phase_of(kt + j);
+          ok = all(&bars.k_full[st], ph);
+          if (one) mbar_arrive(&bars.k_empty[st]);
+          ok = ok && all(&bars.v_full[st], ph);
+          if (one) mbar_arrive(&bars.v_empty[st]);
+        }
+      } else {
+        ok = all(&bars.q_full[pipe], seg & 1);
+        ++seg;
+        tc_fence_after();
+        if (ok) qk(kt);
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = stage_of(kt + j);
+          ok = all(&bars.p_full[pipe], pp & 1);
+          ++pp;
+          ok = ok && all(&bars.v_full[st], phase_of(kt + j));
+          if (!ok) break;
           tc_fence_after();
-          qk(kt);
-          for (int j = 0; ok && j < n; ++j) {
-            const int st = stage_of(kt + j);
-            ok = wait(&bars.p_full[pipe], pp & 1);
-            ++pp;
-            ok = ok && wait(&bars.v_full[st], phase_of(kt + j));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = smem_desc(smem_u32(v_tiles + st * kOperandBytes));
+          const uint64_t vd = vd0 + static_cast<uint64_t>((st * kOperandBytes) >> 4);
 #pragma unroll
-            for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
-              mma_ts(tm_o, tm_s + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4), kIdescPV, j > 0 || x > 0);
-            mma_commit(&bars.v_empty[st]);
-            if (j + 1 < n) qk(kt + j + 1);
-            else done();
-          }
-          ++seg;
+          for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
+            mma_ts(one, tm_o, tm_s + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4), kIdescPV, j > 0 || x > 0);
+          mma_commit(one, &bars.v_empty[st]);
+          if (j + 1 < n) qk(kt + j + 1);
+          else done();
         }
       }
       kt += n;
-      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
     }
   } else if (warp >= 8) {
     // ------------------------------- convert -------------------------------
