@@ -311,9 +311,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     return s.b >= 0;
   };
 
+  // (one instruction for each group of four warps, before its warps part)
+  if (warp < 8) Setmax<kSoftmaxRegs>::inc();
+  else if (warp < 12) Setmax<kConvertRegs>::dec();
+  else Setmax<kMmaRegs>::dec();
+
   if (warp >= 14) {
     // ------------------------------- schedule -------------------------------
-    Setmax<kMmaRegs>::dec();
     if (lane == 0 && warp == 14) {
       Segments sg(c, qs, share);
       notes[me].rows = 0;
@@ -332,7 +336,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       }
     }
   } else if (warp >= 12) {
-    Setmax<kMmaRegs>::dec();
     // ------------------------------- MMA -------------------------------
     // The warp goes through this together and one lane issues: descriptors and barrier addresses are
     // then the warp's (uniform registers), not to be moved there for each instruction.
@@ -401,7 +404,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     // One tile ahead in registers (its codes), two ahead its blocks' scales, three ahead its page
     // ids: nothing waits for what it has just asked for. 128 threads, a 16-byte piece of each page
     // each.
-    Setmax<kConvertRegs>::dec();
     const int tid = threadIdx.x - 256;
     const int strip = tid >> 4, slot = tid & 15;
     struct Meta {
@@ -526,7 +528,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     }
   } else {
     // ------------------------------- softmax -------------------------------
-    Setmax<kSoftmaxRegs>::inc();
     const int row = threadIdx.x & 127;  // of the pipeline; its TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4), bits 16+
     const uint32_t ts = tm_s + lane_off, to = tm_o + lane_off;
