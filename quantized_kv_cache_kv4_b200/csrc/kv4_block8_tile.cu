@@ -10,8 +10,12 @@
 //                          and sum, the weights back to TMEM over the logits;
 //   MMA warps (1 + 1)      one thread issues S = Q K^T (both operands in shared memory) and
 //                          O += P V (P in TMEM); accumulators S and O in TMEM, 4 x 128 columns;
-//   convert warps (4)      load pages' codes and write them as fp16 (exact for both formats)
-//                          into the 128-byte-swizzled tiles the MMAs read.
+//   loading warp           page ids, scales, and the pages' codes into shared memory by bulk copies;
+//   convert warps (4)      write the codes as fp16 (exact for both formats) into the 128-byte-
+//                          swizzled tiles the MMAs read;
+//   scheduling warp        the CTA's runs of key tiles.
+// The loops are kept short in code (rolled where they can be): with everything unrolled the warps
+// spent most of their time on instruction fetch, each kind of them evicting the others' code.
 // The pipelines hold rows 0-127 and 128-255 of one unit and read the same key tiles, which are
 // converted once (two stages).
 //
@@ -34,11 +38,12 @@ constexpr int kTile = 128;               // rows of a pipeline, positions of a k
 constexpr int kUnitRows = 2 * kTile;     // query rows of a unit: both pipelines'
 constexpr int kTilePages = kTile / kPage;
 constexpr int kOperandBytes = kTile * kHeadDim * 2;  // one fp16 operand tile: 32 KB
-constexpr int kTileThreads = 512;        // 8 softmax, 4 convert and 2 MMA warps (and 2 idle)
-// registers per thread of the three kinds: 256 x 176 + 128 x 112 + 128 x 48 = 512 x 128, what
+constexpr int kTileThreads = 512;        // 8 softmax, 4 convert, 2 MMA warps, a scheduling and a loading one
+// registers per thread of the three kinds: 256 x 192 + 128 x 64 + 128 x 64 = 512 x 128, what
 // the block is launched with
-constexpr int kSoftmaxRegs = 176, kConvertRegs = 112, kMmaRegs = 48;
-constexpr int kTileSmem = 6 * kOperandBytes + 1024;  // Q x 2, K x 2, V x 2 (+ alignment)
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 64, kMmaRegs = 64;
+constexpr int kRawBytes = kTilePages * kInt8CodeBytes;  // a key tile's K or V codes: 16 KB
+constexpr int kTileSmem = 6 * kOperandBytes + 2 * kRawBytes + 1024;  // Q, K, V x 2, codes (+ alignment)
 constexpr int kTileCtas = 148;
 constexpr int kTileMinShare = 1;
 constexpr float kLazy = 8.0f;            // log2 of how far a row may outgrow its maximum
@@ -204,6 +209,8 @@ struct alignas(16) TileScales {
   float cv[kTilePages];  // vs 2^(kPShift - vref)
   float vref;            // exponent with every value scale of the segment so far at most 2^vref
   float moved;           // vref before this tile, less vref (0: it has not moved)
+  int left;              // positions of the tile within the length (negative: no more tiles)
+  int pages;             // bit p: page p of the tile was copied
   int any_bad;
 };
 
@@ -218,6 +225,7 @@ struct TileBars {
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   uint64_t q_full[2], s_full[2], p_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t raw_full[2], raw_empty[2];  // the codes of K, of V
 };
 
 // The logits of positions that a row does not see, -inf: all but the tile's first `left`, and
@@ -251,24 +259,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = c.num_kv_heads, G = c.gqa;
-  // pipeline of this warp: softmax warps 0-3 and 4-7, MMA warps 12 and 13, scheduling warps 14
-  // and 15; convert warps 8-11 serve both
+  // pipeline of this warp: softmax warps 0-3 and 4-7, MMA warps 12 and 13; convert warps 8-11, the
+  // scheduling warp 14 and the loading warp 15 serve both
   const int pipe = warp < 8 ? warp >> 2 : warp < 12 ? 0 : (warp - 12) & 1;
 
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < kSegRing; ++k) {
       mbar_init(&bars.seg_full[k], 1);
-      mbar_init(&bars.seg_empty[k], 14);  // warps that read it
+      mbar_init(&bars.seg_empty[k], 11);  // warps that read it
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.q_full[i], kTile);
+      mbar_init(&bars.q_full[i], 4);
       mbar_init(&bars.s_full[i], 2);  // the MMAs' completion, and the issuing thread itself
-      mbar_init(&bars.p_full[i], kTile);
+      mbar_init(&bars.p_full[i], 4);
       mbar_init(&bars.k_full[i], 4);
       mbar_init(&bars.v_full[i], 4);
       mbar_init(&bars.k_empty[i], 2);
       mbar_init(&bars.v_empty[i], 2);
+      mbar_init(&bars.raw_full[i], 1);
+      mbar_init(&bars.raw_empty[i], 4);
     }
     fence_barrier_init();
   }
@@ -290,6 +300,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   const uint32_t tm_s = tmem + 256 * pipe, tm_o = tm_s + 128;
   uint8_t *q_tile = smem + pipe * kOperandBytes;
   uint8_t *k_tiles = smem + 2 * kOperandBytes, *v_tiles = smem + 4 * kOperandBytes;
+  uint8_t *raw = smem + 6 * kOperandBytes;  // K's codes, then V's
   auto stage_of = [](int k) { return k & 1; };  // of the worker's k-th tile
   auto phase_of = [](int k) { return (k >> 1) & 1; };
   auto slot_of = [&](int k) -> TileScales & { return scales[k & 3]; };
@@ -311,193 +322,74 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
     return s.b >= 0;
   };
 
-  // (one instruction for each group of four warps, before its warps part)
-  if (warp < 8) Setmax<kSoftmaxRegs>::inc();
-  else if (warp < 12) Setmax<kConvertRegs>::dec();
-  else Setmax<kMmaRegs>::dec();
-
-  if (warp >= 14) {
-    // ------------------------------- schedule -------------------------------
-    if (lane == 0 && warp == 14) {
-      Segments sg(c, qs, share);
-      notes[me].rows = 0;
-      for (int no = 0;; ++no) {
-        const bool more = sg.next();
-        if (no == 0 && more)
-          notes[me] = crossing(Shares(split.scan[kSplitThreads], workers, kTileMinShare), me, share.begin - sg.k0,
-                               sg.nt, sg.k0, sg.sq.row0, sg.h, sg.u * kUnitRows,
-                               min(kUnitRows, sg.sq.n * G - sg.u * kUnitRows));
-        const int at = no & (kSegRing - 1);
-        if (!wait(&bars.seg_empty[at], ((no / kSegRing) & 1) ^ 1)) break;
-        segs[at] = more ? Seg{sg.b, sg.h, sg.u, sg.k0, sg.k1, sg.nt, sg.first, sg.sq.L, sg.sq.n, sg.sq.row0}
-                              : Seg{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-        mbar_arrive(&bars.seg_full[at]);
-        if (!more) break;
-      }
-    }
-  } else if (warp >= 12) {
-    // ------------------------------- MMA -------------------------------
-    // The warp goes through this together and one lane issues: descriptors and barrier addresses are
-    // then the warp's (uniform registers), not to be moved there for each instruction.
-    int seg = 0, pp = 0;  // live segments and phases of p_full so far
-    const uint32_t one = elect_one();
-    const uint64_t qd = smem_desc(smem_u32(q_tile));
-    const uint64_t kd0 = smem_desc(smem_u32(k_tiles)), vd0 = smem_desc(smem_u32(v_tiles));
-    auto all = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    // S (or the last O) is there; the thread's own arrival hands on what it has seen of the convert
-    // warps' writes (the tile's scales)
-    auto done = [&]() {
-      mma_commit(one, &bars.s_full[pipe]);
-      if (one) mbar_arrive(&bars.s_full[pipe]);
-    };
-    auto qk = [&](int k) {
-      const int st = stage_of(k);
-      ok = all(&bars.k_full[st], phase_of(k));
-      if (!ok) return;
-      tc_fence_after();
-      const uint64_t kd = kd0 + static_cast<uint64_t>((st * kOperandBytes) >> 4);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {  // 16 dims: 32 bytes of a row; the halves 16 KB apart
-        const uint64_t off = static_cast<uint64_t>(((x >> 2) * 16384 + (x & 3) * 32) >> 4);
-        mma_ss(one, tm_s, qd + off, kd + off, kIdescQK, x > 0);
-      }
-      mma_commit(one, &bars.k_empty[st]);
-      done();
-    };
-    Seg sg;
-    while (ok && read_seg(seg_no++, sg)) {
-      const int n = __reduce_max_sync(0xffffffffu, sg.k1 - sg.k0);  // (uniform, and known to be)
-      const bool live = __all_sync(0xffffffffu, sg.u * kUnitRows + pipe * kTile < sg.n * G);
-      if (!live) {  // no rows here: only let go of the shared tiles
-        for (int j = 0; ok && j < n; ++j) {
-          const int st = stage_of(kt + j), ph = phase_of(kt + j);
-          ok = all(&bars.k_full[st], ph);
-          if (one) mbar_arrive(&bars.k_empty[st]);
-          ok = ok && all(&bars.v_full[st], ph);
-          if (one) mbar_arrive(&bars.v_empty[st]);
+  // (a warpgroup's warps execute one setmaxnreg together, before they part)
+  if (warp >= 12) {
+    Setmax<kMmaRegs>::dec();
+    if (warp == 15) {
+      // ------------------------------- load -------------------------------
+      // Page ids a tile ahead of their scales, and those a tile ahead of the copies.
+      struct Meta {
+        int kt;         // the worker's tile number, -1: no tile
+        int k, L;       // the key tile, the length
+        int h, pid;     // kv head; page (lane % 8) of the tile (-2: behind the length)
+        uint16_t ks, vs;  // and its scales
+        bool first;     // the segment's first tile
+      };
+      Seg sg;
+      int at = 0, end = 0, n_tiles = 0;
+      bool more = true;
+      float vref = 0.f;
+      auto ask_page = [&]() {  // the next tile and its page ids
+        Meta m{-1, 0, 0, 0, -2, 0, 0, false};
+        if (at == end) {
+          more = more && read_seg(seg_no++, sg);
+          if (!more) return m;
+          at = sg.k0;
+          end = sg.k1;
         }
-      } else {
-        ok = all(&bars.q_full[pipe], seg & 1);
-        ++seg;
-        tc_fence_after();
-        if (ok) qk(kt);
-        for (int j = 0; ok && j < n; ++j) {
-          const int st = stage_of(kt + j);
-          ok = all(&bars.p_full[pipe], pp & 1);
-          ++pp;
-          ok = ok && all(&bars.v_full[st], phase_of(kt + j));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t vd = vd0 + static_cast<uint64_t>((st * kOperandBytes) >> 4);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
-            mma_ts(one, tm_o, tm_s + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4), kIdescPV, j > 0 || x > 0);
-          mma_commit(one, &bars.v_empty[st]);
-          if (j + 1 < n) qk(kt + j + 1);
-          else done();
+        m.kt = n_tiles++;
+        m.first = at == sg.k0;
+        m.k = at++;
+        m.L = sg.L;
+        m.h = sg.h;
+        const int page = m.k * kTilePages + (lane & 7);
+        if (page < (m.L + kPage - 1) / kPage)
+          m.pid = __ldg(c.page_table + static_cast<size_t>(sg.b) * c.max_pages + page);
+        return m;
+      };
+      auto ask_scales = [&](Meta &m) {  // of its pages, and whether the ids are any
+        if (m.kt < 0 || m.k * kTilePages + (lane & 7) >= (m.L + kPage - 1) / kPage) return;
+        if (m.pid < 0 || m.pid >= c.num_pages) {
+          set_err(err, KV4_DEVERR_PAGE_ID);
+          m.pid = -1;
+        } else {
+          m.ks = __ldg(c.k_params + static_cast<size_t>(m.pid) * H + m.h);
+          m.vs = __ldg(c.v_params + static_cast<size_t>(m.pid) * H + m.h);
         }
-      }
-      kt += n;
-    }
-  } else if (warp >= 8) {
-    // ------------------------------- convert -------------------------------
-    // One tile ahead in registers (its codes), two ahead its blocks' scales, three ahead its page
-    // ids: nothing waits for what it has just asked for. 128 threads, a 16-byte piece of each page
-    // each.
-    const int tid = threadIdx.x - 256;
-    const int strip = tid >> 4, slot = tid & 15;
-    struct Meta {
-      int kt;         // the worker's tile number, -1: no tile
-      int k, L;       // the key tile, the length
-      int h, pid;     // kv head; page (lane % 8) of the tile (-2: behind the length)
-      uint16_t ks, vs;  // and its scales
-      bool first;     // the segment's first tile
-    };
-    Seg sg;
-    int at = 0, end = 0, n_tiles = 0;
-    bool more = true;
-    auto ask_page = [&]() {  // the next tile and its page ids
-      Meta m{-1, 0, 0, 0, -2, 0, 0, false};
-      if (at == end) {
-        more = more && read_seg(seg_no++, sg);
-        if (!more) return m;
-        at = sg.k0;
-        end = sg.k1;
-      }
-      m.kt = n_tiles++;
-      m.first = at == sg.k0;
-      m.k = at++;
-      m.L = sg.L;
-      m.h = sg.h;
-      const int page = m.k * kTilePages + (lane & 7);
-      if (page < (m.L + kPage - 1) / kPage)
-        m.pid = __ldg(c.page_table + static_cast<size_t>(sg.b) * c.max_pages + page);
-      return m;
-    };
-    auto ask_scales = [&](Meta &m) {  // of its pages, and whether the ids are any
-      if (m.pid == -2 && (m.kt < 0 || m.k * kTilePages + (lane & 7) >= (m.L + kPage - 1) / kPage)) return;
-      if (m.pid < 0 || m.pid >= c.num_pages) {
-        set_err(err, KV4_DEVERR_PAGE_ID);
-        m.pid = -1;
-      } else {
-        m.ks = __ldg(c.k_params + static_cast<size_t>(m.pid) * H + m.h);
-        m.vs = __ldg(c.v_params + static_cast<size_t>(m.pid) * H + m.h);
-      }
-    };
-    // A thread's piece of each page; of page 0 where there is none (put() then writes zeros)
-    auto load = [&](const uint8_t *codes, const Meta &m, uint4 (&v)[kTilePages]) {
-      if (c.num_pages == 0) return;  // (nor is there a page 0 then)
-#pragma unroll
-      for (int p = 0; p < kTilePages; ++p) {
-        const int page = max(0, __shfl_sync(0xffffffffu, m.pid, p));
-        v[p] = __ldg(reinterpret_cast<const uint4 *>(
-            codes + (static_cast<size_t>(page) * H + m.h) * kInt8CodeBytes + tid * 16));
-      }
-    };
-    auto put = [&](uint8_t *tile, const Meta &m, uint4 (&v)[kTilePages]) {
-      // what lies behind the length, or on a page that is none, may hold anything
-      if (__any_sync(0xffffffffu, m.pid < 0) || (m.k + 1) * kTile > m.L) {
-#pragma unroll
-        for (int p = 0; p < kTilePages; ++p)
-          if (__shfl_sync(0xffffffffu, m.pid, p) < 0 || (m.k * kTilePages + p) * kPage + slot >= m.L)
-            v[p] = make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int p = 0; p < kTilePages; ++p) {
-        const int row = p * kPage + slot;
-        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) code_pairs<F, false>(w[q], o[2 * q], o[2 * q + 1]);
-        uint8_t *at = tile + (strip >> 2) * 16384 + row * 128;
-        const int chunk = (strip & 3) * 2;  // 16-byte chunks, xor-swizzled by the row
-        *reinterpret_cast<uint4 *>(at + ((chunk ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(at + (((chunk + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
-    float vref = 0.f;
-    uint4 kv[kTilePages] = {}, vv[kTilePages] = {};
-    Meta cur = ask_page(), nxt = ask_page();
-    ask_scales(cur);
-    ask_scales(nxt);
-    Meta nx2 = ask_page();
-    if (cur.kt >= 0) {
-      load(c.k_codes, cur, kv);
-      load(c.v_codes, cur, vv);
-    }
-    while (cur.kt >= 0) {
-      const int st = stage_of(cur.kt), free_phase = phase_of(cur.kt) ^ 1;
-      ok = __all_sync(0xffffffffu, wait(&bars.k_empty[st], free_phase));
-      if (!ok) break;
-      if (tid < 32) {  // the first convert warp writes the scales
-        TileScales &sl = slot_of(cur.kt);
+      };
+      Meta cur = ask_page();
+      ask_scales(cur);
+      Meta nxt = ask_page();
+      for (int k = 0; ok; ++k) {
+        ok = __all_sync(0xffffffffu, wait(&bars.raw_empty[0], (k & 1) ^ 1));
+        if (!ok) {  // let the copies in flight land before the block ends
+          if (k > 0) wait(&bars.raw_full[0], (k & 1) ^ 1), wait(&bars.raw_full[1], (k & 1) ^ 1);
+          break;
+        }
+        TileScales &sl = slot_of(k);
+        if (cur.kt < 0) {  // no more tiles
+          if (lane == 0) {
+            sl.left = -1;
+            mbar_arrive(&bars.raw_full[0]);
+          }
+          break;
+        }
         const float ks = cur.pid == -1 ? -1.f : __half2float(__ushort_as_half(cur.ks));
         const float vs = __half2float(__ushort_as_half(cur.vs));
         float top = vs;
 #pragma unroll
         for (int off = 1; off < kTilePages; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const unsigned there = __ballot_sync(0xffffffffu, cur.pid >= 0) & 0xffu;
         const unsigned bad = __ballot_sync(0xffffffffu, cur.pid == -1);
         int e = -24;
         if (top > 0.f) frexpf(top, &e);  // top < 2^e
@@ -510,24 +402,169 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         if (lane == 0) {
           sl.vref = vref;
           sl.moved = before - vref;
+          sl.left = min(kTile, max(0, cur.L - cur.k * kTile));
+          sl.pages = static_cast<int>(there);
           sl.any_bad = bad != 0u;
         }
+        __syncwarp();
+        const size_t off = (static_cast<size_t>(max(cur.pid, 0)) * H + cur.h) * kInt8CodeBytes;
+        const uint32_t bytes = __popc(there) * kInt8CodeBytes;
+        fence_proxy_async_smem();
+        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[0], bytes);
+        __syncwarp();
+        if (lane < kTilePages && cur.pid >= 0)
+          bulk_g2s(raw + lane * kInt8CodeBytes, c.k_codes + off, kInt8CodeBytes, &bars.raw_full[0]);
+        ok = __all_sync(0xffffffffu, wait(&bars.raw_empty[1], (k & 1) ^ 1));
+        if (!ok) {  // let the copies in flight land before the block ends
+          wait(&bars.raw_full[0], k & 1);
+          if (k > 0) wait(&bars.raw_full[1], (k & 1) ^ 1);
+        } else {
+          fence_proxy_async_smem();
+          if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[1], bytes);
+          __syncwarp();
+          if (lane < kTilePages && cur.pid >= 0)
+            bulk_g2s(raw + kRawBytes + lane * kInt8CodeBytes, c.v_codes + off, kInt8CodeBytes, &bars.raw_full[1]);
+        }
+        cur = nxt;
+        ask_scales(cur);
+        nxt = ask_page();
       }
-      put(k_tiles + st * kOperandBytes, cur, kv);
-      if (lane == 0) mbar_arrive(&bars.k_full[st]);
-      if (nxt.kt >= 0) load(c.k_codes, nxt, kv);
-      ok = __all_sync(0xffffffffu, wait(&bars.v_empty[st], free_phase));
+    } else if (warp == 14) {
+      // ------------------------------- schedule -------------------------------
+      if (lane == 0) {
+        Segments sg(c, qs, share);
+        notes[me].rows = 0;
+        for (int no = 0;; ++no) {
+          const bool more = sg.next();
+          if (no == 0 && more)
+            notes[me] = crossing(Shares(split.scan[kSplitThreads], workers, kTileMinShare), me, share.begin - sg.k0,
+                                 sg.nt, sg.k0, sg.sq.row0, sg.h, sg.u * kUnitRows,
+                                 min(kUnitRows, sg.sq.n * G - sg.u * kUnitRows));
+          const int at = no & (kSegRing - 1);
+          if (!wait(&bars.seg_empty[at], ((no / kSegRing) & 1) ^ 1)) break;
+          segs[at] = more ? Seg{sg.b, sg.h, sg.u, sg.k0, sg.k1, sg.nt, sg.first, sg.sq.L, sg.sq.n, sg.sq.row0}
+                                : Seg{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          mbar_arrive(&bars.seg_full[at]);
+          if (!more) break;
+        }
+      }
+    } else {
+      // ------------------------------- MMA -------------------------------
+      // The warp goes through this together and one lane issues: descriptors and barrier addresses are
+      // then the warp's (uniform registers), not to be moved there for each instruction.
+      int seg = 0, pp = 0;  // live segments and phases of p_full so far
+      const uint32_t one = elect_one();
+      const uint64_t qd = smem_desc(smem_u32(q_tile));
+      const uint64_t kd0 = smem_desc(smem_u32(k_tiles)), vd0 = smem_desc(smem_u32(v_tiles));
+      auto all = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+      // S (or the last O) is there; the thread's own arrival hands on what it has seen of the convert
+      // warps' writes (the tile's scales)
+      auto done = [&]() {
+        mma_commit(one, &bars.s_full[pipe]);
+        if (one) mbar_arrive(&bars.s_full[pipe]);
+      };
+      auto qk = [&](int k) {  // (K is there)
+        const uint64_t kd = kd0 + static_cast<uint64_t>((stage_of(k) * kOperandBytes) >> 4);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {  // 16 dims: 32 bytes of a row; the halves 16 KB apart
+          const uint64_t off = static_cast<uint64_t>(((x >> 2) * 16384 + (x & 3) * 32) >> 4);
+          mma_ss(one, tm_s, qd + off, kd + off, kIdescQK, x > 0);
+        }
+      };
+      Seg sg;
+      while (ok && read_seg(seg_no++, sg)) {
+        const int n = __reduce_max_sync(0xffffffffu, sg.k1 - sg.k0);  // (uniform, and known to be)
+        const bool live = __all_sync(0xffffffffu, sg.u * kUnitRows + pipe * kTile < sg.n * G);
+        if (!live) {  // no rows here: only let go of the shared tiles
+          for (int j = 0; ok && j < n; ++j) {
+            const int st = stage_of(kt + j), ph = phase_of(kt + j);
+            ok = all(&bars.k_full[st], ph);
+            if (one) mbar_arrive(&bars.k_empty[st]);
+            ok = ok && all(&bars.v_full[st], ph);
+            if (one) mbar_arrive(&bars.v_empty[st]);
+          }
+        } else {
+          ok = all(&bars.q_full[pipe], seg & 1);
+          ++seg;
+          tc_fence_after();
+          ok = ok && all(&bars.k_full[stage_of(kt)], phase_of(kt));
+          if (!ok) break;
+          tc_fence_after();
+          qk(kt);
+          done();
+          mma_commit(one, &bars.k_empty[stage_of(kt)]);
+          for (int j = 0; ok && j < n; ++j) {
+            const int st = stage_of(kt + j), next = stage_of(kt + j + 1);
+            const bool more = j + 1 < n;
+            // all that the products need but the weights is waited for ahead of them
+            ok = all(&bars.v_full[st], phase_of(kt + j));
+            if (more) ok = ok && all(&bars.k_full[next], phase_of(kt + j + 1));
+            ok = ok && all(&bars.p_full[pipe], pp & 1);
+            ++pp;
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + static_cast<uint64_t>((st * kOperandBytes) >> 4);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
+              mma_ts(one, tm_o, tm_s + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4), kIdescPV, j > 0 || x > 0);
+            if (more) qk(kt + j + 1);
+            done();
+            mma_commit(one, &bars.v_empty[st]);
+            if (more) mma_commit(one, &bars.k_empty[next]);
+          }
+        }
+        kt += n;
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------- convert -------------------------------
+    Setmax<kConvertRegs>::dec();
+    // 128 threads, a 16-byte piece (16 dims of a position) of each page each.
+    const int tid = threadIdx.x - 256;
+    const int strip = tid >> 4, slot = tid & 15;
+    const uint32_t chunk = (strip & 3) * 2;  // of 16 bytes, xor-swizzled by the row (its low bits: the slot's)
+    const uint32_t to0 = (strip >> 2) * 16384 + slot * 128 + ((chunk ^ (slot & 7)) << 4);
+    const uint32_t to1 = (strip >> 2) * 16384 + slot * 128 + (((chunk + 1) ^ (slot & 7)) << 4);
+    // one tile's K (which = 0) or V
+    auto convert = [&](int which, const uint8_t *from, uint8_t *to, uint64_t *empty, uint64_t *full, int left,
+                       int pages, int free_phase) {
+      ok = __all_sync(0xffffffffu, wait(empty, free_phase));
+      if (!ok) return;
+#pragma unroll 2
+      for (int p = 0; p < kTilePages; ++p) {
+        uint4 v = *reinterpret_cast<const uint4 *>(from + p * kInt8CodeBytes + tid * 16);
+        // what lies behind the length, or of a page that was not copied, may hold anything
+        if (p * kPage + slot >= left || !((pages >> p) & 1)) v = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t o[8];
+        code_pairs<F, false>(v.x, o[0], o[1]);
+        code_pairs<F, false>(v.y, o[2], o[3]);
+        code_pairs<F, false>(v.z, o[4], o[5]);
+        code_pairs<F, false>(v.w, o[6], o[7]);
+        *reinterpret_cast<uint4 *>(to + p * 2048 + to0) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(to + p * 2048 + to1) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(full);
+        mbar_arrive(&bars.raw_empty[which]);
+      }
+    };
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(0xffffffffu, wait(&bars.raw_full[0], k & 1));
       if (!ok) break;
-      put(v_tiles + st * kOperandBytes, cur, vv);
-      if (lane == 0) mbar_arrive(&bars.v_full[st]);
-      if (nxt.kt >= 0) load(c.v_codes, nxt, vv);
-      cur = nxt;
-      nxt = nx2;
-      ask_scales(nxt);
-      nx2 = ask_page();
+      const int left = slot_of(k).left, pages = slot_of(k).pages;
+      if (left < 0) break;
+      const int st = stage_of(k), free_phase = phase_of(k) ^ 1;
+      convert(0, raw, k_tiles + st * kOperandBytes, &bars.k_empty[st], &bars.k_full[st], left, pages, free_phase);
+      ok = ok && __all_sync(0xffffffffu, wait(&bars.raw_full[1], k & 1));
+      if (ok)
+        convert(1, raw + kRawBytes, v_tiles + st * kOperandBytes, &bars.v_empty[st], &bars.v_full[st], left, pages,
+                free_phase);
     }
   } else {
     // ------------------------------- softmax -------------------------------
+    Setmax<kSoftmaxRegs>::inc();
     const int row = threadIdx.x & 127;  // of the pipeline; its TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4), bits 16+
     const uint32_t ts = tm_s + lane_off, to = tm_o + lane_off;
@@ -579,7 +616,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(&bars.q_full[pipe]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_full[pipe]);
 
       float m = kNegBig, l = 0.f, vref = 0.f;
       for (int j = 0; ok && j < n_tiles; ++j, ++kt) {
@@ -657,7 +695,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         l += l2.x + l2.y;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars.p_full[pipe]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[pipe]);
       }
       ok = ok && wait(&bars.s_full[pipe], sp & 1);  // O is complete
       ++sp;
