@@ -8,14 +8,12 @@
 // A CTA runs two pipelines of 128 rows each:
 //   softmax warps (4 + 4)  one thread per row: the row's logits from TMEM, the running maximum
 //                          and sum, the weights back to TMEM over the logits;
-//   MMA warps (1 + 1)      one thread issues S = Q K^T (both operands in shared memory) and
+//   MMA warp               one thread issues S = Q K^T (both operands in shared memory) and
 //                          O += P V (P in TMEM); accumulators S and O in TMEM, 4 x 128 columns;
 //   loading warp           page ids, scales, and the pages' codes into shared memory by bulk copies;
 //   convert warps (4)      write the codes as fp16 (exact for both formats) into the 128-byte-
 //                          swizzled tiles the MMAs read;
 //   scheduling warp        the CTA's runs of key tiles.
-// The loops are kept short in code (rolled where they can be): with everything unrolled the warps
-// spent most of their time on instruction fetch, each kind of them evicting the others' code.
 // The pipelines hold rows 0-127 and 128-255 of one unit and read the same key tiles, which are
 // converted once (two stages).
 //
@@ -28,6 +26,15 @@
 // Split. The key tiles of all units, in order, are dealt to the workers in equal contiguous
 // shares; units that two or more workers share leave partial records (first and last unit of
 // a worker) for the merge.
+//
+// What bounds it. 2 chunks of 3900-4096 positions over 7000-8192 (742 GFLOP, INT8): 890 us, 830
+// TFLOP/s. Of the ~5000 cycles of a key tile the products take 2050 (both pipelines'), a
+// pipeline's softmax 2900 (of which the exponentials 1100-2100, as the other's fall together with
+// them), and a pipeline's softmax waits for its own products. One MMA warp that takes the
+// pipelines in turn keeps them out of phase (two warps, one per pipeline: 999 us). The roles'
+// instructions contend: the loops are short in code where they can be (the convert loop unrolled
+// by 8 instead of 1 costs a fifth of the kernel, exponentials by polynomial on the FMA pipe 6 to
+// 20 %, half rows per thread with 16 softmax warps 2 %).
 #include <algorithm>
 
 #include "kv4_block8.cuh"
@@ -38,14 +45,14 @@ constexpr int kTile = 128;               // rows of a pipeline, positions of a k
 constexpr int kUnitRows = 2 * kTile;     // query rows of a unit: both pipelines'
 constexpr int kTilePages = kTile / kPage;
 constexpr int kOperandBytes = kTile * kHeadDim * 2;  // one fp16 operand tile: 32 KB
-constexpr int kTileThreads = 512;        // 8 softmax, 4 convert, 2 MMA warps, a scheduling and a loading one
+constexpr int kTileThreads = 512;        // 8 softmax and 4 convert warps, one each for MMA, scheduling, loading
 // registers per thread of the three kinds: 256 x 192 + 128 x 64 + 128 x 64 = 512 x 128, what
 // the block is launched with
 constexpr int kSoftmaxRegs = 192, kConvertRegs = 64, kMmaRegs = 64;
 constexpr int kRawBytes = kTilePages * kInt8CodeBytes;  // a key tile's K or V codes: 16 KB
 constexpr int kTileSmem = 6 * kOperandBytes + 2 * kRawBytes + 1024;  // Q, K, V x 2, codes (+ alignment)
-constexpr int kTileCtas = 148;
-constexpr int kTileMinShare = 1;
+constexpr int kTileCtas = 148;           // one per SM (shared memory)
+constexpr int kTileMinShare = 1;         // key tiles of a worker: ~2.5 us of work, a record's join is less
 constexpr float kLazy = 8.0f;            // log2 of how far a row may outgrow its maximum
 constexpr float kPShift = 7.0f;          // P is at most 2^(kLazy + kPShift)
 constexpr uint32_t kTileWait = 1u << 18;  // attempts of one bounded wait
@@ -226,6 +233,7 @@ struct TileBars {
   uint64_t q_full[2], s_full[2], p_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[2], raw_empty[2];  // the codes of K, of V
+  uint64_t idle;                       // the last of the products is done
 };
 
 // The logits of positions that a row does not see, -inf: all but the tile's first `left`, and
@@ -259,15 +267,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = c.num_kv_heads, G = c.gqa;
-  // pipeline of this warp: softmax warps 0-3 and 4-7, MMA warps 12 and 13; convert warps 8-11, the
-  // scheduling warp 14 and the loading warp 15 serve both
-  const int pipe = warp < 8 ? warp >> 2 : warp < 12 ? 0 : (warp - 12) & 1;
-
+  // pipeline of a softmax warp: warps 0-3 and 4-7; convert warps 8-11, the MMA warp 12, the scheduling
+  // warp 14 and the loading warp 15 serve both
+  const int pipe = (warp >> 2) & 1;
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < kSegRing; ++k) {
       mbar_init(&bars.seg_full[k], 1);
-      mbar_init(&bars.seg_empty[k], 11);  // warps that read it
+      mbar_init(&bars.seg_empty[k], 10);  // warps that read it
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 4);
@@ -275,11 +282,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       mbar_init(&bars.p_full[i], 4);
       mbar_init(&bars.k_full[i], 4);
       mbar_init(&bars.v_full[i], 4);
-      mbar_init(&bars.k_empty[i], 2);
-      mbar_init(&bars.v_empty[i], 2);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_empty[i], 1);
       mbar_init(&bars.raw_full[i], 1);
       mbar_init(&bars.raw_empty[i], 4);
     }
+    mbar_init(&bars.idle, 1);
     fence_barrier_init();
   }
   if (warp == 12) {  // all 512 columns: S and O of both pipelines
@@ -448,73 +456,87 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
           if (!more) break;
         }
       }
-    } else {
+    } else if (warp == 12) {
       // ------------------------------- MMA -------------------------------
-      // The warp goes through this together and one lane issues: descriptors and barrier addresses are
-      // then the warp's (uniform registers), not to be moved there for each instruction.
-      int seg = 0, pp = 0;  // live segments and phases of p_full so far
+      // One warp for both pipelines, in turn: a step's products of one are issued together (mixed with
+      // the other's, both would end at the time of the later one), so that they run under the other's
+      // softmax. The warp goes through this together and one lane issues: descriptors and barrier
+      // addresses are then the warp's (uniform registers), not to be moved there for each instruction.
+      int seg = 0, pp0 = 0, pp1 = 0, q1 = 0;  // segments; phases of the p_full and of the second q_full
       const uint32_t one = elect_one();
-      const uint64_t qd = smem_desc(smem_u32(q_tile));
+      const uint64_t qd0 = smem_desc(smem_u32(smem));
       const uint64_t kd0 = smem_desc(smem_u32(k_tiles)), vd0 = smem_desc(smem_u32(v_tiles));
       auto all = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       // S (or the last O) is there; the thread's own arrival hands on what it has seen of the convert
       // warps' writes (the tile's scales)
-      auto done = [&]() {
-        mma_commit(one, &bars.s_full[pipe]);
-        if (one) mbar_arrive(&bars.s_full[pipe]);
+      auto done = [&](int p) {
+        mma_commit(one, &bars.s_full[p]);
+        if (one) mbar_arrive(&bars.s_full[p]);
       };
-      auto qk = [&](int k) {  // (K is there)
+      auto qk = [&](int p, int k) {  // (K is there)
+        const uint64_t qd = qd0 + static_cast<uint64_t>((p * kOperandBytes) >> 4);
         const uint64_t kd = kd0 + static_cast<uint64_t>((stage_of(k) * kOperandBytes) >> 4);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {  // 16 dims: 32 bytes of a row; the halves 16 KB apart
           const uint64_t off = static_cast<uint64_t>(((x >> 2) * 16384 + (x & 3) * 32) >> 4);
-          mma_ss(one, tm_s, qd + off, kd + off, kIdescQK, x > 0);
+          mma_ss(one, tmem + 256 * p, qd + off, kd + off, kIdescQK, x > 0);
         }
+      };
+      auto pv = [&](int p, int k, bool acc) {
+        const uint64_t vd = vd0 + static_cast<uint64_t>((stage_of(k) * kOperandBytes) >> 4);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
+          mma_ts(one, tmem + 256 * p + 128, tmem + 256 * p + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4),
+                 kIdescPV, acc || x > 0);
       };
       Seg sg;
       while (ok && read_seg(seg_no++, sg)) {
         const int n = __reduce_max_sync(0xffffffffu, sg.k1 - sg.k0);  // (uniform, and known to be)
-        const bool live = __all_sync(0xffffffffu, sg.u * kUnitRows + pipe * kTile < sg.n * G);
-        if (!live) {  // no rows here: only let go of the shared tiles
-          for (int j = 0; ok && j < n; ++j) {
-            const int st = stage_of(kt + j), ph = phase_of(kt + j);
-            ok = all(&bars.k_full[st], ph);
-            if (one) mbar_arrive(&bars.k_empty[st]);
-            ok = ok && all(&bars.v_full[st], ph);
-            if (one) mbar_arrive(&bars.v_empty[st]);
-          }
-        } else {
-          ok = all(&bars.q_full[pipe], seg & 1);
-          ++seg;
-          tc_fence_after();
-          ok = ok && all(&bars.k_full[stage_of(kt)], phase_of(kt));
+        const bool two = __all_sync(0xffffffffu, sg.u * kUnitRows + kTile < sg.n * G);  // second pipeline has rows
+        ok = all(&bars.k_full[stage_of(kt)], phase_of(kt)) && all(&bars.q_full[0], seg & 1);
+        ++seg;
+        if (!ok) break;
+        tc_fence_after();
+        qk(0, kt);
+        done(0);
+        if (two) {
+          ok = all(&bars.q_full[1], q1 & 1);
+          ++q1;
           if (!ok) break;
           tc_fence_after();
-          qk(kt);
-          done();
-          mma_commit(one, &bars.k_empty[stage_of(kt)]);
-          for (int j = 0; ok && j < n; ++j) {
-            const int st = stage_of(kt + j), next = stage_of(kt + j + 1);
-            const bool more = j + 1 < n;
-            // all that the products need but the weights is waited for ahead of them
-            ok = all(&bars.v_full[st], phase_of(kt + j));
-            if (more) ok = ok && all(&bars.k_full[next], phase_of(kt + j + 1));
-            ok = ok && all(&bars.p_full[pipe], pp & 1);
-            ++pp;
+          qk(1, kt);
+          done(1);
+        }
+        mma_commit(one, &bars.k_empty[stage_of(kt)]);
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = stage_of(kt + j), next = stage_of(kt + j + 1);
+          const bool more = j + 1 < n;
+          // all that the products need but the weights is waited for ahead of them
+          ok = all(&bars.v_full[st], phase_of(kt + j));
+          if (more) ok = ok && all(&bars.k_full[next], phase_of(kt + j + 1));
+          ok = ok && all(&bars.p_full[0], pp0 & 1);
+          ++pp0;
+          if (!ok) break;
+          tc_fence_after();
+          pv(0, kt + j, j > 0);
+          if (more) qk(0, kt + j + 1);
+          done(0);
+          if (two) {
+            ok = all(&bars.p_full[1], pp1 & 1);
+            ++pp1;
             if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = vd0 + static_cast<uint64_t>((st * kOperandBytes) >> 4);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)  // 16 positions: 16 rows of 128 bytes, 8 columns of P
-              mma_ts(one, tm_o, tm_s + 8 * x, vd + static_cast<uint64_t>((x * 2048) >> 4), kIdescPV, j > 0 || x > 0);
-            if (more) qk(kt + j + 1);
-            done();
-            mma_commit(one, &bars.v_empty[st]);
-            if (more) mma_commit(one, &bars.k_empty[next]);
+            pv(1, kt + j, j > 0);
+            if (more) qk(1, kt + j + 1);
+            done(1);
           }
+          mma_commit(one, &bars.v_empty[st]);
+          if (more) mma_commit(one, &bars.k_empty[next]);
         }
         kt += n;
       }
+      mma_commit(one, &bars.idle);  // (and all arrivals of the tensor cores have been made: the block may end)
+      all(&bars.idle, 0);
     }
   } else if (warp >= 8) {
     // ------------------------------- convert -------------------------------
@@ -530,7 +552,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
                        int pages, int free_phase) {
       ok = __all_sync(0xffffffffu, wait(empty, free_phase));
       if (!ok) return;
-#pragma unroll 2
+#pragma unroll 1
       for (int p = 0; p < kTilePages; ++p) {
         uint4 v = *reinterpret_cast<const uint4 *>(from + p * kInt8CodeBytes + tid * 16);
         // what lies behind the length, or of a page that was not copied, may hold anything
@@ -585,15 +607,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       const int lim = live ? sg.L - sg.n + i : -1;  // last position the row sees
       float a;  // logit units: step of the fixed query times log2(e) / sqrt(128)
       {
+        // Two of the warp's rows at a time, 16 lanes each: whole lines are read.
         uint4 v[16];
         float amax = 0.f;
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          v[x] = live ? reinterpret_cast<const uint4 *>(qs.q + qr * kHeadDim)[x] : make_uint4(0u, 0u, 0u, 0u);
+          const int from = 2 * x + (lane >> 4);
+          const size_t at = (static_cast<size_t>(sg.row0 + __shfl_sync(0xffffffffu, i, from)) * H + sg.h) * G +
+                            __shfl_sync(0xffffffffu, r - i * G, from);
+          v[x] = r - lane + from < rows ? reinterpret_cast<const uint4 *>(qs.q + at * kHeadDim)[lane & 15]
+                                        : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
           const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          float top = 0.f;
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xFFFF0000u))));
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xFFFF0000u))));
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          top = __shfl_sync(0xffffffffu, top, (lane & 1) << 4);
+          if (lane >> 1 == x) amax = top;
         }
         int ex = 0;
         if (amax > 0.f) {
@@ -601,16 +636,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
           ex -= 15;
         }
         const float step = fmaxf(ldexpf(1.0f, ex), 0x1p-120f);  // largest element in [2^14, 2^15)
-        const float inv = 1.0f / step;
+        const float mine = 1.0f / step;
         a = step * kScaleLog2;
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
+          const int from = 2 * x + (lane >> 4), to_row = 32 * (warp & 3) + from, ch = lane & 15;
+          const float inv = __shfl_sync(0xffffffffu, mine, from);
           const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
           uint32_t o[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             o[y] = pack_h2(__uint_as_float(w[y] << 16) * inv, __uint_as_float(w[y] & 0xFFFF0000u) * inv);
-          *reinterpret_cast<uint4 *>(q_tile + (x >> 3) * 16384 + row * 128 + (((x & 7) ^ (row & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(q_tile + (ch >> 3) * 16384 + to_row * 128 + (((ch & 7) ^ (to_row & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
@@ -709,7 +746,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       const float scale = whole ? (l > 0.f ? undo / l : 0.f) : undo;
       float *rec = partials + (static_cast<size_t>(2 * me + (sg.first ? 0 : 1)) * kUnitRows +
                                pipe * kTile + row) * kRecordFloats;
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
         tmem_ld32(to + 32 * q, o);
@@ -717,8 +754,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         float v[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = l > 0.f ? __uint_as_float(o[x]) * scale : 0.f;
-        if (!live) continue;
-        if (whole) {
+        if (live && whole) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t w[4];
@@ -731,7 +767,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
           }
         }
         float *f32 = whole ? (out.out_f32 ? out.out_f32 + qr * kHeadDim : nullptr) : rec;
-        if (f32 != nullptr)
+        if (live && f32 != nullptr)
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             reinterpret_cast<float4 *>(f32 + 32 * q)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
