@@ -418,9 +418,11 @@ size_t kv4_block8_workspace_size(const kv4_config *cfg, int32_t num_seqs, int32_
  *             initialisation. Calls that may overlap on the GPU need one each.
  * A query before position 0 (n > seq_lens[b]), or of an empty sequence, sees nothing: O = 0,
  * lse = -inf. Positions on a page id outside the pool are left out (KV4_DEVERR_PAGE_ID).
- * Logits are sums of exact products in fp32; the weights enter PV as fp16 with 11 significant
- * bits down to 2^-28 of a row's largest. Results do not depend on the order in which warps
- * run. */
+ * A sequence of a length below 0 or above its page table's (KV4_DEVERR_SEQ_LEN) counts as empty.
+ * Logits are sums of exact products in fp32. The weights, times the value scales, enter PV as
+ * fp16: 11 significant bits of weight x scale down to 2^-28 of the largest weight times the
+ * largest scale where max_q_len * Hq / Hkv is at most 64, down to 2^-21 beyond; below that an
+ * absolute error of 2^-39 or 2^-32 of it. Results do not depend on the order in which warps run. */
 kv4_status kv4_block8_attention(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
                                 const kv4_batch *batch, const void *q, const int32_t *q_indptr,
                                 int32_t total_q, int32_t max_q_len, void *out, float *out_f32,
@@ -479,7 +481,8 @@ kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const
  *   dst_ring_idx: int32 [num_seqs], another ring for each sequence, which is no ring this call
  *              reads; NULL = its own.
  *   acc_in, acc_out: fp32 [num_seqs][Hkv][acc_in_stride / acc_out_stride]; both NULL = no
- *              totals. One array for both needs equal strides and dst_page_table NULL. */
+ *              totals. One array for both needs equal strides and dst_page_table NULL; it then
+ *              holds old totals behind new_lens[b], to be zeroed before the sequence grows. */
 kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
                              const kv4_int8_side *side, const kv4_batch *batch,
                              const int32_t *keep, int32_t budget, const int32_t *new_lens,

@@ -2,10 +2,11 @@
 // fp16 scale per (page, kv head), for K and for V. Value = code * scale.
 //
 //   block8_append_token_kernel  one new row per sequence: one warp per (sequence, kv head).
-//   block8_append_rows_kernel   CSR rows: one warp per (page touched, kv head).
-//   block8_attn_kernel<F>       attention with up to 8 query rows (a kv head's query heads
-//                               of one or more positions) per warp, split over the pages.
+//   block8_append_rows_kernel   CSR rows: one warp per (page touched, kv head, K or V).
+//   block8_attn_kernel          attention with 8 or 16 query rows (a kv head's query heads of
+//                               one or more positions) per warp, split over the pages.
 //   block8_merge_kernel         the exact merge of the units that several warps share.
+//   (kv4_block8_tile.cu: attention of more than kWarpRows query rows of a kv head)
 //
 // Block scale. A block's scale is the largest row magnitude it has seen over the largest
 // code (127, or 448 for e4m3), rounded UP to fp16, so that no code saturates (rounding to
@@ -109,7 +110,8 @@ __device__ __forceinline__ float amax4(const float (&x)[4]) {
 }
 
 // One warp per (sequence, kv head, K or V); lane l holds dims 4l .. 4l+3. Bound by its chain of
-// loads (length, page id, scale), so the row is asked for first.
+// loads (length, page id, scale), so the row is asked for first: 1024 sequences x 8 kv heads take
+// 10 us of which the bytes are 1.
 template <int F>
 __global__ void __launch_bounds__(256) block8_append_token_kernel(
     CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
@@ -160,9 +162,10 @@ __device__ __forceinline__ uint4 transpose4(uint32_t a, uint32_t b, uint32_t c, 
 // CSR rows. A CTA looks over kRowsPerCta rows; the first row of the call in each page leads that
 // page's rows (they may reach past the CTA's). One warp per (led page, kv head, K or V): its rows
 // (up to 16 x 256 bytes) in registers, the block's largest magnitude, the codes, and full 64-byte
-// runs of each strip out. Bound by HBM (768 bytes of rows in for 384 of codes out); the search for
-// a row's sequence is shared by the CTA's ~4 pages and all heads (16 rows per CTA: 80 us, 64: see
-// the table of measurements for the call it was taken on).
+// runs of each strip out. Bound by HBM (512 bytes of rows in, 256 of codes out per position and
+// head) and the latency of a page's loads; the search for a row's sequence is shared by the CTA's
+// ~4 pages and all heads. Prefill of 64 sequences of up to 1024 (47k rows x 8 kv heads): 64 rows
+// per CTA, three CTAs per SM, 67 us (4.3 TB/s); 16 rows per CTA 80 us.
 constexpr int kRowsPerCta = 64;
 template <int F>
 __global__ void __launch_bounds__(256, 3) block8_append_rows_kernel(
@@ -245,8 +248,11 @@ __global__ void __launch_bounds__(256, 3) block8_append_rows_kernel(
 // order. A warp has at most two such units: its first (record 2w) and its last (2w + 1).
 constexpr int kAttnCtas = 148 * 3;            // resident CTAs of the largest grid
 constexpr int kAttnWarps = kAttnCtas * kWarps;
-constexpr int kMinShare = 4;                  // pages per warp, at least
-constexpr int kUnitCtas = 296;                // CTAs up to which units get clusters of their own
+constexpr int kMinShare = 4;                  // pages per warp, at least (~1 us: a record's join)
+// Units of at most this many CTAs (two per SM) get clusters of their own, which saves the scan and
+// the merge launch: decode steps of 3 x 500 positions 15 -> 12 us, 4 x 8000 42 -> 21, 32 x 4096 64 ->
+// 55; with more units than this the equal shares balance better.
+constexpr int kUnitCtas = 296;
 constexpr int kCols = 8;                      // query rows of a unit (MMA N)
 
 struct Seq8 : SeqRows {
@@ -290,8 +296,11 @@ constexpr float kLift8 = 14.0f;
 //         of its largest products. e4m3: fp16 MMAs, codes converted, the query a power of two
 //         from its bf16 value; both exact but for the fp32 sums.
 //   PV    fp16 MMAs on the converted codes, fp32 accumulators.
-// Bound by the reading of the pages; two pages (32 positions) per softmax step, so that the
-// cross-lane maximum, the waits and the copies' bookkeeping are paid once for 8 KB.
+// Two pages (32 positions) per softmax step, so that the cross-lane maximum, the waits and the
+// copies' bookkeeping are paid once for 8 KB. NT = 1 (up to 8 rows of a kv head: decode steps) is
+// bound by the reading of the pages: 128 sequences of up to 16384, 5.9 TB/s. NT = 2 by the issue of
+// MMAs, exponentials and conversions: 32 x 4096 positions 57 us with 8 rows, 76 with 16 (one unit),
+// 126 with 32 (two units).
 //
 // UNIT: few units, each given to the warps of a cluster (`parts` of them, equal runs of its pages),
 // which join their records themselves behind a cluster barrier: no scan of the batch and no merge

@@ -187,7 +187,9 @@ cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs
                                   const Outputs &out, void *workspace, int32_t *err, cudaStream_t s);
 
 // Up to this many query rows (positions x query heads of a kv head) of a sequence the warp
-// kernel takes the call, beyond it the tile kernel.
+// kernel takes the call, beyond it the tile kernel, whose time hardly depends on the rows up to
+// 256. 32 x 4096 positions, warp kernel: 16 rows 76 us, 32 rows 126, 64 rows 226; tile kernel: 124
+// to 256 rows 207 to 210. 4 x 8000: 64 rows 69, tile kernel 77 to 89.
 constexpr int kWarpRows = 64;
 
 }  // namespace kv4

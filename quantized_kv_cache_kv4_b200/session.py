@@ -10,6 +10,9 @@ Cache construction for a workload (seq_lens = lengths after step 0's append):
   3. context prefill: every sequence appends its own positions up to seq_len - 2;
   4. each decode step s appends position seq_len - 1 + s and attends over seq_len + s.
 Without a shared prompt, steps 1-2 are skipped and step 3 starts at position 0.
+
+Eviction: weigh_step after a step's attention adds its weights to running totals; evict then
+cuts the sequences that have outgrown a budget, and the later steps go on from there.
 """
 from __future__ import annotations
 
@@ -58,6 +61,7 @@ class DecodeSession:
         # attention calls reuse the work list the previous call on the shared workspace
         # left (layers after the first of one decode step: same lengths and paging)
         self.plan_reuse = False
+        self.totals = None  # attention weight of each cached position, once weigh_step has run
         ws = self._workspace_size(B, self.max_len)
         if workspace is not None and workspace.numel() >= ws:
             self.workspace = workspace  # shared with other layers (calls run in stream order)
@@ -196,6 +200,38 @@ class DecodeSession:
                        self.q[s], self.out if out is None else out, out_f32, lse,
                        stream=stream)
 
+    # ------------------------------------------------------------------ eviction
+    def weigh_step(self, s: int, lse: torch.Tensor):
+        """Add step s's attention weights to the totals (lse: as its attention wrote it,
+        fp32 [B, Hq])."""
+        if self.totals is None:
+            self.totals = torch.zeros((self.wl.num_seqs, self.wl.num_kv_heads, self.max_len),
+                                      dtype=torch.float32, device=self.device)
+        kv4.attention_weights(self.cache, self.batch(self.step_lens[s]), self.q[s], lse,
+                              self.totals, self.totals, self.err)
+
+    def evict(self, s: int, budget: int):
+        """After step s: sequences of more than `budget` positions keep, per kv head, the
+        sinks, the recent window and the positions of the largest totals; the lengths of
+        the later steps follow. Returns (keep int32 [B, Hkv, budget], new_lens int32 [B])."""
+        if self.wl.shared_prefix:
+            raise ValueError("sequences that share pages cannot be evicted in place")
+        if self.totals is None:
+            raise ValueError("evict needs the totals of at least one weigh_step")
+        wl, batch = self.wl, self.batch(self.step_lens[s])
+        keep = torch.empty((wl.num_seqs, wl.num_kv_heads, budget), dtype=torch.int32,
+                           device=self.device)
+        new_lens = torch.empty(wl.num_seqs, dtype=torch.int32, device=self.device)
+        kv4.evict_select(self.cfg, batch, self.totals, keep, new_lens, self.err)
+        # positions appended later start from a total of 0
+        kept = torch.zeros_like(self.totals)
+        kv4.evict_compact(self.cache, batch, keep, new_lens, acc_in=self.totals, acc_out=kept,
+                          err=self.err)
+        self.totals = kept
+        later = torch.arange(1, self.steps - s, dtype=torch.int32, device=self.device)
+        self.step_lens[s + 1:] = new_lens[None, :] + later[:, None]
+        return keep, new_lens
+
     def check_err(self):
         flag = int(self.err.item())
         if flag:
@@ -229,3 +265,42 @@ class BaselineSession(DecodeSession):
         """The comparison caches have no fused entry point: the two calls in order."""
         self.append(batch, k, v, None, stream=stream)
         self.attend(batch, q, out, out_f32, lse, stream=stream)
+
+    def weigh_step(self, s, lse):
+        raise NotImplementedError("attention weights are read from the KV4 cache")
+
+    def evict(self, s, budget):
+        raise NotImplementedError("eviction is the KV4 cache's")
+
+
+class Block8Session(BaselineSession):
+    """The same decode batch over pages of 8-bit codes with one scale per (page, kv head):
+    kv4.BLOCK8_INT8 or kv4.BLOCK8_E4M3, no protected set. Beside the decode steps,
+    verify_step attends with several queries per sequence."""
+
+    def _allocate_cache(self):
+        return kv4.allocate_block8_cache(self.fmt, self.cfg, self.paging.num_pages,
+                                         device=self.device)
+
+    def _workspace_size(self, num_seqs, max_len):
+        return kv4.block8_workspace_size(self.cfg, num_seqs, num_seqs, 1, max_len)
+
+    def append(self, batch, k, v, indptr=None, stream=None):
+        kv4.block8_append(self.cache, batch, k, v, indptr, self.err, stream=stream)
+
+    def attend(self, batch, q, out, out_f32=None, lse=None, stream=None):
+        kv4.block8_attention(self.cache, batch, q, out, self.workspace, out_f32=out_f32, lse=lse,
+                             err=self.err, stream=stream)
+
+    def verify_workspace(self, rows: int, max_queries: int) -> torch.Tensor:
+        """A workspace for verify_step."""
+        size = kv4.block8_workspace_size(self.cfg, self.wl.num_seqs, rows, max_queries,
+                                         self.max_len)
+        return torch.empty(size, dtype=torch.uint8, device=self.device)
+
+    def verify_step(self, s, q, out, indptr, max_queries, workspace, out_f32=None, lse=None,
+                    stream=None):
+        """Causal attention of each sequence's last positions as of step s: q, out bf16
+        [rows, Hq, 128], indptr int32 [B + 1], at most max_queries rows of one sequence."""
+        kv4.block8_attention(self.cache, self.batch(self.step_lens[s]), q, out, workspace, indptr,
+                             max_queries, out_f32, lse, self.err, stream=stream)
