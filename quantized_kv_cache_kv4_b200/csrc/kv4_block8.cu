@@ -249,10 +249,13 @@ __global__ void __launch_bounds__(256, 3) block8_append_rows_kernel(
 constexpr int kAttnCtas = 148 * 3;            // resident CTAs of the largest grid
 constexpr int kAttnWarps = kAttnCtas * kWarps;
 constexpr int kMinShare = 4;                  // pages per warp, at least (~1 us: a record's join)
-// Units of at most this many CTAs (two per SM) get clusters of their own, which saves the scan and
-// the merge launch: decode steps of 3 x 500 positions 15 -> 12 us, 4 x 8000 42 -> 21, 32 x 4096 64 ->
-// 55; with more units than this the equal shares balance better.
+// Units of at most kUnitCtas CTAs (two per SM) whose warps then get at most kUnitPages pages each have
+// clusters of their own, which saves the scan and the merge launch. Clusters / equal shares, us:
+// 4 x 500 positions 8 / 14, 1 x 16000 25 / 43, 4 x 8000 20 / 27, 36 x 2000 31 / 39 (100 to 2000: 25 /
+// 23). With more pages the longest sequence decides: 64 per warp 50 / 57, but ragged (512 to 4096)
+// 47 / 42; 128 per warp and ragged 114 / 74.
 constexpr int kUnitCtas = 296;
+constexpr int kUnitPages = 32;
 constexpr int kCols = 8;                      // query rows of a unit (MMA N)
 
 struct Seq8 : SeqRows {
@@ -791,7 +794,7 @@ static cudaError_t resident_ctas(int *most) {
 }
 
 // CTAs of a cluster that takes one unit (0: the batch is split by pages instead). A cluster's warps
-// get two pages at least of the longest sequence.
+// get two pairs of pages at least of the longest sequence.
 static int unit_cluster(int num_seqs, int max_q_len, int max_seq_len, int H, int G, int rows) {
   const long long units = static_cast<long long>(num_seqs) * H *
                           ((static_cast<long long>(max_q_len) * G + rows - 1) / rows);
@@ -799,7 +802,7 @@ static int unit_cluster(int num_seqs, int max_q_len, int max_seq_len, int H, int
   const int pages = (max_seq_len + kPage - 1) / kPage;
   int ctas = 1;
   while (ctas < 8 && units * ctas * 2 <= kUnitCtas && pages >= 2 * kWarps * ctas * kPair) ctas *= 2;
-  return ctas;
+  return pages > kUnitPages * kWarps * ctas ? 0 : ctas;
 }
 
 template <int F, int NT>

@@ -37,7 +37,7 @@ __device__ __forceinline__ Tiles tiles_of(const CacheView &c, int acc_stride, in
   return t;
 }
 
-constexpr int kWMinShare = 4;  // tiles per warp, at least
+constexpr int kWMinShare = 4;  // tiles per warp, at least (~1 us: as much as a warp's start)
 constexpr int kWStages = 4;
 // a stage: the K codes of two kv heads (INT8: 2 x 2048 bytes), then their scales or parameters
 constexpr int kWOffPar = 2 * kInt8CodeBytes;
@@ -63,7 +63,10 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a01, uint32
 // only rounding of a logit is the fp32 accumulation. INT4 codes enter as fp16 subnormals (c * 2^-24,
 // or 16 c * 2^-24 for the odd dims, whose query elements carry the factor 1/16); a group's scale and
 // minimum multiply its product and its query sum, s = kk sum_g (scale_g (q c)_g + min_g sum(q)_g / kk).
-// Bound by instruction issue and the reading of K.
+// 64 x 2048 positions, 32 query and 8 kv heads: 31 us with two heads per warp, 42 with one; 48 long
+// tails 80 and 114 us (4.0 TB/s); 4 x 500 positions 8.9 and 7.7. Bound by the chain of a tile (codes to
+// MMAs to exponentials to the sum, 146 to 165 registers a thread allow three warps per scheduler)
+// next to the reading of K; two to six CTAs per SM with fewer stages are no faster.
 template <int HPW>
 __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     CacheView c, const uint16_t *__restrict__ q, const float *__restrict__ lse, const float *acc_in,
@@ -858,7 +861,9 @@ cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc,
                           int32_t *keep, int32_t *new_lens, int32_t *err, cudaStream_t s) {
   const int units = c.num_seqs * c.num_kv_heads;
   const int longest = max_seq_len < acc_stride ? max_seq_len : acc_stride;
-  // the fewest keys per thread that hold the longest row
+  // the fewest keys per thread that hold the longest row (64 x 8 rows of 2048: 10 us with 4 keys, 25
+  // with 32; of 8192: 18 with 16, 26 with 32, 83 with the row read again; 128 x 8 of up to 16384: 44
+  // with 32, 240 with the row read again)
   if (longest <= 4 * kSelThreads)
     select_kernel<4><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
   else if (longest <= 16 * kSelThreads)
