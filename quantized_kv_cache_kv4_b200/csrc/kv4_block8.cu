@@ -750,9 +750,12 @@ static int attn_warps(long long t_max) {
   return static_cast<int>((w + kWarps - 1) / kWarps * kWarps);
 }
 
+// Pages of n positions (any n: n + 15 may not fit).
+static int pages_of(int n) { return n / kPage + (n % kPage != 0); }
+
 static long long items_bound(int num_seqs, int total_q, int max_seq_len, int H, int G, int rows) {
   const long long units = (static_cast<long long>(total_q) * G + rows - 1) / rows + num_seqs;
-  return units * H * std::max(1, (max_seq_len + kPage - 1) / kPage);
+  return units * H * std::max(1, pages_of(max_seq_len));
 }
 
 // A note and two records of each warp, of the larger of the two unit sizes; or, for few units, two
@@ -799,7 +802,7 @@ static int unit_cluster(int num_seqs, int max_q_len, int max_seq_len, int H, int
   const long long units = static_cast<long long>(num_seqs) * H *
                           ((static_cast<long long>(max_q_len) * G + rows - 1) / rows);
   if (units > kUnitCtas) return 0;
-  const int pages = (max_seq_len + kPage - 1) / kPage;
+  const int pages = pages_of(max_seq_len);
   int ctas = 1;
   while (ctas < 8 && units * ctas * 2 <= kUnitCtas && pages >= 2 * kWarps * ctas * kPair) ctas *= 2;
   return pages > kUnitPages * kWarps * ctas ? 0 : ctas;

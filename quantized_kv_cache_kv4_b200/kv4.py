@@ -447,10 +447,10 @@ def _launch(fn, args, err, stream, *tensors):
     """fn(*args, err, stream) with the tensors' device current: a launch goes to the current
     device, whichever the caller left current."""
     dev = tensors[0].get_device()
-    for t in tensors:
+    e = _addr_or_null(err, "err", torch.int32, (1,))
+    for t in tensors + (err,):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"kv4 arguments on different devices: {tensors[0].device} and {t.device}")
-    e = _addr_or_null(err, "err", torch.int32, (1,))
     if dev == torch.cuda.current_device():
         return fn(*args, e, torch.cuda.current_stream(dev).cuda_stream if stream is None
                   else stream.cuda_stream)
@@ -482,6 +482,8 @@ class Block8Cache:
             _addr(self.k, "k", code, codes), _addr(self.v, "v", code, codes),
             _addr(self.k_scales, "k_scales", torch.float16, scales),
             _addr(self.v_scales, "v_scales", torch.float16, scales), pages))
+        if len({t.get_device() for t in (self.k, self.v, self.k_scales, self.v_scales)}) > 1:
+            raise ValueError("a block8 cache on several devices")
 
     @property
     def num_pages(self):
@@ -514,8 +516,8 @@ def block8_append(cache: Block8Cache, batch: BatchTensors, k_new: torch.Tensor,
     args = (cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(cache.pool), ctypes.byref(bs),
             _addr(k_new, "k_new", torch.bfloat16, rows), _addr(v_new, "v_new", torch.bfloat16, rows),
             _addr_or_null(new_indptr, "new_indptr", torch.int32, (bs.num_seqs + 1,)), n)
-    _check(_launch(_lib.kv4_block8_append, args, err, stream, cache.k, batch.seq_lens, k_new, v_new,
-                   new_indptr), "kv4_block8_append")
+    _check(_launch(_lib.kv4_block8_append, args, err, stream, cache.k, batch.page_table,
+                   batch.seq_lens, k_new, v_new, new_indptr), "kv4_block8_append")
 
 
 def block8_workspace_size(cfg: Config, num_seqs: int, total_q: int, max_q_len: int,
@@ -543,8 +545,8 @@ def block8_attention(cache: Block8Cache, batch: BatchTensors, q: torch.Tensor, o
             _addr_or_null(out_f32, "out_f32", torch.float32, rows),
             _addr_or_null(lse, "lse", torch.float32, (n, Hq)),
             _addr(workspace, "workspace", torch.uint8, (None,)), workspace.numel())
-    _check(_launch(_lib.kv4_block8_attention, args, err, stream, cache.k, batch.seq_lens, q, out,
-                   workspace, q_indptr, out_f32, lse), "kv4_block8_attention")
+    _check(_launch(_lib.kv4_block8_attention, args, err, stream, cache.k, batch.page_table,
+                   batch.seq_lens, q, out, workspace, q_indptr, out_f32, lse), "kv4_block8_attention")
 
 
 # ----------------------------------------------------------------------------
@@ -566,8 +568,8 @@ def attention_weights(cache: Cache, batch: BatchTensors, q: torch.Tensor, lse: t
             _addr(lse, "lse", torch.float32, (B, cfg.num_q_heads)),
             _addr_or_null(acc_in, "acc_in", torch.float32, total),
             _addr(acc_out, "acc_out", torch.float32, total), stride)
-    _check(_launch(_lib.kv4_attention_weights, args, err, stream, cache.k_codes, batch.seq_lens, q,
-                   lse, acc_out, acc_in), "kv4_attention_weights")
+    _check(_launch(_lib.kv4_attention_weights, args, err, stream, cache.k_codes,
+                   batch.page_table, batch.seq_lens, q, lse, acc_out, acc_in), "kv4_attention_weights")
 
 
 def evict_select(cfg: Config, batch: BatchTensors, acc: torch.Tensor, keep: torch.Tensor,
@@ -605,5 +607,5 @@ def evict_compact(cache: Cache, batch: BatchTensors, keep: torch.Tensor, new_len
             _addr_or_null(dst_ring_idx, "dst_ring_idx", torch.int32, (B,)),
             _addr_or_null(acc_in, "acc_in", torch.float32, (B, H, s_in)), s_in,
             _addr_or_null(acc_out, "acc_out", torch.float32, (B, H, s_out)), s_out)
-    _check(_launch(_lib.kv4_evict_compact, args, err, stream, cache.k_codes, batch.seq_lens, keep,
-                   new_lens, dst_page_table, dst_ring_idx, acc_in, acc_out), "kv4_evict_compact")
+    _check(_launch(_lib.kv4_evict_compact, args, err, stream, cache.k_codes, batch.page_table,
+                   batch.seq_lens, keep, new_lens, dst_page_table, dst_ring_idx, acc_in, acc_out), "kv4_evict_compact")

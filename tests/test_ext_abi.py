@@ -140,3 +140,41 @@ def test_binding_refuses_wrong_types_and_shapes(kv4):
         kv4.allocate_block8_cache(5, kv4.make_config(8, 2, 0, 0), 4, device="cpu")
     with pytest.raises(ValueError):
         kv4.allocate_block8_cache(kv4.BLOCK8_INT8, kv4.make_config(8, 2, 0, 0), 4, device="cpu")
+
+
+def test_block8_workspace_at_the_largest_lengths(kv4):
+    """Rounding a length up to pages must not run over: the size never falls."""
+    cfg = kv4.make_config(32, 8, 0, 0)
+    top = 2 ** 31 - 1
+    for n, q, m in ((1, 1, 1), (4, 16, 4), (4, 400, 100)):
+        sizes = [kv4.block8_workspace_size(cfg, n, q, m, L) for L in (0, 1, 1000, 2 ** 30, top - 15, top - 1, top)]
+        assert sizes == sorted(sizes) and sizes[-1] == sizes[-4]
+
+
+def test_binding_refuses_several_devices(kv4):
+    """Every tensor of a call, the error word among them, has to be on one device."""
+    import torch
+
+    class On(torch.Tensor):  # a tensor that says it is on a GPU
+        is_cuda = True
+        gpu = 0
+
+        def get_device(self):
+            return self.gpu
+
+    def on(gpu, *shape, dtype=torch.int32):
+        t = torch.zeros(shape, dtype=dtype).as_subclass(On)
+        t.gpu = gpu
+        return t
+
+    called = []
+    with pytest.raises(ValueError, match="different devices"):
+        kv4._launch(lambda *a: called.append(a), (), on(1, 1), None, on(0, 4))
+    with pytest.raises(ValueError, match="different devices"):
+        kv4._launch(lambda *a: called.append(a), (), None, None, on(0, 4), None, on(2, 4))
+    cfg = kv4.make_config(8, 2, 0, 0)
+    codes = [on(g, 3, 2, 8, 16, 16, dtype=torch.int8) for g in (0, 1)]
+    scales = [on(0, 3, 2, dtype=torch.float16) for _ in range(2)]
+    with pytest.raises(ValueError, match="several devices"):
+        kv4.Block8Cache(kv4.BLOCK8_INT8, cfg, *codes, *scales)
+    assert not called
