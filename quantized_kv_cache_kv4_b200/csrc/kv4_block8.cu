@@ -159,26 +159,29 @@ __device__ __forceinline__ uint4 transpose4(uint32_t a, uint32_t b, uint32_t c, 
   return hi1 ? make_uint4(u, p1, w, q1) : make_uint4(p0, u, q0, w);
 }
 
-// CSR rows. A CTA looks over kRowsPerCta rows; the first row of the call in each page leads that
+// CSR rows. A CTA looks over `span` rows; the first row of the call in each page leads that
 // page's rows (they may reach past the CTA's). One warp per (led page, kv head, K or V): its rows
 // (up to 16 x 256 bytes) in registers, the block's largest magnitude, the codes, and full 64-byte
 // runs of each strip out. Bound by HBM (512 bytes of rows in, 256 of codes out per position and
 // head) and the latency of a page's loads; the search for a row's sequence is shared by the CTA's
 // ~4 pages and all heads. Prefill of 64 sequences of up to 1024 (47k rows x 8 kv heads): 64 rows
-// per CTA, three CTAs per SM, 67 us (4.3 TB/s); 16 rows per CTA 80 us.
-constexpr int kRowsPerCta = 64;
+// per CTA, three CTAs per SM, 67 us (4.3 TB/s); 16 rows per CTA 80 us. Fewer rows than that fills
+// the GPU with are dealt to more CTAs: 1024 sequences of 1 to 3 rows 87 -> 22 us, 64 of 2 to 9 rows 39 ->
+// 7.5, one of 300 rows 18 -> 7.
+constexpr int kRowsPerCta = 64;  // at most
+constexpr int kAppendCtas = 148 * 3;
 template <int F>
 __global__ void __launch_bounds__(256, 3) block8_append_rows_kernel(
     CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
-    const int32_t *__restrict__ indptr, int32_t total_new, int32_t *err) {
+    const int32_t *__restrict__ indptr, int32_t total_new, int span, int32_t *err) {
   __shared__ int4 lead[kRowsPerCta];  // (first row, rows, slot, page)
   __shared__ int n_lead;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H = c.num_kv_heads;
   if (threadIdx.x == 0) n_lead = 0;
   __syncthreads();
-  if (threadIdx.x < kRowsPerCta) {
-    const int row = blockIdx.x * kRowsPerCta + threadIdx.x;
+  if (threadIdx.x < span) {
+    const int row = blockIdx.x * span + threadIdx.x;
     if (row < total_new) {
       int b, pos, L;
       locate_new_token(c.seq_lens, c.num_seqs, indptr, row, b, pos, L);
@@ -731,8 +734,9 @@ static cudaError_t launch_block8_append_t(const CacheView &c, const uint16_t *k_
     const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
     block8_append_token_kernel<F><<<blocks, 256, 0, s>>>(c, k_new, v_new, err);
   } else {
-    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(total_new) + kRowsPerCta - 1) / kRowsPerCta);
-    block8_append_rows_kernel<F><<<blocks, 256, 0, s>>>(c, k_new, v_new, indptr, total_new, err);
+    const int span = std::min(kRowsPerCta, (total_new - 1) / kAppendCtas + 1);
+    const unsigned blocks = static_cast<unsigned>((total_new - 1) / span + 1);
+    block8_append_rows_kernel<F><<<blocks, 256, 0, s>>>(c, k_new, v_new, indptr, total_new, span, err);
   }
   return cudaGetLastError();
 }
