@@ -7,7 +7,8 @@
 //                        largest totals of the rest, in ascending order of position.
 //   compact_kernel       the kept rows' INT4 codes, parameters and totals to the front of
 //                        other pages; compact_in_place_kernel of the sequence's own.
-//   ring_kernel          the recent window's INT8 copies to the slots of their new positions.
+//                        Both also move the recent window's INT8 copies to the slots of their
+//                        new positions.
 #include "kv4_attn_common.cuh"
 #include "kv4_split.cuh"
 
@@ -663,11 +664,12 @@ __device__ __forceinline__ uint4 *row_piece(const CacheView &c, size_t blk, int 
 }
 
 // The recent window's INT8 copies: position p (before) is p - (L - n) afterwards, so slot p mod R
-// moves to slot (p - (L - n)) mod R, of the same ring or another. One CTA of 256 threads per
-// (sequence, kv head); all rows (at most 144, 16 pieces of 16 bytes each) are held in registers
+// moves to slot (p - (L - n)) mod R, of the same ring or another. kRingThreads threads of a CTA (its
+// others gone) per (sequence, kv head); all rows (at most 144, 16 pieces of 16 bytes each) are held in registers
 // before any is written.
+constexpr int kRingThreads = 256;
 __device__ __forceinline__ void move_ring(const CacheView &c, const Moves &mv, int b, int h, int32_t *err) {
-  constexpr int kPieces = KV4_MAX_PROTECTED * 16 / 256;  // 9 per thread
+  constexpr int kPieces = KV4_MAX_PROTECTED * 16 / kRingThreads;  // 9 per thread
   const int H = c.num_kv_heads, S = c.num_sinks, R = c.num_recent;
   const int L = c.seq_lens[b];
   const int n = kept_rows(c, mv, b, L, nullptr);
@@ -769,23 +771,25 @@ __global__ void __launch_bounds__(256) compact_kernel(CacheView c, Moves mv, int
   if (totals) mv.acc_out[unit * mv.out_stride + j] = a;
 }
 
-__global__ void __launch_bounds__(256) ring_kernel(CacheView c, Moves mv, int32_t *err) {
-  const int H = c.num_kv_heads, b = blockIdx.x / H;
-  move_ring(c, mv, b, blockIdx.x - b * H, err);
-}
-
 // In the sequence's own pages: one CTA per (sequence, kv head), 16 rows per warp and round.
 // Row j comes from a position >= j, so what a round writes was read in it or before it: one
-// barrier between a round's loads and its stores is all the order there is to keep.
+// barrier between a round's loads and its stores is all the order there is to keep. The second half
+// of the grid, where there is a recent window, moves the rings
+// (one sequence of 777 rows to 500 in 5 us, 64 of 2048 to 1024 in 41; a launch of its own: 9 and 44).
 constexpr int kInPlaceThreads = 512;
 __global__ void __launch_bounds__(kInPlaceThreads) compact_in_place_kernel(CacheView c, Moves mv,
                                                                           int32_t *err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int H = c.num_kv_heads;
-  const int b = blockIdx.x / H, h = blockIdx.x - b * H;
+  const int H = c.num_kv_heads, units = c.num_seqs * H;
+  const int unit0 = blockIdx.x < units ? blockIdx.x : blockIdx.x - units;
+  const int b = unit0 / H, h = unit0 - b * H;
+  if (blockIdx.x >= units) {
+    if (threadIdx.x < kRingThreads) move_ring(c, mv, b, h, err);
+    return;
+  }
   const int L = c.seq_lens[b];
   const int n = kept_rows(c, mv, b, L, h == 0 && threadIdx.x == 0 ? err : nullptr);
-  const size_t unit = blockIdx.x;
+  const size_t unit = unit0;
   const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages;
   const int half = lane >> 4;
   for (int j0 = 0; j0 < n; j0 += kInPlaceThreads / 2) {
@@ -887,10 +891,7 @@ cudaError_t launch_compact(const CacheView &c, const int32_t *keep, int budget, 
     compact_kernel<<<static_cast<unsigned>(c.num_seqs) * (c.num_kv_heads + blocks), 256, 0, s>>>(c, mv, blocks, err);
     return cudaGetLastError();
   }
-  compact_in_place_kernel<<<units, kInPlaceThreads, 0, s>>>(c, mv, err);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || c.num_recent == 0) return e;
-  ring_kernel<<<units, 256, 0, s>>>(c, mv, err);
+  compact_in_place_kernel<<<c.num_recent > 0 ? 2 * units : units, kInPlaceThreads, 0, s>>>(c, mv, err);
   return cudaGetLastError();
 }
 
