@@ -401,3 +401,79 @@ def test_decode_run():
         m.append(k, v, [1, 1, 1], indptr=False)
         m.attend([1, 1, 1], seed=step)
     m.check_pages()
+
+
+@pytest.mark.parametrize("n,G", [(40, 4), (9, 8), (5, 2)], ids=["tiles", "tiles-one-pipeline", "warps"])
+def test_several_positions_on_streams_and_in_graphs(n, G):
+    """Calls of several positions at once on two streams, replayed from a graph, and one after
+    the other on one workspace that the call before left full."""
+    kv4 = _kv4()
+    m = Model("int8", [400, 130, 257, 64], 2, G=G)
+    counts = [390, 121, 250, 60]
+    k, v = rows(sum(counts), 2, 171)
+    m.append(k, v, counts)
+    new = [n, n // 2, n, 1]
+    m.attend(new)
+    total, Hq = sum(new), 2 * G
+    g = torch.Generator(device="cuda").manual_seed(172)
+    q = torch.randn((total, Hq, 128), generator=g, device="cuda").to(torch.bfloat16)
+    ip, batch = ints(np.concatenate([[0], np.cumsum(new)])), m.batch()
+    size = kv4.block8_workspace_size(m.cfg, 4, total, n, 400)
+
+    def call(out, ws, stream=None):
+        kv4.block8_attention(m.cache, batch, q, out, ws, ip, n, err=m.err, stream=stream)
+
+    bufs = [(torch.zeros_like(q), torch.full((size,), 255, dtype=torch.uint8, device="cuda")) for _ in range(4)]
+    call(*bufs[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for (out, ws), s in zip(bufs[1:3], streams):
+            call(out, ws, s)
+    torch.cuda.synchronize()
+    assert torch.equal(bufs[1][0], bufs[0][0]) and torch.equal(bufs[2][0], bufs[0][0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(*bufs[3])
+        call(bufs[2][0], bufs[3][1])
+    for _ in range(2):
+        bufs[3][0].zero_()
+        bufs[2][0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[3][0], bufs[0][0]) and torch.equal(bufs[2][0], bufs[0][0])
+    m.attend(new, seed=5, workspace=bufs[3][1])
+    assert int(m.err.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pages_behind_four_gigabytes(fmt):
+    """Pages whose codes lie past 2^32 bytes hold and give what those of a small pool do."""
+    kv4 = _kv4()
+    lens, H, G = [300, 77], 8, 4
+    cfg = kv4.make_config(H * G, H, 0, 0)
+    pages = [-(-L // 16) for L in lens]
+    k, v = rows(sum(lens), H, 181)
+    g = torch.Generator(device="cuda").manual_seed(182)
+    got = []
+    for pool in (sum(pages), 2 ** 32 // (2048 * H) + 40):
+        cache = kv4.allocate_block8_cache(kv4.BLOCK8_INT8 if fmt == "int8" else kv4.BLOCK8_E4M3, cfg, pool)
+        table = np.zeros((2, max(pages)), np.int32)
+        table[0, :pages[0]] = pool - 1 - np.arange(pages[0])
+        table[1, :pages[1]] = pool - 1 - pages[0] - np.arange(pages[1])
+        batch = kv4.BatchTensors(ints(table), ints(lens), None, None, 300)
+        err = ints([0])
+        kv4.block8_append(cache, batch, k, v, ints([0, lens[0], sum(lens)]), err)
+        res = [cache.k[-sum(pages):].view(torch.uint8).clone(), cache.v_scales[-sum(pages):].clone()]
+        for n in (1, 4, 40):
+            q = torch.randn((2 * n, H * G, 128), generator=g.manual_seed(n), device="cuda").to(torch.bfloat16)
+            out = torch.zeros_like(q)
+            ws = torch.empty(kv4.block8_workspace_size(cfg, 2, 2 * n, n, 300), dtype=torch.uint8, device="cuda")
+            kv4.block8_attention(cache, batch, q, out, ws, ints([0, n, 2 * n]), n, err=err)
+            res.append(out)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        assert res[2].float().abs().max() > 0.01
+        got.append(res)
+        del cache
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -354,3 +354,42 @@ def test_captured_eviction():
         res.append([keep, new] + [rows_of(s.cache, table, b, np.tile(np.arange(n[b]), (2, 1))) for b in range(3)]
                    + [acc[b, :, :n[b]] for b in range(3)])
     assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+def test_pages_behind_four_gigabytes():
+    """Weights and moves of rows whose pages lie past 2^32 bytes are those of a small pool."""
+    kv4, _, _ = _mods()
+    lens, H, G, S, R, budget = [700, 150], 8, 4, 4, 32, 100
+    cfg = kv4.make_config(H * G, H, S, R)
+    pages = [-(-L // 16) for L in lens]
+    g = torch.Generator(device="cuda").manual_seed(191)
+    k, v = (torch.randn((sum(lens), H, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((2, H * G, 128), generator=g, device="cuda").to(torch.bfloat16)
+    got = []
+    for pool in (sum(pages), 2 ** 32 // (1024 * H) + 100):
+        cache = kv4.allocate_cache(cfg, pool, 2, 2)
+        table = np.zeros((2, max(pages)), np.int32)
+        table[0, :pages[0]] = pool - 1 - np.arange(pages[0])
+        table[1, :pages[1]] = pool - 1 - pages[0] - np.arange(pages[1])
+        batch = kv4.BatchTensors(ints(table), ints(lens), ints([0, 1]), ints([0, 1]), 700)
+        err = ints([0])
+        kv4.quantize_append(cache, batch, k, v, ints([0, lens[0], sum(lens)]), err)
+        out, lse = torch.empty_like(q), torch.empty((2, H * G), device="cuda")
+        ws = torch.empty(kv4.workspace_size(cfg, 2, 700), dtype=torch.uint8, device="cuda")
+        kv4.decode_attention(cache, batch, q, out, ws, None, lse, err)
+        acc = torch.zeros((2, H, 700), device="cuda")
+        kv4.attention_weights(cache, batch, q, lse, acc, err=err)
+        keep = torch.empty((2, H, budget), dtype=torch.int32, device="cuda")
+        new = ints([0, 0])
+        kv4.evict_select(cfg, batch, acc, keep, new, err)
+        kv4.evict_compact(cache, batch, keep, new, err=err)
+        after = kv4.BatchTensors(batch.page_table, new, batch.sink_idx, batch.ring_idx, budget)
+        out2 = torch.empty_like(q)
+        kv4.decode_attention(cache, after, q, out2, ws, None, None, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and new.tolist() == [budget, budget]
+        assert out2.float().abs().max() > 0.01
+        got.append([out, lse, acc, keep, out2, cache.k_codes[-sum(pages):].clone(), cache.v_params[-sum(pages):].clone(),
+                    cache.ring_k.clone()])
+        del cache
+    assert all(torch.equal(a, b) for a, b in zip(*got))
