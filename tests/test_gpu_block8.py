@@ -477,3 +477,28 @@ def test_pages_behind_four_gigabytes(fmt):
         got.append(res)
         del cache
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("single", [True, False], ids=["token", "rows"])
+def test_append_infinities(fmt, single):
+    """Infinite elements take the largest code, alone in a block and over codes that are rounded
+    again; every output that sees them is finite."""
+    m = Model(fmt, [20, 20], 2, G=2)
+    k, v = rows(10, 2, 191)
+    m.append(k, v, [5, 5])
+    for step in range(3):
+        k, v = rows(2, 2, 192 + step)
+        if step != 1:
+            k[0, 0, 3], k[1, 1, 127], v[0, 1, 0], v[1, 0, 64] = np.inf, -np.inf, -np.inf, np.inf
+        m.append(k, v, [1, 1], indptr=not single)
+    torch.cuda.synchronize()
+    assert int(m.err.item()) == 0
+    m.check_pages()
+    kv4 = _kv4()
+    q = torch.randn((2, 4, 128), device="cuda").to(torch.bfloat16)
+    out, ws = torch.empty_like(q), torch.empty(kv4.block8_workspace_size(m.cfg, 2, 2, 1, 20), dtype=torch.uint8,
+                                               device="cuda")
+    kv4.block8_attention(m.cache, m.batch(), q, out, ws)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out).all())
