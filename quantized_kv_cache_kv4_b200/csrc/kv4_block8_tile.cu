@@ -378,12 +378,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       Meta cur = ask_page();
       ask_scales(cur);
       Meta nxt = ask_page();
-      for (int k = 0; ok; ++k) {
+      int k = 0;
+      for (; ok; ++k) {
         ok = __all_sync(0xffffffffu, wait(&bars.raw_empty[0], (k & 1) ^ 1));
-        if (!ok) {  // let the copies in flight land before the block ends
-          if (k > 0) wait(&bars.raw_full[0], (k & 1) ^ 1), wait(&bars.raw_full[1], (k & 1) ^ 1);
-          break;
-        }
+        if (!ok) break;
         TileScales &sl = slot_of(k);
         if (cur.kt < 0) {  // no more tiles
           if (lane == 0) {
@@ -423,20 +421,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         if (lane < kTilePages && cur.pid >= 0)
           bulk_g2s(raw + lane * kInt8CodeBytes, c.k_codes + off, kInt8CodeBytes, &bars.raw_full[0]);
         ok = __all_sync(0xffffffffu, wait(&bars.raw_empty[1], (k & 1) ^ 1));
-        if (!ok) {  // let the copies in flight land before the block ends
+        if (!ok) {  // (this tile's K, the last one's V)
           wait(&bars.raw_full[0], k & 1);
           if (k > 0) wait(&bars.raw_full[1], (k & 1) ^ 1);
-        } else {
-          fence_proxy_async_smem();
-          if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[1], bytes);
-          __syncwarp();
-          if (lane < kTilePages && cur.pid >= 0)
-            bulk_g2s(raw + kRawBytes + lane * kInt8CodeBytes, c.v_codes + off, kInt8CodeBytes, &bars.raw_full[1]);
+          k = 0;
+          break;
         }
+        fence_proxy_async_smem();
+        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[1], bytes);
+        __syncwarp();
+        if (lane < kTilePages && cur.pid >= 0)
+          bulk_g2s(raw + kRawBytes + lane * kInt8CodeBytes, c.v_codes + off, kInt8CodeBytes, &bars.raw_full[1]);
         cur = nxt;
         ask_scales(cur);
         nxt = ask_page();
       }
+      // However the loop ended (by a wait for the next segment that gave up, too), the last copies land
+      // before the block ends: the convert warps may have given up on them. (Before the end's mark,
+      // which is a phase of K's barrier, K's last copy has been converted.)
+      if (k > 0 && !ok) wait(&bars.raw_full[0], (k & 1) ^ 1);
+      if (k > 0) wait(&bars.raw_full[1], (k & 1) ^ 1);
     } else if (warp == 14) {
       // ------------------------------- schedule -------------------------------
       if (lane == 0) {
