@@ -419,6 +419,8 @@ size_t kv4_block8_workspace_size(const kv4_config *cfg, int32_t num_seqs, int32_
  * A query before position 0 (n > seq_lens[b]), or of an empty sequence, sees nothing: O = 0,
  * lse = -inf. Positions on a page id outside the pool are left out (KV4_DEVERR_PAGE_ID).
  * A sequence of a length below 0 or above its page table's (KV4_DEVERR_SEQ_LEN) counts as empty.
+ * Where a wait gives up (KV4_DEVERR_TIMEOUT), the run of pages that the waiting worker had still to
+ * finish, of one or more sequences, counts as not there.
  * Logits are sums of exact products in fp32. The weights, times the value scales, enter PV as
  * fp16: 11 significant bits of weight x scale down to 2^-28 of the largest weight times the
  * largest scale where max_q_len * Hq / Hkv is at most 64, down to 2^-21 beyond; below that an
@@ -504,6 +506,9 @@ kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
  * normally and the context stays usable. Work items are numbered in the order the
  * attention's work list holds them (full INT4 chunks first, in sequence order). item < 0
  * cancels a pending request.
+ * kv4_block8_attention takes the request too. It has no work list: item is the number of a warp
+ * of its grid (max_q_len * Hq / Hkv at most 64), whose first copy is withheld and whose whole
+ * share then counts as empty.
  */
 void kv4_test_withhold_copy(int32_t item, uint32_t wait_limit);
 

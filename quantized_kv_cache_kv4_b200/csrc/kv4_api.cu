@@ -168,6 +168,13 @@ void take_test_hook(kv4::Workspace *w) {
   g_withheld = WithheldCopy{};
 }
 
+void take_test_hook(kv4::Waits *w) {
+  if (g_withheld.item < 0) return;
+  w->withheld = g_withheld.item;
+  if (g_withheld.wait_limit > 0) w->limit = g_withheld.wait_limit;
+  g_withheld = WithheldCopy{};
+}
+
 // The pages of a cache without a protected set: BF16, per-token INT8 or 8-bit blocks.
 kv4_status make_paged_view(const kv4_config *cfg, const kv4_paged_pool *pool,
                            const kv4_batch *batch, bool scales, kv4::CacheView *v) {
@@ -465,9 +472,11 @@ kv4_status kv4_block8_attention(int32_t format, const kv4_config *cfg, const kv4
                                            batch->max_seq_len))
     return KV4_ERR_WORKSPACE_TOO_SMALL;
   const kv4::Outputs o{static_cast<uint16_t *>(out), out_f32, lse};
+  kv4::Waits waits;
+  take_test_hook(&waits);
   cudaError_t e = kv4::launch_block8_attention(format, v, static_cast<const uint16_t *>(q), q_indptr,
                                                total_q, max_q_len, batch->max_seq_len, o, workspace,
-                                               err_flag, reinterpret_cast<cudaStream_t>(stream));
+                                               waits, err_flag, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
 }
 

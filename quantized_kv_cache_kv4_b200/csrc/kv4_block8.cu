@@ -333,7 +333,7 @@ constexpr float kLift8 = 14.0f;
 template <int F, int NT, bool UNIT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kernel(
     CacheView c, Queries qs, Outputs out, float *partials, Crossing *__restrict__ notes, int parts,
-    int per_head, int32_t *err) {
+    int per_head, Waits waits, int32_t *err) {
   constexpr int ROWS = kCols * NT;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitSmem split;
@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
   if (UNIT && unit0 % per_head >= sq.units) return;  // (the whole cluster)
 
   uint32_t parity = 0;
+  bool dead = false;  // a wait gave up: its unit's part and all that follow are empty, and copy nothing
   const int mi = lane >> 3, r8 = lane & 7;
   // ldmatrix lane addresses of two strips: (strip 2pr | slots 0-7), (| slots 8-15), strip 2pr+1
   const int ld8 = ((mi >> 1) * 256) + (mi & 1) * 128 + r8 * 16;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
       u = unit - h * sq.units;
     }
     const bool whole = !UNIT && pg0 == 0 && pg1 == sq.pages;
-    const int np = sq.L > 0 ? pg1 - pg0 : 0, pairs = (np + kPair - 1) / kPair;
+    const int np = sq.L > 0 && !dead ? pg1 - pg0 : 0, pairs = (np + kPair - 1) / kPair;
     const int32_t *pt = c.page_table + static_cast<size_t>(b) * c.max_pages + pg0;
 
     if (!UNIT && t == t_begin && lane == 0)
@@ -437,7 +438,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
     };
     pid = load_ids(0);
     int issued = min(pairs, kStages8);
-    for (int j = 0; j < issued; ++j) issue(j);
+    const int withheld = t == t_begin && me == waits.withheld ? 1 : 0;  // (the testing hook)
+    for (int j = withheld; j < issued; ++j) issue(j);
     pid_next = load_ids(32);
 
     // ---- query operands: column gid of group g = query row u * ROWS + 8g + gid ----
@@ -499,7 +501,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
       for (int cc = 0; cc < 8; ++cc) o[g][cc][0] = o[g][cc][1] = o[g][cc][2] = o[g][cc][3] = 0.f;
     }
 
-    bool dead = false;
     for (int j = 0; j < pairs; ++j) {
       const int k = kPair * j;
       if ((k & 31) == 0) {  // the next 32 pages' scales
@@ -529,11 +530,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
         cv_l *= fast_exp2(-vref);
       }
       const int st = j % kStages8;
-      if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u)) {
+      if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u, waits.limit)) {
         if (lane == 0) set_err(err, KV4_DEVERR_TIMEOUT);
-        for (int i = j; i < issued; ++i)  // let its copies in flight land before it ends
-          mbar_wait_bounded(&bars[i % kStages8], (parity >> (i % kStages8)) & 1u, kWaitLimit * 16u);
+        const uint32_t longer = waits.limit > 0x0FFFFFFFu ? 0xFFFFFFFFu : waits.limit * 16u;
+        for (int i = j + withheld; i < issued; ++i)  // let its copies in flight land before it ends
+          mbar_wait_bounded(&bars[i % kStages8], (parity >> (i % kStages8)) & 1u, longer);
         dead = true;
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          m[g][0] = m[g][1] = kNegBig;
+          l[g][0] = l[g][1] = 0.f;
+        }
         break;
       }
       parity ^= 1u << st;
@@ -676,7 +683,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
       __syncwarp();
       if (issued < pairs) issue(issued++);  // the stage is free again
     }
-    if (!UNIT && dead) return;
 
     const float undo = fast_exp2(vref);
 #pragma unroll
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], off);
         const int col = 8 * g + 2 * tig + e, rc = u * ROWS + col;
-        if (rc >= rows || dead) continue;
+        if (rc >= rows) continue;
         if (whole) {
           const size_t qr = static_cast<size_t>(sq.row0 + rc / G) * H * G + h * G + rc % G;
           const float inv = l[g][e] > 0.f ? undo / l[g][e] : 0.f;
@@ -833,8 +839,8 @@ static int unit_cluster(int num_seqs, int max_q_len, int max_seq_len, int H, int
 
 template <int F, int NT>
 static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, int max_seq_len,
-                                        const Outputs &out, void *workspace, int32_t *err,
-                                        cudaStream_t s) {
+                                        const Outputs &out, void *workspace, const Waits &waits,
+                                        int32_t *err, cudaStream_t s) {
   int most = 0;
   constexpr int ROWS = kCols * NT;
   if (const int ctas = unit_cluster(c.num_seqs, qs.max_n, max_seq_len, c.num_kv_heads, c.gqa, ROWS)) {
@@ -853,7 +859,7 @@ static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, i
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, block8_attn_kernel<F, NT, true>, c, qs, out, static_cast<float *>(workspace),
-                              static_cast<Crossing *>(nullptr), ctas * kWarps, per_head, err);
+                              static_cast<Crossing *>(nullptr), ctas * kWarps, per_head, waits, err);
   }
   cudaError_t e = resident_ctas<F, NT, false>(&most);
   if (e != cudaSuccess) return e;
@@ -861,7 +867,8 @@ static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, i
   const int grid = std::min(attn_warps(bound) / kWarps, most);
   Crossing *notes = static_cast<Crossing *>(workspace);
   float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + notes_bytes(grid * kWarps));
-  block8_attn_kernel<F, NT, false><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, notes, 0, 0, err);
+  block8_attn_kernel<F, NT, false><<<grid, kWarps * 32, kCta8Smem, s>>>(c, qs, out, partials, notes, 0, 0, waits,
+                                                                        err);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(block8_merge_kernel<NT>, dim3(grid * kWarps - 1), 256, s, out,
@@ -872,15 +879,13 @@ static cudaError_t launch_block8_attn_t(const CacheView &c, const Queries &qs, i
 cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t *q,
                                     const int32_t *q_indptr, int total_q, int max_q_len,
                                     int max_seq_len, const Outputs &out, void *workspace,
-                                    int32_t *err, cudaStream_t s) {
+                                    const Waits &waits, int32_t *err, cudaStream_t s) {
   const Queries qs{q, q_indptr, total_q, max_q_len};
   const long long rows = static_cast<long long>(max_q_len) * c.gqa;
   if (rows > kWarpRows) return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, err, s);
-  if (fmt == kFmtInt8)
-    return rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1>(c, qs, max_seq_len, out, workspace, err, s)
-                         : launch_block8_attn_t<kFmtInt8, 2>(c, qs, max_seq_len, out, workspace, err, s);
-  return rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1>(c, qs, max_seq_len, out, workspace, err, s)
-                       : launch_block8_attn_t<kFmtE4m3, 2>(c, qs, max_seq_len, out, workspace, err, s);
+  auto launch = fmt == kFmtInt8 ? (rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1> : launch_block8_attn_t<kFmtInt8, 2>)
+                                : (rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1> : launch_block8_attn_t<kFmtE4m3, 2>);
+  return launch(c, qs, max_seq_len, out, workspace, waits, err, s);
 }
 
 }  // namespace kv4

@@ -89,6 +89,12 @@ struct Workspace {
 
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded-wait attempts in normal operation
 
+// What the testing hook asks of a call that has no work list (nothing: the defaults).
+struct Waits {
+  int32_t withheld = -1;        // worker whose first copy is not issued
+  uint32_t limit = kWaitLimit;  // attempts of one bounded wait for a copy
+};
+
 // Where the merged attention output goes.
 struct Outputs {
   uint16_t *out;   // bf16 [B][Hq][128]
@@ -156,7 +162,7 @@ size_t block8_workspace_bytes(int num_seqs, int total_q, int max_q_len, int max_
 cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t *q,
                                     const int32_t *q_indptr, int total_q, int max_q_len,
                                     int max_seq_len, const Outputs &out, void *workspace,
-                                    int32_t *err, cudaStream_t s);
+                                    const Waits &waits, int32_t *err, cudaStream_t s);
 
 // Eviction (kv4_evict.cu).
 cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,

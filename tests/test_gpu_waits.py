@@ -1,0 +1,104 @@
+"""A wait that gives up in the block-scaled cache's attention: the testing hook withholds one
+worker's first copy (nothing is issued, so nothing is in flight) and bounds each wait by 64 attempts. The call returns with KV4_DEVERR_TIMEOUT alone, that worker's part
+counts as empty, everything else is as usual, and so is the next call."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_long_batches import Batch8, SMS, bf, rows
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = 32
+WARPS = 4  # of a block
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from quantized_kv_cache_kv4_b200 import build
+    build.build()
+
+
+def withhold(worker):
+    from quantized_kv_cache_kv4_b200 import kv4
+    kv4._lib.kv4_test_withhold_copy(worker, 64)
+
+
+def pages_of(L):
+    return max(1, -(-L // 16))
+
+
+def share(total, workers, least, w):
+    """[begin, end) of worker w, as the kernels deal `total` items."""
+    k = max(1, min(workers, total // least))
+    per, more = divmod(total, k)
+    at = lambda i: min(i * per + min(i, more), total)  # noqa: E731
+    return at(w), at(w + 1)
+
+
+def empty_masks(lens, n, H, G):
+    return {b: torch.zeros((H, m * G, L), dtype=torch.bool) for b, (L, m) in enumerate(zip(lens, n))}
+
+
+def lost_of_warp(lens, n, H, G, unit_rows, worker):
+    """The positions that worker's share of (sequence, kv head, unit, page) covers, by row."""
+    lost = empty_masks(lens, n, H, G)
+    units = [-(-m * G // unit_rows) for m in n]
+    total = sum(u * pages_of(L) * H for u, L in zip(units, lens))
+    bound = (-(-sum(n) * G // unit_rows) + len(lens)) * H * pages_of(max(lens))
+    warps = max(1, min(SMS * 3 * WARPS, bound // 4))
+    grid = min(-(-warps // WARPS), SMS * (3 if unit_rows == 8 else 2))
+    t0, t1 = share(total, grid * WARPS, 4, worker)
+    at, seen = 0, []
+    for b, L in enumerate(lens):
+        for h in range(H):
+            for u in range(units[b]):
+                lo, hi = max(t0, at), min(t1, at + pages_of(L))
+                if lo < hi:
+                    r = slice(u * unit_rows, (u + 1) * unit_rows)
+                    lost[b][h, r, 16 * (lo - at):16 * (hi - at)] = True
+                    seen.append((b, h, u, hi - lo, pages_of(L)))
+                at += pages_of(L)
+    return lost, seen
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 7], ids=["8-rows", "16-rows", "two-units"])
+@pytest.mark.parametrize("worker", [0, 5, 611])
+def test_equal_shares(fmt, n, worker):
+    """Shares that end inside units and hold whole ones; the same warp's next units are empty too."""
+    H, G = 4, 4
+    lens = np.random.default_rng(31).integers(1, 260, 150).tolist()
+    lens[0] = 900
+    assert len(lens) * H > 296
+    counts = [min(n, L) for L in lens]
+    m = Batch8(fmt, lens, H, G, *(bf(x) for x in rows(sum(lens), H, 32)), seed=5)
+    unit_rows = 8 if n * G <= 8 else 16
+    lost, seen = lost_of_warp(lens, counts, H, G, unit_rows, worker)
+    assert seen
+    withhold(worker)
+    m.check(counts, 33, lost=lost, flag=TIMEOUT)
+    m.check(counts, 33)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [1, 4])
+def test_clusters(fmt, n):
+    """A unit dealt to the warps of a cluster: one warp's run of its pages is left out."""
+    lens, H, G = [2000, 777], 2, 4
+    m = Batch8(fmt, lens, H, G, *(bf(x) for x in rows(sum(lens), H, 34)), seed=6)
+    units, pages, ctas = 2 * H, pages_of(max(lens)), 1
+    while ctas < 8 and units * ctas * 2 <= 296 and pages >= 2 * WARPS * ctas * 2:
+        ctas *= 2
+    parts = ctas * WARPS
+    assert pages <= 32 * WARPS * ctas and parts == 32
+    for unit, part in ((0, 0), (1, 31), (3, 7)):  # (sequence 0, head 0), (0, 1), (1, 1)
+        b, h = divmod(unit, H)
+        p = pages_of(lens[b])
+        lost = empty_masks(lens, [n, n], H, G)
+        lost[b][h, :, 16 * (p * part // parts):16 * (p * (part + 1) // parts)] = True
+        withhold(unit * parts + part)
+        m.check([n, n], 35, lost=lost, flag=TIMEOUT)
+    m.check([n, n], 35)
