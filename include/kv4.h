@@ -507,8 +507,8 @@ kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
  * attention's work list holds them (full INT4 chunks first, in sequence order). item < 0
  * cancels a pending request.
  * kv4_block8_attention takes the request too. It has no work list: item is the number of a warp
- * of its grid (max_q_len * Hq / Hkv at most 64), whose first copy is withheld and whose whole
- * share then counts as empty.
+ * of its grid (max_q_len * Hq / Hkv at most 64) or of a thread block (beyond), whose first copy
+ * is withheld and whose whole share then counts as empty.
  */
 void kv4_test_withhold_copy(int32_t item, uint32_t wait_limit);
 

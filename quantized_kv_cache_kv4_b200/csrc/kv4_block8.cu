@@ -881,11 +881,13 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
                                     int max_seq_len, const Outputs &out, void *workspace,
                                     const Waits &waits, int32_t *err, cudaStream_t s) {
   const Queries qs{q, q_indptr, total_q, max_q_len};
+  Waits warp_waits = waits;
+  if (warp_waits.limit == 0) warp_waits.limit = kWaitLimit;
   const long long rows = static_cast<long long>(max_q_len) * c.gqa;
-  if (rows > kWarpRows) return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, err, s);
+  if (rows > kWarpRows) return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, waits, err, s);
   auto launch = fmt == kFmtInt8 ? (rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1> : launch_block8_attn_t<kFmtInt8, 2>)
                                 : (rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1> : launch_block8_attn_t<kFmtE4m3, 2>);
-  return launch(c, qs, max_seq_len, out, workspace, waits, err, s);
+  return launch(c, qs, max_seq_len, out, workspace, warp_waits, err, s);
 }
 
 }  // namespace kv4

@@ -184,7 +184,8 @@ __device__ __forceinline__ void join_records(const float *partials, int rows, in
 // Launches of the many-rows attention (kv4_block8_tile.cu).
 size_t tile_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, int G);
 cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs, int max_seq_len,
-                                  const Outputs &out, void *workspace, int32_t *err, cudaStream_t s);
+                                  const Outputs &out, void *workspace, const Waits &waits, int32_t *err,
+                                  cudaStream_t s);
 
 // Up to this many query rows (positions x query heads of a kv head) of a sequence the warp
 // kernel takes the call, beyond it the tile kernel, whose time hardly depends on the rows up to

@@ -257,7 +257,7 @@ template <int F>
 __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView c, Queries qs, Outputs out,
                                                                      float *__restrict__ partials,
                                                                      Crossing *__restrict__ notes,
-                                                                     int32_t *err) {
+                                                                     Waits waits, int32_t *err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ SplitSmem split;
   __shared__ TileBars bars;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
   auto phase_of = [](int k) { return (k >> 1) & 1; };
   auto slot_of = [&](int k) -> TileScales & { return scales[k & 3]; };
   auto wait = [&](uint64_t *bar, int parity) {
-    if (mbar_wait_bounded(bar, parity, kTileWait)) return true;
+    if (mbar_wait_bounded(bar, parity, waits.limit)) return true;
     set_err(err, KV4_DEVERR_TIMEOUT);
     return false;
   };
@@ -416,9 +416,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         const size_t off = (static_cast<size_t>(max(cur.pid, 0)) * H + cur.h) * kInt8CodeBytes;
         const uint32_t bytes = __popc(there) * kInt8CodeBytes;
         fence_proxy_async_smem();
-        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[0], bytes);
+        const bool asks = k > 0 || me != waits.withheld;  // (the testing hook)
+        if (lane == 0 && asks) mbar_arrive_expect_tx(&bars.raw_full[0], bytes);
         __syncwarp();
-        if (lane < kTilePages && cur.pid >= 0)
+        if (lane < kTilePages && cur.pid >= 0 && asks)
           bulk_g2s(raw + lane * kInt8CodeBytes, c.k_codes + off, kInt8CodeBytes, &bars.raw_full[0]);
         ok = __all_sync(0xffffffffu, wait(&bars.raw_empty[1], (k & 1) ^ 1));
         if (!ok) {  // (this tile's K, the last one's V)
@@ -780,6 +781,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
       if (live && !whole) *reinterpret_cast<float2 *>(rec + kHeadDim) = make_float2(m, l);
       tc_fence_before();
     }
+    if (!ok) {
+      // This warp's rows of the segment where it gave up, and of all that follow: empty.
+      Segments rest(c, qs, find_share(c.num_seqs, me, workers, kTileMinShare, split, items));
+      for (int no = 0; rest.next(); ++no) {
+        const int r = rest.u * kUnitRows + pipe * kTile + row;
+        if (no < seg_no - 1 || r >= rest.sq.n * G) continue;
+        if (rest.k0 == 0 && rest.k1 == rest.nt) {
+          const size_t qr = static_cast<size_t>(rest.sq.row0 + r / G) * H * G + rest.h * G + r % G;
+          for (int x = 0; x < kHeadDim / 8; ++x)
+            reinterpret_cast<uint4 *>(out.out + qr * kHeadDim)[x] = make_uint4(0u, 0u, 0u, 0u);
+          for (int x = 0; out.out_f32 && x < kHeadDim / 4; ++x)
+            reinterpret_cast<float4 *>(out.out_f32 + qr * kHeadDim)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (out.lse) out.lse[qr] = -CUDART_INF_F;
+        } else {
+          float *rec = partials + (static_cast<size_t>(2 * me + (rest.first ? 0 : 1)) * kUnitRows +
+                                   pipe * kTile + row) * kRecordFloats;
+          *reinterpret_cast<float2 *>(rec + kHeadDim) = make_float2(kNegBig, 0.f);
+        }
+      }
+    }
   }
   __syncthreads();
   if (warp == 12) {
@@ -820,7 +841,7 @@ size_t tile_workspace_bytes(int num_seqs, int total_q, int max_seq_len, int H, i
 
 template <int F>
 static cudaError_t launch_tile_t(const CacheView &c, const Queries &qs, int max_seq_len, const Outputs &out,
-                                 void *workspace, int32_t *err, cudaStream_t s) {
+                                 void *workspace, const Waits &waits, int32_t *err, cudaStream_t s) {
   static PerDevice sms;
   int n_sm = 0;
   cudaError_t e = once_per_device(sms, [](int dev, int *g) {
@@ -832,7 +853,7 @@ static cudaError_t launch_tile_t(const CacheView &c, const Queries &qs, int max_
   const int ctas = std::min(n_sm, tile_ctas(c.num_seqs, qs.total, max_seq_len, c.num_kv_heads, c.gqa));
   Crossing *notes = static_cast<Crossing *>(workspace);
   float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + notes_bytes(ctas));
-  block8_tile_kernel<F><<<ctas, kTileThreads, kTileSmem, s>>>(c, qs, out, partials, notes, err);
+  block8_tile_kernel<F><<<ctas, kTileThreads, kTileSmem, s>>>(c, qs, out, partials, notes, waits, err);
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_after(block8_tile_merge_kernel, dim3(ctas - 1, 8), 256, s, out,
@@ -841,9 +862,12 @@ static cudaError_t launch_tile_t(const CacheView &c, const Queries &qs, int max_
 }
 
 cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs, int max_seq_len,
-                                  const Outputs &out, void *workspace, int32_t *err, cudaStream_t s) {
-  return fmt == kFmtInt8 ? launch_tile_t<kFmtInt8>(c, qs, max_seq_len, out, workspace, err, s)
-                         : launch_tile_t<kFmtE4m3>(c, qs, max_seq_len, out, workspace, err, s);
+                                  const Outputs &out, void *workspace, const Waits &waits, int32_t *err,
+                                  cudaStream_t s) {
+  Waits own = waits;
+  if (own.limit == 0) own.limit = kTileWait;
+  return (fmt == kFmtInt8 ? launch_tile_t<kFmtInt8> : launch_tile_t<kFmtE4m3>)(c, qs, max_seq_len, out, workspace, own,
+                                                                                err, s);
 }
 
 }  // namespace kv4

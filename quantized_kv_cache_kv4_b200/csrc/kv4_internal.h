@@ -92,7 +92,7 @@ constexpr uint32_t kWaitLimit = 1u << 22;  // bounded-wait attempts in normal op
 // What the testing hook asks of a call that has no work list (nothing: the defaults).
 struct Waits {
   int32_t withheld = -1;        // worker whose first copy is not issued
-  uint32_t limit = kWaitLimit;  // attempts of one bounded wait for a copy
+  uint32_t limit = 0;           // attempts of one bounded wait (0: the kernel's own)
 };
 
 // Where the merged attention output goes.

@@ -1,5 +1,5 @@
 """A wait that gives up in the block-scaled cache's attention: the testing hook withholds one
-worker's first copy (nothing is issued, so nothing is in flight) and bounds each wait by 64 attempts. The call returns with KV4_DEVERR_TIMEOUT alone, that worker's part
+worker's first copy (nothing is issued, so nothing is in flight) and bounds each wait. The call returns with KV4_DEVERR_TIMEOUT alone, that worker's part
 counts as empty, everything else is as usual, and so is the next call."""
 import numpy as np
 import pytest
@@ -21,9 +21,9 @@ def _need_gpu():
     build.build()
 
 
-def withhold(worker):
+def withhold(worker, attempts=64):
     from quantized_kv_cache_kv4_b200 import kv4
-    kv4._lib.kv4_test_withhold_copy(worker, 64)
+    kv4._lib.kv4_test_withhold_copy(worker, attempts)
 
 
 def pages_of(L):
@@ -102,3 +102,43 @@ def test_clusters(fmt, n):
         withhold(unit * parts + part)
         m.check([n, n], 35, lost=lost, flag=TIMEOUT)
     m.check([n, n], 35)
+
+
+def lost_of_block(lens, n, H, G, worker):
+    """The positions of block `worker`'s share of (sequence, kv head, unit of 256 rows, key tile)."""
+    lost, units = empty_masks(lens, n, H, G), []
+    for b, (L, m) in enumerate(zip(lens, n)):
+        for h in range(H):
+            for u in range(-(-m * G // 256)):
+                last = min(m - 1, ((u + 1) * 256 - 1) // G)
+                units.append((b, h, u, max(0, L - m + last) // 128 + 1))
+    bound = (-(-sum(n) * G // 256) + len(lens)) * H * (max(lens) // 128 + 1)
+    t0, t1 = share(sum(x[3] for x in units), min(SMS, bound), 1, worker)
+    at, whole, cut = 0, 0, 0
+    for b, h, u, nt in units:
+        lo, hi = max(t0, at), min(t1, at + nt)
+        if lo < hi:
+            lost[b][h, 256 * u:256 * u + 256, 128 * (lo - at):128 * (hi - at)] = True
+            whole, cut = whole + (hi - lo == nt), cut + (hi - lo < nt)
+        at += nt
+    return lost, whole, cut
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("name,lens,H,G,n", [
+    ("long-units", [1500, 1417, 40], 8, 4, [700, 333, 1]),
+    ("many-units", np.random.default_rng(36).integers(20, 300, 130).tolist(), 8, 4, None),
+    ("one-tile", [300, 65, 128], 2, 1, [65, 65, 2]),
+], ids=["long-units", "many-units", "one-tile"])
+def test_tiles(fmt, name, lens, H, G, n):
+    """Every role of a block gives up, whole units and parts of units are empty."""
+    n = n or [-(-2 * L // 3) for L in lens]
+    m = Batch8(fmt, lens, H, G, *(bf(x) for x in rows(sum(lens), H, 37)), seed=7)
+    wholes = cuts = 0
+    for worker in (0, 5, 97):
+        lost, whole, cut = lost_of_block(lens, n, H, G, worker)
+        wholes, cuts = wholes + whole, cuts + cut
+        withhold(worker, 1 << 14)  # (a block's roles wait for one another through whole segments)
+        m.check(n, 38, lost=lost, flag=TIMEOUT if whole + cut else 0)
+    assert wholes + cuts and (name == "one-tile" or wholes and cuts)
+    m.check(n, 38)
