@@ -448,7 +448,8 @@ kv4_status kv4_block8_attention(int32_t format, const kv4_config *cfg, const kv4
  *        same batch wrote it (a weight is then at most 1).
  *   acc_in, acc_out: fp32 [num_seqs][Hkv][acc_stride], may be the same; acc_in NULL = zeros.
  *        A sequence longer than acc_stride is refused (KV4_DEVERR_SEQ_LEN). Positions on a bad
- *        page or side index are left as they were, with its error bit. */
+ *        page or side index are left as they were, with its error bit, and so are those that a
+ *        worker whose wait gave up (KV4_DEVERR_TIMEOUT) had still to reach. */
 kv4_status kv4_attention_weights(const kv4_config *cfg, const kv4_int4_pool *pool,
                                  const kv4_int8_side *side, const kv4_batch *batch, const void *q,
                                  const float *lse, const float *acc_in, float *acc_out,
@@ -506,9 +507,10 @@ kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
  * normally and the context stays usable. Work items are numbered in the order the
  * attention's work list holds them (full INT4 chunks first, in sequence order). item < 0
  * cancels a pending request.
- * kv4_block8_attention takes the request too. It has no work list: item is the number of a warp
- * of its grid (max_q_len * Hq / Hkv at most 64) or of a thread block (beyond), whose first copy
- * is withheld and whose whole share then counts as empty.
+ * kv4_block8_attention and kv4_attention_weights take the request too. They have no work list:
+ * item is the number of a warp of the grid (kv4_block8_attention with max_q_len * Hq / Hkv above
+ * 64: of a thread block), whose first copy is withheld, so that its whole share counts as empty
+ * (the totals of its share are left as they were).
  */
 void kv4_test_withhold_copy(int32_t item, uint32_t wait_limit);
 

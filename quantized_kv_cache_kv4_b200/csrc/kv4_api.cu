@@ -491,8 +491,10 @@ kv4_status kv4_attention_weights(const kv4_config *cfg, const kv4_int4_pool *poo
   if (batch->num_seqs == 0) return KV4_OK;
   if (q == nullptr || lse == nullptr || acc_out == nullptr || misaligned16(q))
     return KV4_ERR_INVALID_ARG;
+  kv4::Waits waits;
+  take_test_hook(&waits);
   cudaError_t e = kv4::launch_weights(v, batch->max_seq_len, static_cast<const uint16_t *>(q), lse,
-                                      acc_in, acc_out, acc_stride, err_flag,
+                                      acc_in, acc_out, acc_stride, waits, err_flag,
                                       reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
 }

@@ -68,10 +68,12 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a01, uint32
 // tails 80 and 114 us (4.0 TB/s); 4 x 500 positions 8.9 and 7.7. Bound by the chain of a tile (codes to
 // MMAs to exponentials to the sum, 146 to 165 registers a thread allow three warps per scheduler)
 // next to the reading of K; two to six CTAs per SM with fewer stages are no faster.
-template <int HPW>
+// HOOK: a call with the testing hook armed; without, the constant wait limit folds into the code (as
+// an argument it costs 2 to 4 %).
+template <int HPW, bool HOOK>
 __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     CacheView c, const uint16_t *__restrict__ q, const float *__restrict__ lse, const float *acc_in,
-    float *acc_out, int acc_stride, int32_t *err) {
+    float *acc_out, int acc_stride, Waits waits, int32_t *err) {
   constexpr int CPH = 8 / HPW;  // columns per head
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitSmem split;
@@ -164,7 +166,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
     };
     pid = load_pages(k0);
     int issued = min(k1, k0 + kWStages);
-    for (int k = k0; k < issued; ++k) issue(k);
+    const int withheld = HOOK && t == share.begin && me == waits.withheld ? 1 : 0;
+    for (int k = k0 + withheld; k < issued; ++k) issue(k);
     pid_next = load_pages(k0 + 32);
 
     // ---- query fragments: column gid = (head gid / CPH, query gid % CPH) ----
@@ -253,11 +256,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) weights_kernel(
       in = in && moves;
       const float old = in && acc_in != nullptr ? acc_in[acc0 + pos] : 0.f;
       const int st = (k - k0) % kWStages;
-      if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u)) {
+      const uint32_t limit = HOOK ? waits.limit : kWaitLimit;
+      if (!mbar_wait_bounded(&bars[st], (parity >> st) & 1u, limit)) {
         if (lane == 0) set_err(err, KV4_DEVERR_TIMEOUT);
-        for (int i = k; i < issued; ++i)
-          mbar_wait_bounded(&bars[(i - k0) % kWStages], (parity >> ((i - k0) % kWStages)) & 1u,
-                            kWaitLimit * 16u);
+        const uint32_t longer = limit > 0x0FFFFFFFu ? 0xFFFFFFFFu : limit * 16u;
+        for (int i = k + withheld; i < issued; ++i)  // let its copies in flight land before it ends
+          mbar_wait_bounded(&bars[(i - k0) % kWStages], (parity >> ((i - k0) % kWStages)) & 1u, longer);
         dead = true;
         break;
       }
@@ -830,19 +834,19 @@ __global__ void __launch_bounds__(kInPlaceThreads) compact_in_place_kernel(Cache
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-template <int HPW>
+template <int HPW, bool HOOK>
 static cudaError_t launch_weights_t(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
-                                    const float *acc_in, float *acc_out, int acc_stride, int32_t *err,
-                                    cudaStream_t s) {
+                                    const float *acc_in, float *acc_out, int acc_stride, const Waits &waits,
+                                    int32_t *err, cudaStream_t s) {
   static PerDevice grids;
   int most = 0;
   cudaError_t e = once_per_device(grids, [](int dev, int *g) {
-    cudaError_t r = cudaFuncSetAttribute(weights_kernel<HPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t r = cudaFuncSetAttribute(weights_kernel<HPW, HOOK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kWCtaSmem);
     int sms = 0, per_sm = 0;
     if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (r == cudaSuccess)
-      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, weights_kernel<HPW>, kWarps * 32, kWCtaSmem);
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, weights_kernel<HPW, HOOK>, kWarps * 32, kWCtaSmem);
     *g = sms * (per_sm > 0 ? per_sm : 1);
     return r;
   }, &most);
@@ -851,14 +855,18 @@ static cudaError_t launch_weights_t(const CacheView &c, int max_seq_len, const u
                           (max_seq_len / kPage + 2 + c.sink_tiles + c.ring_tiles);
   const long long want = (tiles / kWMinShare + kWarps) / kWarps;
   const int grid = static_cast<int>(want < most ? want : most);
-  weights_kernel<HPW><<<grid, kWarps * 32, kWCtaSmem, s>>>(c, q, lse, acc_in, acc_out, acc_stride, err);
+  weights_kernel<HPW, HOOK><<<grid, kWarps * 32, kWCtaSmem, s>>>(c, q, lse, acc_in, acc_out, acc_stride, waits, err);
   return cudaGetLastError();
 }
 
 cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
-                           const float *acc_in, float *acc_out, int acc_stride, int32_t *err, cudaStream_t s) {
-  return c.gqa <= 4 ? launch_weights_t<2>(c, max_seq_len, q, lse, acc_in, acc_out, acc_stride, err, s)
-                    : launch_weights_t<1>(c, max_seq_len, q, lse, acc_in, acc_out, acc_stride, err, s);
+                           const float *acc_in, float *acc_out, int acc_stride, const Waits &waits,
+                           int32_t *err, cudaStream_t s) {
+  Waits own = waits;
+  if (own.limit == 0) own.limit = kWaitLimit;
+  auto launch = own.withheld >= 0 ? (c.gqa <= 4 ? launch_weights_t<2, true> : launch_weights_t<1, true>)
+                                  : (c.gqa <= 4 ? launch_weights_t<2, false> : launch_weights_t<1, false>);
+  return launch(c, max_seq_len, q, lse, acc_in, acc_out, acc_stride, own, err, s);
 }
 
 cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc, int acc_stride, int budget,

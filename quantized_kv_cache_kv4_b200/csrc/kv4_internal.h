@@ -166,8 +166,8 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
 
 // Eviction (kv4_evict.cu).
 cudaError_t launch_weights(const CacheView &c, int max_seq_len, const uint16_t *q, const float *lse,
-                           const float *acc_in, float *acc_out, int acc_stride, int32_t *err,
-                           cudaStream_t s);
+                           const float *acc_in, float *acc_out, int acc_stride, const Waits &waits,
+                           int32_t *err, cudaStream_t s);
 cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc, int acc_stride, int budget,
                           int32_t *keep, int32_t *new_lens, int32_t *err, cudaStream_t s);
 cudaError_t launch_compact(const CacheView &c, const int32_t *keep, int budget,

@@ -1,11 +1,11 @@
-"""A wait that gives up in the block-scaled cache's attention: the testing hook withholds one
-worker's first copy (nothing is issued, so nothing is in flight) and bounds each wait. The call returns with KV4_DEVERR_TIMEOUT alone, that worker's part
+"""A wait that gives up in the block-scaled cache's attention or in the attention weights: the
+testing hook withholds one worker's first copy (nothing is issued, so nothing is in flight) and bounds each wait. The call returns with KV4_DEVERR_TIMEOUT alone, that worker's part
 counts as empty, everything else is as usual, and so is the next call."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_long_batches import Batch8, SMS, bf, rows
+from test_gpu_long_batches import Batch8, SMS, bf, ints, paging, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +142,59 @@ def test_tiles(fmt, name, lens, H, G, n):
         m.check(n, 38, lost=lost, flag=TIMEOUT if whole + cut else 0)
     assert wholes + cuts and (name == "one-tile" or wholes and cuts)
     m.check(n, 38)
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 4), (16, 2)], ids=["two-heads-per-warp", "one-head-per-warp"])
+@pytest.mark.parametrize("worker", [0, 3, 70])
+def test_weights(Hq, H, worker):
+    """The totals of the warp's share stay as they were, all others are the usual ones."""
+    from quantized_kv_cache_kv4_b200 import kv4
+    S, R, G = 4, 40, Hq // H
+    lens = [700, 33, 2, 410, 160, 1300]
+    B, hpw = len(lens), 2 if G <= 4 else 1
+    cfg = kv4.make_config(Hq, H, S, R)
+    table, pages = paging(lens, 8)
+    cache = kv4.allocate_cache(cfg, pages, B, B)
+    batch = kv4.BatchTensors(ints(table), ints(lens), ints(range(B)), ints(range(B)), max(lens))
+    err = ints([0])
+    k, v = (bf(x) for x in rows(sum(lens), H, 39))
+    kv4.quantize_append(cache, batch, k, v, ints(np.concatenate([[0], np.cumsum(lens)])), err)
+    q = bf(rows(B, Hq, 40)[0])
+    out, lse = torch.empty_like(q), torch.empty((B, Hq), device="cuda")
+    ws = torch.empty(kv4.workspace_size(cfg, B, max(lens)), dtype=torch.uint8, device="cuda")
+    kv4.decode_attention(cache, batch, q, out, ws, None, lse, err)
+    old = torch.rand((B, H, max(lens)), device="cuda")
+    usual, cut = (torch.full_like(old, -3.0) for _ in range(2))
+    kv4.attention_weights(cache, batch, q, lse, usual, acc_in=old, err=err)
+    withhold(worker)
+    kv4.attention_weights(cache, batch, q, lse, cut, acc_in=old, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == TIMEOUT
+    # a sequence's tiles per pair of heads: INT4 pages that hold [S, L - R), sink tiles, ring tiles
+    tiles = []
+    for L in lens:
+        t = [range(max(S, 16 * p), min(L - R, 16 * p + 16)) for p in range(S // 16, (L - R - 1) // 16 + 1)] if L - R > S else []
+        t += [range(0, min(S, L))]
+        if max(S, L - R) < L:
+            slots = [[p for p in range(max(S, L - R), L) if p % R // 16 == i] for i in range(-(-R // 16))]
+            t += slots
+        tiles.append(t)
+    slots = -(-H // hpw)
+    total = sum(len(t) for t in tiles) * slots
+    bound = B * slots * (max(lens) // 16 + 2 + 1 + -(-R // 16))
+    grid = min((bound // 4 + WARPS) // WARPS, SMS * 3)
+    t0, t1 = share(total, grid * WARPS, 4, worker)
+    want, at, left = usual.clone(), 0, 0
+    for b, t in enumerate(tiles):
+        for h in range(slots):
+            for x in t:
+                if t0 <= at < t1:
+                    want[b, h * hpw:h * hpw + hpw, list(x)] = -3.0
+                    left += 1
+                at += 1
+    assert left == t1 - t0 > 0
+    assert torch.equal(cut, want)
+    err.zero_()
+    kv4.attention_weights(cache, batch, q, lse, cut, acc_in=old, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(cut, usual)
