@@ -731,12 +731,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) block8_attn_kern
 // Block blockIdx.x joins the unit that the share of warp blockIdx.x + 1 starts inside of, where
 // that warp is the unit's second (its note says so).
 template <int NT>
-__global__ void __launch_bounds__(256) block8_merge_kernel(Outputs out, const float *__restrict__ partials,
-                                                           const Crossing *__restrict__ notes, int H, int G) {
+__global__ void __launch_bounds__(256) block8_merge_kernel(Outputs out, const float *partials, const Crossing *notes,
+                                                           int H, int G) {
   constexpr int ROWS = kCols * NT;
   wait_for_launch_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x + 1;
-  const Crossing x = notes[me];
+  const Crossing x = read_note(notes + me);
   for (int col = warp; col < x.rows; col += 8) {
     const int r = x.first_row + col;
     const size_t qr = static_cast<size_t>(x.row0 + r / G) * H * G + x.h * G + r % G;

@@ -104,6 +104,13 @@ __device__ __forceinline__ Crossing crossing(const Shares &sh, int me, long long
   return x;
 }
 
+// A note as the kernel before it left it in L2.
+__device__ __forceinline__ Crossing read_note(const Crossing *note) {
+  const int4 *p = reinterpret_cast<const int4 *>(note);
+  const int4 a = __ldcg(p), b = __ldcg(p + 1);
+  return Crossing{a.x, a.y, a.z, a.w, b.x, b.y, {0, 0}};
+}
+
 inline size_t notes_bytes(size_t workers) { return (workers * sizeof(Crossing) + 255) / 256 * 256; }
 
 // A kernel that may be resident before the launch before it has ended, and waits for that here.

@@ -811,11 +811,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
 
 // Blocks (blockIdx.x, *) join the unit that the share of worker blockIdx.x + 1 starts inside of,
 // where that worker is the unit's second (its note says so); rows over blockIdx.y and the warps.
-__global__ void __launch_bounds__(256) block8_tile_merge_kernel(Outputs out, const float *__restrict__ partials,
-                                                                const Crossing *__restrict__ notes, int H, int G) {
+__global__ void __launch_bounds__(256) block8_tile_merge_kernel(Outputs out, const float *partials,
+                                                                const Crossing *notes, int H, int G) {
   wait_for_launch_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x + 1;
-  const Crossing x = notes[me];
+  const Crossing x = read_note(notes + me);
   for (int i = blockIdx.y * 8 + warp; i < x.rows; i += gridDim.y * 8) {
     const int r = x.first_row + i;
     const size_t qr = static_cast<size_t>(x.row0 + r / G) * H * G + x.h * G + r % G;
