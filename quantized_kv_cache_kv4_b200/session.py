@@ -16,6 +16,8 @@ cuts the sequences that have outgrown a budget, and the later steps go on from t
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -201,35 +203,44 @@ class DecodeSession:
                        stream=stream)
 
     # ------------------------------------------------------------------ eviction
-    def weigh_step(self, s: int, lse: torch.Tensor):
+    def _on(self, stream):
+        """Context in which torch's own work runs on `stream` too (None: the current one)."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    def weigh_step(self, s: int, lse: torch.Tensor, stream=None):
         """Add step s's attention weights to the totals (lse: as its attention wrote it,
         fp32 [B, Hq])."""
-        if self.totals is None:
-            self.totals = torch.zeros((self.wl.num_seqs, self.wl.num_kv_heads, self.max_len),
-                                      dtype=torch.float32, device=self.device)
-        kv4.attention_weights(self.cache, self.batch(self.step_lens[s]), self.q[s], lse,
-                              self.totals, self.totals, self.err)
+        with self._on(stream):
+            if self.totals is None:
+                self.totals = torch.zeros((self.wl.num_seqs, self.wl.num_kv_heads, self.max_len),
+                                          dtype=torch.float32, device=self.device)
+            kv4.attention_weights(self.cache, self.batch(self.step_lens[s]), self.q[s], lse,
+                                  self.totals, self.totals, self.err, stream=stream)
 
-    def evict(self, s: int, budget: int):
+    def evict(self, s: int, budget: int, stream=None):
         """After step s: sequences of more than `budget` positions keep, per kv head, the
         sinks, the recent window and the positions of the largest totals; the lengths of
-        the later steps follow. Returns (keep int32 [B, Hkv, budget], new_lens int32 [B])."""
+        the later steps follow. Returns (keep int32 [B, Hkv, budget], new_lens int32 [B]);
+        they, like the totals from here on, belong to `stream` (None: the current one)."""
         if self.wl.shared_prefix:
             raise ValueError("sequences that share pages cannot be evicted in place")
         if self.totals is None:
             raise ValueError("evict needs the totals of at least one weigh_step")
         wl, batch = self.wl, self.batch(self.step_lens[s])
-        keep = torch.empty((wl.num_seqs, wl.num_kv_heads, budget), dtype=torch.int32,
-                           device=self.device)
-        new_lens = torch.empty(wl.num_seqs, dtype=torch.int32, device=self.device)
-        kv4.evict_select(self.cfg, batch, self.totals, keep, new_lens, self.err)
-        # positions appended later start from a total of 0
-        kept = torch.zeros_like(self.totals)
-        kv4.evict_compact(self.cache, batch, keep, new_lens, acc_in=self.totals, acc_out=kept,
-                          err=self.err)
-        self.totals = kept
-        later = torch.arange(1, self.steps - s, dtype=torch.int32, device=self.device)
-        self.step_lens[s + 1:] = new_lens[None, :] + later[:, None]
+        with self._on(stream):
+            keep = torch.empty((wl.num_seqs, wl.num_kv_heads, budget), dtype=torch.int32,
+                               device=self.device)
+            new_lens = torch.empty(wl.num_seqs, dtype=torch.int32, device=self.device)
+            kv4.evict_select(self.cfg, batch, self.totals, keep, new_lens, self.err, stream=stream)
+            # positions appended later start from a total of 0
+            kept = torch.zeros_like(self.totals)
+            kv4.evict_compact(self.cache, batch, keep, new_lens, acc_in=self.totals, acc_out=kept,
+                              err=self.err, stream=stream)
+            # the old totals may be another stream's memory: not to be given away before this
+            self.totals.record_stream(torch.cuda.current_stream(self.device))
+            self.totals = kept
+            later = torch.arange(1, self.steps - s, dtype=torch.int32, device=self.device)
+            self.step_lens[s + 1:] = new_lens[None, :] + later[:, None]
         return keep, new_lens
 
     def check_err(self):
@@ -266,10 +277,10 @@ class BaselineSession(DecodeSession):
         self.append(batch, k, v, None, stream=stream)
         self.attend(batch, q, out, out_f32, lse, stream=stream)
 
-    def weigh_step(self, s, lse):
+    def weigh_step(self, s, lse, stream=None):
         raise NotImplementedError("attention weights are read from the KV4 cache")
 
-    def evict(self, s, budget):
+    def evict(self, s, budget, stream=None):
         raise NotImplementedError("eviction is the KV4 cache's")
 
 

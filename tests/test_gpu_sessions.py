@@ -190,3 +190,31 @@ def test_block8_session(fmt, lens, prompt, group):
         at += n[b]
     with pytest.raises(NotImplementedError):
         s.evict(0, 40)
+
+
+def test_eviction_on_the_steps_stream():
+    """Steps, weights and evictions on a side stream that lags behind, next to work on the current
+    stream: nothing of them runs, or reads a length, before the step that it follows."""
+    _, session, workload = _mods()
+    steps, budget, runs = 5, 70, []
+    for side in (None, torch.cuda.Stream()):
+        wl = workload.custom_workload([90, 200, 33], num_q_heads=8, num_kv_heads=2, num_sinks=4, num_recent=32,
+                                      seed=33)
+        s = session.DecodeSession(wl, steps=steps)
+        outs = [torch.zeros((3, 8, 128), device="cuda") for _ in range(steps)]
+        lse = torch.zeros((3, 8), device="cuda")
+        torch.cuda.synchronize()
+        kept = []
+        for step in range(steps):
+            if side is not None:
+                with torch.cuda.stream(side):
+                    torch.cuda._sleep(20_000_000)  # ~10 ms: what does not follow the step runs before it
+            s.fused_step(step, out_f32=outs[step], lse=lse, stream=side)
+            s.weigh_step(step, lse, stream=side)
+            if step in (1, 3):
+                kept += s.evict(step, budget, stream=side)
+        torch.cuda.synchronize()
+        s.check_err()
+        runs.append(outs + kept + [s.totals, s.step_lens])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+    assert int(runs[0][-1][-1].max()) == budget + 1
