@@ -189,8 +189,37 @@ def make_config(num_q_heads, num_kv_heads, num_sinks, num_recent, chunk_pages=0,
                   chunk_pages, DEMOTION[demotion], PREFIX[prefix])
 
 
+def _dense(t, what, itemsize, shape, dev):
+    """Raises unless t is a contiguous CUDA tensor on device `dev` (None: any), of elements of
+    `itemsize` bytes (a dtype: of that type), of this shape (None in it: any size)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: a tensor is wanted, not {type(t).__name__}")
+    if t.dtype is not itemsize if isinstance(itemsize, torch.dtype) else t.element_size() != itemsize:
+        raise ValueError(f"{what}: elements of {itemsize} are wanted, not {t.dtype}"
+                         if isinstance(itemsize, torch.dtype) else
+                         f"{what}: elements of {itemsize} bytes are wanted, not {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(shape)} is wanted, not {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted "
+                         f"(got device={t.device}, contiguous={t.is_contiguous()})")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what}: kv4 arguments on different devices ({t.get_device()}, not {dev})")
+
+
+class _Checked:
+    """Remembers what of an object has been checked, until one of its attributes is set anew."""
+
+    _seen = None
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_seen":
+            object.__setattr__(self, "_seen", None)
+
+
 @dataclasses.dataclass
-class Cache:
+class Cache(_Checked):
     """Device storage of one layer's cache, in the library's format (see kv4.h)."""
 
     cfg: Config
@@ -210,6 +239,26 @@ class Cache:
     @property
     def num_pages(self):
         return self.k_codes.shape[0]
+
+    def check(self):
+        """Raises unless all its tensors have the format's shapes and element sizes, dense on one
+        device (a side store that the configuration does not use may be anything)."""
+        H, S, R = self.cfg.num_kv_heads, self.cfg.num_sinks, self.cfg.num_recent
+        if self._seen == (H, S, R):
+            return
+        _dense(self.k_codes, "k_codes", 1, (None, H, 4, PAGE, 16), None)
+        pages, dev = self.k_codes.shape[0], self.k_codes.get_device()
+        _dense(self.v_codes, "v_codes", 1, (pages, H, 4, PAGE, 16), dev)
+        _dense(self.k_params, "k_params", 2, (pages, H, PAGE, 4, 2), dev)
+        _dense(self.v_params, "v_params", 2, (pages, H, PAGE, 4, 2), dev)
+        for name, slots in (("sink", S), ("ring", R)):
+            if slots == 0:
+                continue
+            tiles, sets = (slots + PAGE - 1) // PAGE, getattr(self, name + "_k").shape[0]
+            for x in ("_k", "_v"):
+                _dense(getattr(self, name + x), name + x, 1, (sets, H, tiles, 8, PAGE, 16), dev)
+                _dense(getattr(self, name + x + "s"), name + x + "s", 2, (sets, H, tiles * PAGE), dev)
+        self._seen = (H, S, R)
 
     def pool_struct(self) -> Int4Pool:
         return Int4Pool(self.k_codes.data_ptr(), self.v_codes.data_ptr(),
@@ -246,13 +295,30 @@ def allocate_cache(cfg: Config, num_pages: int, num_sink_sets: int, num_rings: i
 
 
 @dataclasses.dataclass
-class BatchTensors:
+class BatchTensors(_Checked):
     page_table: torch.Tensor  # int32 [B, max_pages]
     seq_lens: torch.Tensor    # int32 [B]
     sink_idx: torch.Tensor | None  # int32 [B]; None where there are no sinks
     ring_idx: torch.Tensor | None
     max_seq_len: int
     plan_reuse: bool = False  # use the work list the last call on the workspace left
+
+    def check(self, table=True, sinks=False, rings=False):
+        """Raises unless the lengths, and what else the call reads, are dense int32 tensors on one
+        device with an entry for each sequence."""
+        want = 1 | 2 * table | 4 * sinks | 8 * rings
+        seen = self._seen or 0
+        if seen & want == want:
+            return
+        _dense(self.seq_lens, "seq_lens", torch.int32, (None,), None)
+        B, dev = self.seq_lens.shape[0], self.seq_lens.get_device()
+        for wanted, name, dims in ((table, "page_table", 2), (sinks, "sink_idx", 1), (rings, "ring_idx", 1)):
+            t = getattr(self, name)
+            if wanted and (t is not None or name == "page_table"):
+                _dense(t, name, torch.int32, (None,) * dims, dev)
+                if t.shape[0] < B:
+                    raise ValueError(f"{name}: {t.shape[0]} entries for {B} sequences")
+        self._seen = seen | want
 
     def struct(self) -> Batch:
         return Batch(self.page_table.data_ptr(), self.page_table.shape[1],
@@ -511,6 +577,7 @@ def block8_append(cache: Block8Cache, batch: BatchTensors, k_new: torch.Tensor,
                   v_new: torch.Tensor, new_indptr: torch.Tensor | None = None,
                   err: torch.Tensor | None = None, stream=None):
     """k_new, v_new: bf16 [rows, Hkv, 128]; new_indptr int32 [B+1] or None (one row per seq)."""
+    batch.check()
     n, bs = k_new.shape[0], batch.struct()
     rows = (n, cache.cfg.num_kv_heads, HEAD_DIM)
     args = (cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(cache.pool), ctypes.byref(bs),
@@ -536,6 +603,7 @@ def block8_attention(cache: Block8Cache, batch: BatchTensors, q: torch.Tensor, o
     """q, out: bf16 [rows, Hq, 128]; q_indptr int32 [B+1]: sequence b's rows are its last
     positions, at most max_q_len of them, causal (None: one per sequence); out_f32 fp32 like
     out; lse fp32 [rows, Hq]; workspace: uint8, block8_workspace_size(...) bytes."""
+    batch.check()
     n, Hq, bs = q.shape[0], cache.cfg.num_q_heads, batch.struct()
     rows = (n, Hq, HEAD_DIM)
     args = (cache.fmt, ctypes.byref(cache.cfg), ctypes.byref(cache.pool), ctypes.byref(bs),
@@ -559,7 +627,10 @@ def attention_weights(cache: Cache, batch: BatchTensors, q: torch.Tensor, lse: t
     """acc_out = acc_in + each position's attention weight in this decode step. q bf16
     [B, Hq, 128]; lse fp32 [B, Hq] as decode_attention wrote it; acc_in, acc_out fp32
     [B, Hkv, positions] (may be the same; None: zeros)."""
-    cfg, bs = cache.cfg, batch.struct()
+    cfg = cache.cfg
+    cache.check()
+    batch.check(sinks=cfg.num_sinks > 0, rings=cfg.num_recent > 0)
+    bs = batch.struct()
     B, stride = bs.num_seqs, acc_out.shape[-1]
     total = (B, cfg.num_kv_heads, stride)
     pool, side = cache.pool_struct(), cache.side_struct()
@@ -576,6 +647,7 @@ def evict_select(cfg: Config, batch: BatchTensors, acc: torch.Tensor, keep: torc
                  new_lens: torch.Tensor, err: torch.Tensor | None = None, stream=None):
     """The positions to keep: acc fp32 [B, Hkv, positions]; keep int32 [B, Hkv, budget]
     (ascending, -1 behind the last) and new_lens int32 [B] are written."""
+    batch.check(table=False)
     bs = batch.struct()
     B, H, stride, budget = bs.num_seqs, cfg.num_kv_heads, acc.shape[-1], keep.shape[-1]
     if B and new_lens.data_ptr() == bs.seq_lens:
@@ -595,7 +667,10 @@ def evict_compact(cache: Cache, batch: BatchTensors, keep: torch.Tensor, new_len
     """Moves the kept rows (keep, new_lens as evict_select wrote them) to the front of the pages
     of dst_page_table int32 [B, pages] (None: the sequence's own), the recent window's INT8
     copies to ring dst_ring_idx int32 [B] (None: its own), and the totals to acc_out."""
-    cfg, bs = cache.cfg, batch.struct()
+    cfg = cache.cfg
+    cache.check()
+    batch.check(rings=cfg.num_recent > 0)
+    bs = batch.struct()
     B, H, budget = bs.num_seqs, cfg.num_kv_heads, keep.shape[-1]
     pages = 0 if dst_page_table is None else dst_page_table.shape[-1]
     s_in, s_out = (0 if t is None else t.shape[-1] for t in (acc_in, acc_out))

@@ -178,3 +178,148 @@ def test_binding_refuses_several_devices(kv4):
     with pytest.raises(ValueError, match="several devices"):
         kv4.Block8Cache(kv4.BLOCK8_INT8, cfg, *codes, *scales)
     assert not called
+
+
+class _On:
+    """Tensors that say they are on a GPU."""
+
+    def __init__(self):
+        import torch
+
+        class On(torch.Tensor):
+            is_cuda = True
+            gpu = 0
+
+            def get_device(self):
+                return self.gpu
+
+        self.cls, self.torch = On, torch
+
+    def __call__(self, shape, dtype, gpu=0):
+        return self.of(self.torch.zeros(shape, dtype=dtype), gpu)
+
+    def of(self, t, gpu=0):
+        t = t.as_subclass(self.cls)
+        t.gpu = gpu
+        return t
+
+
+def _kv4_cache(kv4, on, S=4, R=40, pages=5, H=2, sets=3):
+    import torch
+    cpu = kv4.allocate_cache(kv4.make_config(8, H, S, R), pages, sets, sets, device="cpu")
+    names = [n for n in vars(cpu) if isinstance(getattr(cpu, n), torch.Tensor)]
+    assert len(names) == 12
+    for n in names:
+        setattr(cpu, n, on.of(getattr(cpu, n)))
+    return cpu, names
+
+
+def test_eviction_checks_every_tensor_of_the_cache(kv4):
+    """Another type, shape, order or device of any of the twelve tensors, and of the batch's own, is
+    refused before a pointer is taken; a tensor set anew is looked at again."""
+    import torch
+    on = _On()
+    lens, ids = on((3,), torch.int32), on((3,), torch.int32)
+    q, lse = on((3, 8, 128), torch.bfloat16), on((3, 8), torch.float32)
+    acc, keep, new = on((3, 2, 60), torch.float32), on((3, 2, 44), torch.int32), on((3,), torch.int32)
+    launched = []
+
+    def refused(cache, batch, match=None):
+        with pytest.MonkeyPatch.context() as mp:
+            mp.setattr(kv4, "_launch", lambda *a: launched.append(a) or 0)
+            for call in (lambda: kv4.attention_weights(cache, batch, q, lse, acc),
+                         lambda: kv4.evict_compact(cache, batch, keep, new)):
+                with pytest.raises(ValueError, match=match):
+                    call()
+        assert not launched
+
+    def taken(cache, batch):
+        with pytest.MonkeyPatch.context() as mp:
+            mp.setattr(kv4, "_launch", lambda *a: launched.append(a) or 0)
+            kv4.attention_weights(cache, batch, q, lse, acc)
+            kv4.evict_compact(cache, batch, keep, new)
+        assert len(launched) == 2
+        launched.clear()
+
+    batch = kv4.BatchTensors(on((3, 4), torch.int32), lens, ids, ids, 60)
+    cache, names = _kv4_cache(kv4, on)
+    taken(cache, batch)
+    for name in names:
+        good = getattr(cache, name)
+        wide = torch.zeros(good.shape[:-1] + (2 * good.shape[-1],), dtype=good.dtype)
+        for bad in (on(good.shape, good.dtype, gpu=1), on(good.shape, torch.int64), on.of(wide[..., ::2]),
+                    on(good.shape[:-1], good.dtype), on(good.shape[:1] + (3,) + good.shape[2:], good.dtype),
+                    torch.zeros(good.shape, dtype=good.dtype)):
+            setattr(cache, name, bad)
+            refused(cache, batch)
+        setattr(cache, name, good)
+        taken(cache, batch)
+    # a store that the configuration does not use may be anything
+    plain, _ = _kv4_cache(kv4, on, S=0, R=0)
+    plain.sink_k = plain.ring_vs = on((1,), torch.int64)
+    taken(plain, kv4.BatchTensors(on((3, 4), torch.int32), lens, on((3,), torch.int64), None, 60))
+    table = torch.zeros((3, 8), dtype=torch.int32)
+    for field, bad in (("page_table", on.of(table[:, :4])), ("page_table", on((3, 4), torch.int64)),
+                       ("page_table", on((3, 4), torch.int32, gpu=1)), ("page_table", on((2, 4), torch.int32)),
+                       ("page_table", None), ("seq_lens", on((3,), torch.int64)),
+                       ("seq_lens", on.of(torch.zeros(1, dtype=torch.int32).expand(3))),
+                       ("ring_idx", on((3,), torch.int64)), ("ring_idx", on((2,), torch.int32)),
+                       ("ring_idx", on((3,), torch.int32, gpu=1))):
+        broken = kv4.BatchTensors(on((3, 4), torch.int32), lens, ids, ids, 60)
+        broken.check(rings=True, sinks=True)
+        setattr(broken, field, bad)
+        refused(cache, broken)
+    # rows that the batch does not have are not read
+    taken(cache, kv4.BatchTensors(on((9, 4), torch.int32), lens, on((7,), torch.int32), None, 60))
+
+
+def test_block8_and_select_check_the_batch(kv4):
+    import torch
+    on = _On()
+    cfg = kv4.make_config(8, 2, 0, 0)
+    codes = [on((5, 2, 8, 16, 16), torch.int8) for _ in range(2)]
+    scales = [on((5, 2), torch.float16) for _ in range(2)]
+    cache = kv4.Block8Cache(kv4.BLOCK8_INT8, cfg, *codes, *scales)
+    k, q, out = on((3, 2, 128), torch.bfloat16), on((3, 8, 128), torch.bfloat16), on((3, 8, 128), torch.bfloat16)
+    ws, acc = on((100,), torch.uint8), on((3, 2, 60), torch.float32)
+    keep, new = on((3, 2, 9), torch.int32), on((3,), torch.int32)
+    table, lens = on((3, 4), torch.int32), on((3,), torch.int32)
+    sliced = on.of(torch.zeros((3, 8), dtype=torch.int32)[:, :4])
+    launched = []
+    with pytest.MonkeyPatch.context() as mp:
+        mp.setattr(kv4, "_launch", lambda *a: launched.append(a) or 0)
+        for t, n in ((sliced, lens), (on((3, 4), torch.int64), lens), (table, on((3,), torch.int64)),
+                     (table, on.of(torch.zeros(6, dtype=torch.int32)[::2]))):
+            b = kv4.BatchTensors(t, n, None, None, 60)
+            with pytest.raises(ValueError):
+                kv4.block8_append(cache, b, k, k)
+            with pytest.raises(ValueError):
+                kv4.block8_attention(cache, b, q, out, ws)
+            if n is not lens:
+                with pytest.raises(ValueError):
+                    kv4.evict_select(cfg, b, acc, keep, new)
+        assert not launched
+        b = kv4.BatchTensors(table, lens, None, None, 60)
+        kv4.block8_append(cache, b, k, k)
+        kv4.block8_attention(cache, b, q, out, ws)
+        kv4.evict_select(cfg, kv4.BatchTensors(sliced, lens, None, None, 60), acc, keep, new)
+        assert len(launched) == 3
+
+
+def test_checked_objects_are_copied(kv4):
+    """What has been checked is no part of a copy or a comparison."""
+    import copy
+
+    import torch
+    on = _On()
+    b = kv4.BatchTensors(on((3, 4), torch.int32), on((3,), torch.int32), None, None, 60)
+    b.check()
+    import dataclasses
+    c = dataclasses.replace(b, seq_lens=on((3,), torch.int64))
+    with pytest.raises(ValueError):
+        c.check()
+    d = copy.copy(b)
+    d.seq_lens = on((3,), torch.int64)
+    with pytest.raises(ValueError):
+        d.check()
+    b.check()
