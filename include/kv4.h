@@ -91,8 +91,9 @@ typedef enum {
 #define KV4_DEVERR_WORKSPACE 16u /* the batch needs more work items than the workspace holds
                                     (the call then writes zero outputs, lse = -inf) */
 #define KV4_DEVERR_TIMEOUT 32u   /* a bounded wait for an async copy gave up */
-#define KV4_DEVERR_KEEP 64u      /* kv4_evict_compact: a kept position out of range, out of order,
-                                    or a recent window that was not kept whole */
+#define KV4_DEVERR_KEEP 64u      /* kv4_evict_compact: a kept position below its new place or not
+                                    below the length, a sink that was not kept, or a recent
+                                    window that was not kept whole */
 
 #define KV4_MAX_PROTECTED 144
 
@@ -474,10 +475,10 @@ kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const
  * recent window to the ring slots of their new positions. The sinks keep their places. What
  * lies behind new_lens[b] is left as it was.
  *   batch:     the lengths, pages, sinks and rings before.
- *   keep:      ascending per (b, h), and holding the recent window whole, as kv4_evict_select
- *              writes it. A position below j or not below seq_lens[b] is skipped
- *              (KV4_DEVERR_KEEP); a window not kept whole leaves its ring as it was, with the
- *              same bit.
+ *   keep:      ascending per (b, h), and holding the sinks and the recent window whole, as
+ *              kv4_evict_select writes it. A position below j or not below seq_lens[b], or
+ *              another than j for j < S, is skipped (KV4_DEVERR_KEEP); a window not kept whole
+ *              leaves its ring as it was, with the same bit.
  *   dst_page_table: int32 [num_seqs][dst_max_pages], pages of the same pool that hold no row
  *              this call reads (for sequences that share their prompt's pages); NULL = each
  *              sequence's own pages, which no other sequence may then share.

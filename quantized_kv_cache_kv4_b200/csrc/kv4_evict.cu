@@ -657,6 +657,12 @@ __device__ __forceinline__ int kept_rows(const CacheView &c, const Moves &mv, in
   return n;
 }
 
+// Whether position src of L may go to place j: kept positions ascend, so src >= j, and the sinks keep
+// their places (their INT8 copies do not move).
+__device__ __forceinline__ bool may_move(const CacheView &c, int src, int j, int L) {
+  return src >= j && src < L && (j >= c.num_sinks || src == j);
+}
+
 // 16-byte piece i of a row: K groups 0-3, V groups 0-3, K parameters, V parameters.
 __device__ __forceinline__ uint4 *row_piece(const CacheView &c, size_t blk, int slot, int i) {
   if (i < 8) {
@@ -754,7 +760,7 @@ __global__ void __launch_bounds__(256) compact_kernel(CacheView c, Moves mv, int
     return;
   }
   if (j >= n) return;
-  if (src < j || src >= L) {  // (ascending positions have src >= j)
+  if (!may_move(c, src, j, L)) {
     set_err(err, KV4_DEVERR_KEEP);
     return;
   }
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(kInPlaceThreads) compact_in_place_kernel(Cache
     int dpage = -1, src = -1;
     if (j < n) {
       src = mv.keep[unit * mv.budget + j];
-      if (src < j || src >= L) {
+      if (!may_move(c, src, j, L)) {
         set_err(err, KV4_DEVERR_KEEP);
       } else {
         const int spage = pt[src / kPage];

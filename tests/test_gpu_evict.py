@@ -393,3 +393,40 @@ def test_pages_behind_four_gigabytes():
                     cache.ring_k.clone()])
         del cache
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("other", [False, True], ids=["own-pages", "other-pages"])
+def test_compact_flags_a_sink_that_was_not_kept(other):
+    """A kept set without a sink: its INT8 copy stays where it is, so another row in its place would
+    be read as the sink. The place is flagged and left as it was; the rest moves."""
+    kv4, _, _ = _mods()
+    s = make([200, 200], 8, 2, 4, 32)
+    c, batch = s.cache, s.batch(s.step_lens[0])
+    acc = torch.rand((2, 2, 200), device="cuda")
+    keep, new = ints(np.zeros((2, 2, 64))), ints([0, 0])
+    kv4.evict_select(s.cfg, batch, acc, keep, new, s.err)
+    k = keep.cpu().numpy()
+    k[1, 0, 2] = next(p for p in range(4, 168) if p not in k[1, 0])  # one more of the others instead
+    keep.copy_(torch.from_numpy(np.sort(k, -1)))
+    k = keep.cpu().numpy()
+    assert k[1, 0, 2] == 3 and np.all(np.diff(k[1, 0]) > 0)
+    table, places = s.page_table.cpu().numpy(), np.tile(np.arange(64), (2, 1))
+    dst = table
+    if other:
+        extra = np.arange(8, dtype=np.int32).reshape(2, 4) + c.num_pages
+        for name in ("k_codes", "v_codes", "k_params", "v_params"):
+            t = getattr(c, name)
+            setattr(c, name, torch.cat([t, torch.full((8,) + t.shape[1:], 7, dtype=t.dtype, device="cuda")]))
+        dst = extra
+    want = [rows_of(c, table, b, k[b]) for b in range(2)]
+    before = rows_of(c, dst, 1, places)
+    kv4.evict_compact(c, batch, keep, new, ints(dst) if other else None, err=s.err)
+    torch.cuda.synchronize()
+    assert int(s.err.item()) == 64
+    got = [rows_of(c, dst, b, places) for b in range(2)]
+    assert torch.equal(got[0], want[0])
+    bad = [j for j in range(4) if k[1, 0, j] != j]
+    assert bad == [2, 3]
+    for j in range(64):
+        assert torch.equal(got[1][0, j], before[0, j] if j in bad else want[1][0, j]), j
+    assert torch.equal(got[1][1], want[1][1])
