@@ -885,8 +885,9 @@ cudaError_t launch_block8_attention(int fmt, const CacheView &c, const uint16_t 
   if (warp_waits.limit == 0) warp_waits.limit = kWaitLimit;
   const long long rows = static_cast<long long>(max_q_len) * c.gqa;
   if (rows > kWarpRows) return launch_tile_attention(fmt, c, qs, max_seq_len, out, workspace, waits, err, s);
-  auto launch = fmt == kFmtInt8 ? (rows <= kCols ? launch_block8_attn_t<kFmtInt8, 1> : launch_block8_attn_t<kFmtInt8, 2>)
-                                : (rows <= kCols ? launch_block8_attn_t<kFmtE4m3, 1> : launch_block8_attn_t<kFmtE4m3, 2>);
+  const bool one = rows <= kCols;
+  auto launch = fmt == kFmtInt8 ? (one ? launch_block8_attn_t<kFmtInt8, 1> : launch_block8_attn_t<kFmtInt8, 2>)
+                                : (one ? launch_block8_attn_t<kFmtE4m3, 1> : launch_block8_attn_t<kFmtE4m3, 2>);
   return launch(c, qs, max_seq_len, out, workspace, warp_waits, err, s);
 }
 

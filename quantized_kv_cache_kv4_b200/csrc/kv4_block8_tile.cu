@@ -210,7 +210,8 @@ struct Segments {
   }
 };
 
-// What a key tile's blocks are scaled by; a ring of four, so that a slot is written again only after the softmax threads have left it.
+// What a key tile's blocks are scaled by; a ring of four, so that a slot is written again only after
+// the softmax threads have left it.
 struct alignas(16) TileScales {
   float ks[kTilePages];  // negative: the page is left out
   float cv[kTilePages];  // vs 2^(kPShift - vref)
@@ -723,8 +724,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
             const float2 cv2 = make_float2(cv, cv);
 #pragma unroll
             for (int x = 0; x < 16; x += 2) {
-              float2 z = ffma2(make_float2(__uint_as_float(s[q][16 * hb + x]), __uint_as_float(s[q][16 * hb + x + 1])),
-                               ak2, m2);
+              const uint32_t *at = s[q] + 16 * hb + x;
+              float2 z = ffma2(make_float2(__uint_as_float(at[0]), __uint_as_float(at[1])), ak2, m2);
               z.x = fast_exp2(z.x);
               z.y = fast_exp2(z.y);
               l2 = fadd2(l2, z);
@@ -775,7 +776,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) block8_tile_kernel(CacheView 
         if (live && f32 != nullptr)
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            reinterpret_cast<float4 *>(f32 + 32 * q)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            reinterpret_cast<float4 *>(f32 + 32 * q)[x] =
+                make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
       }
       if (live && whole && out.lse) out.lse[qr] = l > 0.f ? m * kLn2 + logf(l) : -CUDART_INF_F;
       if (live && !whole) *reinterpret_cast<float2 *>(rec + kHeadDim) = make_float2(m, l);
@@ -866,8 +868,8 @@ cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs
                                   cudaStream_t s) {
   Waits own = waits;
   if (own.limit == 0) own.limit = kTileWait;
-  return (fmt == kFmtInt8 ? launch_tile_t<kFmtInt8> : launch_tile_t<kFmtE4m3>)(c, qs, max_seq_len, out, workspace, own,
-                                                                                err, s);
+  auto launch = fmt == kFmtInt8 ? launch_tile_t<kFmtInt8> : launch_tile_t<kFmtE4m3>;
+  return launch(c, qs, max_seq_len, out, workspace, own, err, s);
 }
 
 }  // namespace kv4

@@ -1,6 +1,6 @@
-// A batch of T work items (runs of pages, in sequence order) split into equal contiguous
-// shares, one per worker (a warp, or a CTA's pipeline): no work list, no counter and no launch of its own. Every CTA scans
-// the sequences' item counts itself (a few KB of lengths from L2), so that a share starts
+// A batch of T work items (runs of pages, in sequence order) split into equal contiguous shares,
+// one per worker (a warp, or a CTA): no work list, no counter and no launch of its own. Every CTA
+// scans the sequences' item counts itself (a few KB of lengths from L2), so that a share starts
 // with a search over the block's scan and a walk over one thread's run of sequences.
 #pragma once
 
@@ -31,15 +31,15 @@ struct SplitSmem {
   long long wsum[kSplitThreads / 32];
 };
 
-// The share [begin, end) of worker `me` of W (a warp; all its lanes pass the same), and the sequence its first item is
-// in (whose first item is seq_first). items(b): items of sequence b (>= 0). An empty share
-// has begin >= end. All threads of the block call it.
-// total: where the number of items goes.
+// The share [begin, end) of a worker, and the sequence its first item is in (whose first item is
+// seq_first). An empty share has begin >= end.
 struct Share {
   long long begin, end, seq_first;
   int b;
 };
-// The share of worker `me` from the block's scan (after take_share; no barrier).
+
+// The share of worker `me` of W from the block's scan (after take_share; no barrier).
+// items(b, check): items of sequence b (>= 0).
 template <class Items>
 __device__ __forceinline__ Share find_share(int B, int me, int W, int least, const SplitSmem &sm,
                                             Items items) {
@@ -64,9 +64,10 @@ __device__ __forceinline__ Share find_share(int B, int me, int W, int least, con
   return s;
 }
 
+// The block's scan, and the share of worker `me` (a warp's lanes pass the same). All threads of the
+// block call it; items are asked for with check set once per sequence and block.
 template <class Items>
-__device__ __forceinline__ Share take_share(int B, int me, int W, int least, SplitSmem &sm, Items items,
-                                            long long *total = nullptr) {
+__device__ __forceinline__ Share take_share(int B, int me, int W, int least, SplitSmem &sm, Items items) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int run = (B + kSplitThreads - 1) / kSplitThreads;
   long long mine = 0;
@@ -90,7 +91,6 @@ __device__ __forceinline__ Share take_share(int B, int me, int W, int least, Spl
   }
   if (threadIdx.x == 0) sm.scan[0] = 0;
   __syncthreads();
-  if (total != nullptr) *total = sm.scan[kSplitThreads];
   return find_share(B, me, W, least, sm, items);
 }
 

@@ -683,4 +683,5 @@ def evict_compact(cache: Cache, batch: BatchTensors, keep: torch.Tensor, new_len
             _addr_or_null(acc_in, "acc_in", torch.float32, (B, H, s_in)), s_in,
             _addr_or_null(acc_out, "acc_out", torch.float32, (B, H, s_out)), s_out)
     _check(_launch(_lib.kv4_evict_compact, args, err, stream, cache.k_codes, batch.page_table,
-                   batch.seq_lens, keep, new_lens, dst_page_table, dst_ring_idx, acc_in, acc_out), "kv4_evict_compact")
+                   batch.seq_lens, keep, new_lens, dst_page_table, dst_ring_idx, acc_in, acc_out),
+           "kv4_evict_compact")
