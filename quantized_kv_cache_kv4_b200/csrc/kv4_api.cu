@@ -508,7 +508,8 @@ kv4_status kv4_evict_select(const kv4_config *cfg, const kv4_batch *batch, const
       budget < cfg->num_sinks + cfg->num_recent)
     return KV4_ERR_INVALID_ARG;
   if (batch->num_seqs == 0) return KV4_OK;
-  if (batch->seq_lens == nullptr || acc == nullptr || keep == nullptr || new_lens == nullptr)
+  if (batch->seq_lens == nullptr || acc == nullptr || keep == nullptr || new_lens == nullptr ||
+      new_lens == batch->seq_lens)
     return KV4_ERR_INVALID_ARG;
   kv4::CacheView v{};
   v.seq_lens = batch->seq_lens;

@@ -323,3 +323,16 @@ def test_checked_objects_are_copied(kv4):
     with pytest.raises(ValueError):
         d.check()
     b.check()
+
+
+def test_select_refuses_the_lengths_as_its_output(kv4):
+    """A unit of the grid would read the lengths that another has already written."""
+    cfg, _, _, _, batch = structs(kv4)
+    r = ctypes.byref
+
+    def call(new, B=2):
+        batch.num_seqs = B
+        return kv4._lib.kv4_evict_select(r(cfg), r(batch), FAKE, 64, 40, FAKE, new, None, None)
+
+    assert call(batch.seq_lens) == -1
+    assert call(batch.seq_lens, B=0) == 0  # nothing to do
