@@ -533,7 +533,8 @@ kv4_status kv4_evict_compact(const kv4_config *cfg, const kv4_int4_pool *pool,
   kv4_status st = make_view(cfg, pool, side, batch, &v);
   if (st != KV4_OK) return st;
   if (budget < 1 || acc_in_stride < 0 || acc_out_stride < 0) return KV4_ERR_INVALID_ARG;
-  if (dst_page_table != nullptr && dst_max_pages < 1) return KV4_ERR_INVALID_ARG;
+  if (dst_page_table != nullptr && (dst_max_pages < 1 || dst_page_table == batch->page_table))
+    return KV4_ERR_INVALID_ARG;
   if ((acc_in == nullptr) != (acc_out == nullptr)) return KV4_ERR_INVALID_ARG;
   // rows moved to other pages are moved in any order, so their totals need other room too;
   // in one array the rows of the totals must not slide over one another either

@@ -336,3 +336,11 @@ def test_select_refuses_the_lengths_as_its_output(kv4):
 
     assert call(batch.seq_lens) == -1
     assert call(batch.seq_lens, B=0) == 0  # nothing to do
+
+
+def test_compact_refuses_the_batchs_own_pages_as_others(kv4):
+    """Rows that go to other pages move in any order: the batch's own table is not another."""
+    cfg, _, pool, side, batch = structs(kv4)
+    r = ctypes.byref
+    assert kv4._lib.kv4_evict_compact(r(cfg), r(pool), r(side), r(batch), FAKE, 40, FAKE + 0x1000, batch.page_table,
+                                      4, None, None, 0, None, 0, None, None) == -1
