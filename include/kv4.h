@@ -422,10 +422,16 @@ size_t kv4_block8_workspace_size(const kv4_config *cfg, int32_t num_seqs, int32_
  * A sequence of a length below 0 or above its page table's (KV4_DEVERR_SEQ_LEN) counts as empty.
  * Where a wait gives up (KV4_DEVERR_TIMEOUT), the run of pages that the waiting worker had still to
  * finish, of one or more sequences, counts as not there.
- * Logits are sums of exact products in fp32. The weights, times the value scales, enter PV as
- * fp16: 11 significant bits of weight x scale down to 2^-28 of the largest weight times the
- * largest scale where max_q_len * Hq / Hkv is at most 64, down to 2^-21 beyond; below that an
- * absolute error of 2^-39 or 2^-32 of it. Results do not depend on the order in which warps run. */
+ * Logits are sums in fp32 of products of codes and query elements, exact down to elements of 2^-31
+ * of their query's largest; with INT8 codes and max_q_len * Hq / Hkv at most 64 the query enters as
+ * 23-bit fixed point, so that an element below 2^-14 of the largest is off by up to 2^-22 of that.
+ * The weights, times the value scales, enter PV as fp16: 11 significant bits of weight x scale down
+ * to 2^-27 of the largest weight times the largest scale where max_q_len * Hq / Hkv is at most 64,
+ * down to 2^-20 beyond; below that an absolute error of 2^-38 or 2^-31 of it. Results do not depend
+ * on the order in which warps run.
+ * max_q_len picks the kernel of the whole call: above 64 rows of a kv head every sequence takes
+ * tiles of 128 rows and 128 positions, whatever its own queries. Decode rows and long chunks are
+ * better sent in a call each. With max_q_len 0 the call does nothing. */
 kv4_status kv4_block8_attention(int32_t format, const kv4_config *cfg, const kv4_paged_pool *pool,
                                 const kv4_batch *batch, const void *q, const int32_t *q_indptr,
                                 int32_t total_q, int32_t max_q_len, void *out, float *out_f32,

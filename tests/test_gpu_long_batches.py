@@ -65,9 +65,10 @@ class Batch8:
             out += [c, scales[ids].double().t().repeat_interleave(16, 1)[:, :L]]
         return out
 
-    def check(self, n, seed, qscale=1.0, q_of=None, lost=None, flag=0):
+    def check(self, n, seed, qscale=1.0, q_of=None, lost=None, flag=0, query_step=0.0):
         """Attention of the last n[b] positions of each sequence, every row. lost: {sequence: bool
-        [H, n G, L]}, positions that its rows are without; flag: the error bits of the call."""
+        [H, n G, L]}, positions that its rows are without; flag: the error bits of the call;
+        query_step: what an element of a query may be off by, of its largest."""
         kv4 = _kv4()
         Hq, total, most = self.H * self.G, sum(n), max(n)
         g = torch.Generator(device="cuda").manual_seed(seed)
@@ -88,10 +89,10 @@ class Batch8:
         for b, m in enumerate(n):
             if m:
                 self.compare(b, q[at:at + m], out[at:at + m], o32[at:at + m], lse[at:at + m], most * self.G <= 64,
-                             None if lost is None else lost.get(b))
+                             None if lost is None else lost.get(b), query_step)
             at += m
 
-    def compare(self, b, q, out, o32, lse, few, lost=None):
+    def compare(self, b, q, out, o32, lse, few, lost=None, query_step=0.0):
         L, n, H, G = self.lens[b], q.shape[0], self.H, self.G
         kc, ks, vc, vs = self.held(b)
         k, v = kc * ks[..., None], vc * vs[..., None]
@@ -110,6 +111,7 @@ class Batch8:
         # logits: fp32 sums of 128 products (130 roundings of 2^-24 of the sum of magnitudes), the
         # scales' products and 2^x another 2^-22 of the logit
         ds = (130 * 2.0 ** -24 + 2.0 ** -21) * mag + 2.0 ** -21
+        ds += query_step * q.abs().amax(-1) * k.abs().sum(-1).amax(1)[:, None] / math.sqrt(128)
         # weights off by e^ds and rounded to fp16 (2^-11), L products and sums in fp32, two roundings
         # of 2^-24 and a factor 2^x off by 2^-22 for each step of at least 32 positions that moves the
         # maximum or the value scales' exponent
@@ -205,6 +207,26 @@ def test_drifting_logits_and_value_scales(fmt, logit, value, few):
         n = [600, 437]
         assert key_tiles(lens, n, H, G) >= 4 * SMS
         m.check(n, 13, q_of=q_of)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [1, 9, 40], ids=["8-rows", "16-rows", "tiles"])
+@pytest.mark.parametrize("large", [2.0 ** 8, 2.0 ** 16, 2.0 ** 24])
+def test_queries_with_one_large_element(fmt, n, large):
+    """An element that meets zero keys and is far larger than the others that make the logits: they
+    lose bits with INT8 codes and few rows only, where the query is 23-bit fixed point (from 2^-14 of
+    the largest down)."""
+    lens, H, G = [500, 333], 4, 4
+    k, v = rows(sum(lens), H, 22)
+    k[..., 5] = 0.0
+    m = Batch8(fmt, lens, H, G, bf(k), bf(v))
+
+    def q_of(q):
+        q = q.clone()
+        q[..., 5] = 4 * large
+        return torch.where(q.abs() < 2.0 ** -4, 2.0 ** -4, q)  # (fp16 holds down to 2^-31 of the largest)
+
+    m.check([n, n], 23, q_of=q_of, query_step=2.0 ** -22 if fmt == "int8" and n * G <= 64 and large > 2 ** 8 else 0.0)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
