@@ -119,7 +119,7 @@ __device__ __forceinline__ float amax4(const float (&x)[4]) {
 
 // One warp per (sequence, kv head, K or V); lane l holds dims 4l .. 4l+3. Bound by its chain of
 // loads (length, page id, scale), so the row is asked for first: 1024 sequences x 8 kv heads take
-// 10 us of which the bytes are 1.
+// 4.8 us in graph replays (10.4 a call through the binding), of which the bytes are 1.
 template <int F>
 __global__ void __launch_bounds__(256) block8_append_token_kernel(
     CacheView c, const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
@@ -174,10 +174,10 @@ __device__ __forceinline__ uint4 transpose4(uint32_t a, uint32_t b, uint32_t c, 
 // (up to 16 x 256 bytes) in registers, the block's largest magnitude, the codes, and full 64-byte
 // runs of each strip out. Bound by HBM (512 bytes of rows in, 256 of codes out per position and
 // head) and the latency of a page's loads; the search for a row's sequence is shared by the CTA's
-// ~4 pages and all heads. Prefill of 64 sequences of up to 1024 (47k rows x 8 kv heads): 64 rows
-// per CTA, three CTAs per SM, 67 us (4.3 TB/s); 16 rows per CTA 80 us. Fewer rows than that fills
-// the GPU with are dealt to more CTAs: 1024 sequences of 1 to 3 rows 87 -> 22 us, 64 of 2 to 9 rows 39 ->
-// 7.5, one of 300 rows 18 -> 7.
+// ~4 pages and all heads. Prefill of 64 sequences of up to 1500 rows (47k rows x 8 kv heads), graph
+// replays: 64 rows per CTA, three CTAs per SM, 63 us in e4m3 (4.6 TB/s), 73 in INT8 (whose codes take
+// more instructions); 16 rows per CTA 80 us. Fewer rows than that fills the GPU with are dealt to more
+// CTAs: 1024 sequences of 1 to 3 rows 87 -> 22 us, 64 of 2 to 9 rows 39 -> 7.5, one of 300 rows 18 -> 7.
 constexpr int kRowsPerCta = 64;  // at most
 constexpr int kAppendCtas = 148 * 3;
 template <int F>
@@ -311,8 +311,9 @@ constexpr int kStage8Bytes = kPair * kPage8Bytes;
 constexpr int kWarp8Smem = kStages8 * kStage8Bytes;
 constexpr int kCta8Smem = kWarps * kWarp8Smem;
 // The weights p = 2^(s - m) enter PV in fp16 as p * 2^14 * vs / 2^vref, vref the exponent of
-// the largest value scale so far (at most 2^14; 11 significant bits down to 2^-14). The
-// running maximum is kept as m - 14, which makes (m - 14, l 2^14, acc 2^14) the same state.
+// the largest value scale so far (at most 2^14; 11 significant bits down to 2^-14): the tensor
+// cores take 16-bit operands, and a weight's 2^-11 is an eighth of what the bf16 output rounds by.
+// The running maximum is kept as m - 14, which makes (m - 14, l 2^14, acc 2^14) the same state.
 constexpr float kLift8 = 14.0f;
 
 // One warp's share of a batch. NT groups of 8 query rows share each page's operands.
@@ -323,9 +324,9 @@ constexpr float kLift8 = 14.0f;
 //   PV    fp16 MMAs on the converted codes, fp32 accumulators.
 // Two pages (32 positions) per softmax step, so that the cross-lane maximum, the waits and the
 // copies' bookkeeping are paid once for 8 KB. NT = 1 (up to 8 rows of a kv head: decode steps) is
-// bound by the reading of the pages: 128 sequences of up to 16384, 5.9 TB/s. NT = 2 by the issue of
-// MMAs, exponentials and conversions: 32 x 4096 positions 57 us with 8 rows, 76 with 16 (one unit),
-// 126 with 32 (two units).
+// bound by the reading of the pages: 128 sequences of up to 16384, 382 us (e4m3, 6.0 TB/s) and 390
+// (INT8). NT = 2 by the issue of MMAs, exponentials and conversions: 32 x 4096 positions 59 us with 8
+// rows, 71 with 16 (one unit), 119 with 32 (two units) in INT8, 1 to 3 % less in e4m3 (graph replays).
 //
 // UNIT: few units, each given to the warps of a cluster (`parts` of them, equal runs of its pages),
 // which join their records themselves behind a cluster barrier: no scan of the batch and no merge

@@ -196,8 +196,10 @@ cudaError_t launch_tile_attention(int fmt, const CacheView &c, const Queries &qs
 
 // Up to this many query rows (positions x query heads of a kv head) of a sequence the warp
 // kernel takes the call, beyond it the tile kernel, whose time hardly depends on the rows up to
-// 256. 32 x 4096 positions, warp kernel: 16 rows 76 us, 32 rows 126, 64 rows 226; tile kernel: 124
-// to 256 rows 207 to 210. 4 x 8000: 64 rows 69, tile kernel 77 to 89.
+// 128. Warp kernel / tile kernel, INT8, graph replays, us: 32 x 4096 positions 32 rows 117 / 168, 48
+// rows 162 / 168, 64 rows 212 / 171; 4 x 8000 32 rows 36 / 52, 48 rows 53 / 52, 64 rows 64 / 53; 128 x
+// 1000 48 rows 179 / 203, 64 rows 231 / 207. By time the border is at 48 rows; it is at 64 because
+// the warp kernel keeps the weights to 2^-38 of the largest, the tile kernel to 2^-31.
 constexpr int kWarpRows = 64;
 
 }  // namespace kv4

@@ -64,10 +64,11 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a01, uint32
 // only rounding of a logit is the fp32 accumulation. INT4 codes enter as fp16 subnormals (c * 2^-24,
 // or 16 c * 2^-24 for the odd dims, whose query elements carry the factor 1/16); a group's scale and
 // minimum multiply its product and its query sum, s = kk sum_g (scale_g (q c)_g + min_g sum(q)_g / kk).
-// 64 x 2048 positions, 32 query and 8 kv heads: 31 us with two heads per warp, 42 with one; 48 long
-// tails 80 and 114 us (4.0 TB/s); 4 x 500 positions 8.9 and 7.7. Bound by the chain of a tile (codes to
-// MMAs to exponentials to the sum, 146 to 165 registers a thread allow three warps per scheduler)
-// next to the reading of K; two to six CTAs per SM with fewer stages are no faster.
+// 64 x 2048 positions, 32 query and 8 kv heads, graph replays: 33 us with two heads per warp, 42 with
+// one; 48 long tails 85 (3.7 TB/s) and 114 us; 4 x 500 positions 8.9 and 7.7. 64 query heads (one head
+// per warp): 44 and 122. Bound by the chain of a tile (codes to MMAs to exponentials to the sum, 146 to
+// 165 registers a thread allow three warps per scheduler) next to the reading of K; two to six CTAs per
+// SM with fewer stages are no faster.
 // HOOK: a call with the testing hook armed; without, the constant wait limit folds into the code (as
 // an argument it costs 2 to 4 %).
 template <int HPW, bool HOOK>
@@ -785,7 +786,8 @@ __global__ void __launch_bounds__(256) compact_kernel(CacheView c, Moves mv, int
 // Row j comes from a position >= j, so what a round writes was read in it or before it: one
 // barrier between a round's loads and its stores is all the order there is to keep. The second half
 // of the grid, where there is a recent window, moves the rings
-// (one sequence of 777 rows to 500 in 5 us, 64 of 2048 to 1024 in 41; a launch of its own: 9 and 44).
+// (graph replays: one sequence of 777 rows to 500 in 5 us, 64 of 2048 to 1024 in 43; with a launch of
+// its own 4 and 3 us more).
 constexpr int kInPlaceThreads = 512;
 __global__ void __launch_bounds__(kInPlaceThreads) compact_in_place_kernel(CacheView c, Moves mv,
                                                                           int32_t *err) {
@@ -879,9 +881,9 @@ cudaError_t launch_select(const CacheView &c, int max_seq_len, const float *acc,
                           int32_t *keep, int32_t *new_lens, int32_t *err, cudaStream_t s) {
   const int units = c.num_seqs * c.num_kv_heads;
   const int longest = max_seq_len < acc_stride ? max_seq_len : acc_stride;
-  // the fewest keys per thread that hold the longest row (64 x 8 rows of 2048: 10 us with 4 keys, 25
-  // with 32; of 8192: 18 with 16, 26 with 32, 83 with the row read again; 128 x 8 of up to 16384: 44
-  // with 32, 240 with the row read again)
+  // the fewest keys per thread that hold the longest row (graph replays, 64 x 8 rows of 2048: 10 us
+  // with 4 keys, 25 with 32; of 4096: 17 with 16; of 8192: 18 with 16, 26 with 32, 83 with the row read
+  // again; 128 x 8 of up to 16384: 45 with 32, 240 with the row read again)
   if (longest <= 4 * kSelThreads)
     select_kernel<4><<<units, kSelThreads, 0, s>>>(c, longest, acc, acc_stride, budget, keep, new_lens, err);
   else if (longest <= 16 * kSelThreads)
