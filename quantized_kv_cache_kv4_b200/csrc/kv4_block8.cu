@@ -319,8 +319,9 @@ constexpr float kLift8 = 14.0f;
 // One warp's share of a batch. NT groups of 8 query rows share each page's operands.
 //   QK^T  INT8: integer MMAs on the codes as they are; the query as 23-bit fixed point (its
 //         largest element at least 2^21 and below 2^22 steps) in three limbs: an element below
-//         2^-14 of the largest is off by up to 2^-22 of it, the products' sums are exact. e4m3: fp16 MMAs, codes converted, the query a power of two
-//         from its bf16 value; both exact but for the fp32 sums.
+//         2^-14 of the largest is off by up to 2^-22 of it, the products' sums are exact. e4m3: fp16
+//         MMAs, codes converted, the query a power of two from its bf16 value; both exact but for
+//         the fp32 sums.
 //   PV    fp16 MMAs on the converted codes, fp32 accumulators.
 // Two pages (32 positions) per softmax step, so that the cross-lane maximum, the waits and the
 // copies' bookkeeping are paid once for 8 KB. NT = 1 (up to 8 rows of a kv head: decode steps) is

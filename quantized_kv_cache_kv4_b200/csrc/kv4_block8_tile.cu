@@ -28,13 +28,13 @@
 // a worker) for the merge.
 //
 // What bounds it. 2 chunks of 3900-4096 positions over 7000-8192 (743 GFLOP): 875 us a call among
-// others in INT8 (850 TFLOP/s), 3 % less in e4m3. Of the ~5000 cycles of a key tile the products take 2050 (both pipelines'), a
-// pipeline's softmax 2900 (of which the exponentials 1100-2100, as the other's fall together with
-// them), and a pipeline's softmax waits for its own products. One MMA warp that takes the
-// pipelines in turn keeps them out of phase (two warps, one per pipeline: 999 us). The roles'
-// instructions contend: the loops are short in code where they can be (the convert loop unrolled
-// by 8 instead of 1 costs a fifth of the kernel, exponentials by polynomial on the FMA pipe 6 to
-// 20 %, half rows per thread with 16 softmax warps 2 %).
+// others in INT8 (850 TFLOP/s), 2 to 3 % less in e4m3. Of the ~5000 cycles of a key tile the products
+// take 2050 (both pipelines'), a pipeline's softmax 2900 (of which the exponentials 1100-2100, as the
+// other's fall together with them), and a pipeline's softmax waits for its own products. One MMA warp
+// that takes the pipelines in turn keeps them out of phase (two warps, one per pipeline: 999 us). The
+// roles' instructions contend: the loops are short in code where they can be (the convert loop
+// unrolled by 8 instead of 1 costs a fifth of the kernel, exponentials by polynomial on the FMA pipe 6
+// to 20 %, half rows per thread with 16 softmax warps 2 %).
 #include <algorithm>
 
 #include "kv4_block8.cuh"
